@@ -10,6 +10,9 @@ prepare_chunk_indices, prepare_chunk_offsets).
 Shapes: q, k ``[B, T, Hq, K]``; v ``[B, T, Hv, V]``; g, beta ``[B, T, Hv]``;
 states ``[N, Hv, K, V]`` (``[N, Hv, V, K]`` with ``state_v_first``), fp32.
 K = V = 128; bf16 or fp16 inputs; Hv a multiple of Hq.
+
+The operators around the recurrence in a layer (``_layer_ops``): the short
+causal convolution and the RMS norm with the residual's addition.
 """
 from __future__ import annotations
 
@@ -18,6 +21,9 @@ from typing import Optional
 
 import torch
 
+from ._layer_ops import (causal_conv1d, causal_conv1d_bwd, causal_conv1d_fwd,
+                         causal_conv1d_update, rms_norm, rms_norm_bwd, rms_norm_fwd,
+                         rms_norm_quant)
 from ._lib import (GDR_BF16, GDR_FP16, GDR_FP32, GdrError, Problem, check, lib)
 
 __all__ = [
@@ -25,6 +31,8 @@ __all__ = [
     "chunk_gated_delta_rule_bwd",
     "fused_recurrent_gated_delta_rule", "prepare_lens", "prepare_chunk_indices",
     "prepare_chunk_offsets", "unpack_states", "GdrError",
+    "causal_conv1d", "causal_conv1d_fwd", "causal_conv1d_bwd", "causal_conv1d_update",
+    "rms_norm", "rms_norm_fwd", "rms_norm_bwd", "rms_norm_quant",
 ]
 
 CHUNK = 64

@@ -1,0 +1,375 @@
+"""The operators around the recurrence in a layer: the short causal
+convolution and the RMS norm with the residual's addition.
+
+Thin bindings over libgdr.so, re-exported by the package: PyTorch provides
+device memory, the current stream and autograd; every computation runs in the
+library's HIP kernels.  Errors are :class:`GdrError`, as everywhere in the
+package.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from ._lib import (GDR_BF16, GDR_FP16, GDR_FP32, ConvProblem, GdrError, NormProblem, check, lib)
+
+_DT = {torch.bfloat16: GDR_BF16, torch.float16: GDR_FP16, torch.float32: GDR_FP32}
+_NULL_GUARD = contextlib.nullcontext()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _code(t, name):
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise GdrError(4, "%s has the unsupported dtype %s" % (name, t.dtype)) from None
+
+
+def _guard(t):
+    """Makes t's device the current one around a launch."""
+    if t.device.index == torch.cuda.current_device():
+        return _NULL_GUARD
+    return torch.cuda.device(t.device)
+
+
+def _stream(t):
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _need_gpu(name, t):
+    if not t.is_cuda:
+        raise GdrError(8, "%s is on %s; the kernels run on an MI355X" % (name, t.device))
+
+
+def _expect(name, t, shape, dtypes, device):
+    """t must have this shape, one of these dtypes and this device."""
+    if tuple(t.shape) != tuple(shape):
+        raise GdrError(2, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype not in dtypes:
+        raise GdrError(4, "%s must be %s, got %s"
+                       % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.device != device:
+        raise GdrError(8, "%s is on %s but x is on %s" % (name, t.device, device))
+
+
+def _like(name, t, shape, dtypes, device):
+    """:func:`_expect` (None passes), and t contiguous."""
+    if t is None:
+        return None
+    _expect(name, t, shape, dtypes, device)
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _token_rows(x, inner):
+    """(x, stride): x [B, T, ...] as rows one token stride apart, the last
+    `inner` dimensions contiguous; copied only when it is not laid out so."""
+    B, T = x.shape[0], x.shape[1]
+    width = 1
+    ok = True
+    for d in range(1, inner + 1):
+        if x.shape[-d] != 1 and x.stride(-d) != width:
+            ok = False
+        width *= x.shape[-d]
+    if ok:
+        s = x.stride(1) if T > 1 else (x.stride(0) if B > 1 else width)
+        if s >= width and (B == 1 or T == 1 or x.stride(0) == T * s):
+            return x, s
+    return x.contiguous(), width
+
+
+def _seqs(x, cu_seqlens, cu_seqlens_cpu):
+    """(N, device offsets, host offsets) of packed sequences, or (B, None, None)."""
+    if cu_seqlens is None:
+        if cu_seqlens_cpu is not None:
+            raise GdrError(6, "cu_seqlens_cpu is given without cu_seqlens")
+        return x.shape[0], None, None
+    dev = cu_seqlens.to(device=x.device, dtype=torch.int32).contiguous()
+    if cu_seqlens_cpu is None:
+        # one blocking device-to-host copy (pass cu_seqlens_cpu to avoid it)
+        cu_seqlens_cpu = cu_seqlens.detach().to("cpu")
+    host = cu_seqlens_cpu.to(device="cpu", dtype=torch.int32).contiguous()
+    if host.dim() != 1 or host.numel() < 2 or dev.shape != host.shape:
+        raise GdrError(6, "cu_seqlens needs one offset per sequence and the end, got shape %s"
+                       % (tuple(host.shape),))
+    return host.numel() - 1, dev, host
+
+
+def _bytes(n, device):
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+# ---- short causal convolution -------------------------------------------------
+
+def _activation(name):
+    if name in (None, "none"):
+        return 0
+    if name in ("silu", "swish"):
+        return 1
+    raise GdrError(10, "activation must be None or 'silu', got %r" % (name,))
+
+
+class _Conv:
+    """The checked arguments of one convolution call."""
+
+    def __init__(self, x, weight, bias, activation, state, cu_seqlens, cu_seqlens_cpu):
+        if x.dim() != 3 or weight.dim() != 2:
+            raise GdrError(2, "x must be [B, T, D] and weight [D, W], got %s and %s"
+                           % (tuple(x.shape), tuple(weight.shape)))
+        _need_gpu("x", x)
+        B, T, D = x.shape
+        W = weight.shape[1]
+        dev = x.device
+        dt = _code(x, "x")
+        self.weight = _like("weight", weight, (D, W), (x.dtype, torch.float32), dev)
+        self.bias = _like("bias", bias, (D,), (weight.dtype,), dev)
+        N, self.cu, self.cu_host = _seqs(x, cu_seqlens, cu_seqlens_cpu)
+        self.state_shape = (N, W - 1, D)
+        self.state = _like("initial_state", state, self.state_shape, (x.dtype,), dev)
+        self.x, stride = _token_rows(x, 1)
+        self.p = ConvProblem(B=B, T=T, D=D, W=W, N=N, cu_seqlens_dev=_ptr(self.cu),
+                             cu_seqlens_host=_ptr(self.cu_host), dtype=dt,
+                             w_dtype=_code(weight, "weight"), activation=_activation(activation),
+                             x_stride=stride)
+        self.ref = ctypes.byref(self.p)
+        check(lib.gdr_conv1d_check(self.ref, None, 0))
+
+
+def causal_conv1d_fwd(x, weight, bias=None, activation="silu", initial_state=None,
+                      output_final_state=True, cu_seqlens=None, cu_seqlens_cpu=None):
+    """:func:`causal_conv1d` without autograd: ``(y, final_state)``."""
+    c = _Conv(x, weight, bias, activation, initial_state, cu_seqlens, cu_seqlens_cpu)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    last = None
+    if output_final_state:
+        last = torch.empty(c.state_shape, dtype=x.dtype, device=x.device)
+    with _guard(x):
+        check(lib.gdr_conv1d_fwd(c.ref, _ptr(c.x), _ptr(c.weight), _ptr(c.bias), _ptr(c.state),
+                                 _ptr(y), _ptr(last), _stream(x)))
+    return y, last
+
+
+def causal_conv1d_bwd(x, weight, bias, dy, dfinal_state=None, activation="silu",
+                      initial_state=None, cu_seqlens=None, cu_seqlens_cpu=None):
+    """The gradient of :func:`causal_conv1d`: ``(dx, dweight, dbias,
+    dinitial_state)``, the last two ``None`` without a bias or an initial
+    state.  ``dfinal_state`` (optional) is the gradient of the final state."""
+    c = _Conv(x, weight, bias, activation, initial_state, cu_seqlens, cu_seqlens_cpu)
+    dev = x.device
+    dy = _like("dy", dy, x.shape, (x.dtype,), dev)
+    dfinal_state = _like("dfinal_state", dfinal_state, c.state_shape, (x.dtype,), dev)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dw = torch.empty_like(c.weight)
+    db = None if bias is None else torch.empty_like(c.bias)
+    ds = None if c.state is None else torch.empty_like(c.state)
+    n = lib.gdr_conv1d_bwd_workspace_size(c.ref)
+    ws = _bytes(n, dev)
+    with _guard(x):
+        check(lib.gdr_conv1d_bwd(c.ref, _ptr(c.x), _ptr(c.weight), _ptr(c.bias), _ptr(dy),
+                                 _ptr(dfinal_state), _ptr(c.state), _ptr(dx), _ptr(dw), _ptr(db),
+                                 _ptr(ds), _ptr(ws), n, _stream(x)))
+    return dx, dw, db, ds
+
+
+class _CausalConv1d(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, activation, initial_state, output_final_state, cu_seqlens,
+                cu_seqlens_cpu):
+        ctx.set_materialize_grads(False)
+        if cu_seqlens is not None and cu_seqlens_cpu is None:
+            cu_seqlens_cpu = cu_seqlens.detach().to("cpu")
+        y, last = causal_conv1d_fwd(x, weight, bias, activation, initial_state,
+                                    output_final_state, cu_seqlens, cu_seqlens_cpu)
+        ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens, cu_seqlens_cpu)
+        ctx.activation = activation
+        return y, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dlast):
+        x, weight, bias, state, cu, cu_cpu = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        dx, dw, db, ds = causal_conv1d_bwd(x, weight, bias, dy, dlast, ctx.activation, state, cu,
+                                           cu_cpu)
+        return dx, dw, db, None, ds, None, None, None
+
+
+def causal_conv1d(x, weight, bias=None, activation="silu", initial_state=None,
+                  output_final_state=False, cu_seqlens=None, cu_seqlens_cpu=None):
+    """Short causal depthwise convolution with autograd: ``(y, final_state)``.
+
+    ``y[t] = act(bias + sum_j weight[:, j] * x[t - (W-1) + j])`` per channel,
+    ``W`` = 2, 3 or 4, ``activation`` ``"silu"`` or ``None``.  x ``[B, T, D]``
+    (bf16, fp16 or fp32; a slice of a wider projection is read in place);
+    weight ``[D, W]`` and bias ``[D]`` in x's dtype or fp32.  States ``[N, W-1,
+    D]`` in x's dtype hold the last ``W-1`` inputs, oldest first; without
+    ``initial_state`` what precedes a sequence is zero.  ``cu_seqlens``: packed
+    sequences (``B == 1``), ``N = len(cu_seqlens) - 1``; sequences may be empty.
+    Gradients flow to x, weight, bias and initial_state."""
+    return _CausalConv1d.apply(x, weight, bias, activation, initial_state,
+                               bool(output_final_state), cu_seqlens, cu_seqlens_cpu)
+
+
+def causal_conv1d_update(x, conv_state, weight, bias=None, activation="silu"):
+    """One or a few tokens per sequence on a cached state (decode): returns y,
+    shaped like x (``[B, D]`` or ``[B, T, D]``), and updates ``conv_state``
+    ``[B, W-1, D]`` in place.  No autograd."""
+    squeeze = x.dim() == 2
+    x3 = x.unsqueeze(1) if squeeze else x
+    if not conv_state.is_contiguous():
+        raise GdrError(10, "conv_state is updated in place and must be contiguous")
+    c = _Conv(x3, weight, bias, activation, conv_state, None, None)
+    y = torch.empty(x3.shape, dtype=x.dtype, device=x.device)
+    with _guard(x):
+        check(lib.gdr_conv1d_update(c.ref, _ptr(c.x), _ptr(conv_state), _ptr(c.weight),
+                                    _ptr(c.bias), _ptr(y), _stream(x)))
+    return y.squeeze(1) if squeeze else y
+
+
+# ---- RMS norm with the residual's addition ----------------------------------------
+
+_FORMATS = {None: 0, "fp8": 1, "int8": 2}
+
+
+class _Norm:
+    """The checked arguments of one norm call on rows of D columns."""
+
+    def __init__(self, x, weight, eps, res_dtype, fmt=None, group_size=0):
+        if x.dim() < 1 or weight.dim() != 1:
+            raise GdrError(2, "x must be [..., D] and weight [D], got %s and %s"
+                           % (tuple(x.shape), tuple(weight.shape)))
+        _need_gpu("x", x)
+        D = x.shape[-1]
+        dt = _code(x, "x")
+        if fmt not in _FORMATS:
+            raise GdrError(10, "format must be 'fp8' or 'int8', got %r" % (fmt,))
+        self.weight = _like("weight", weight, (D,), (x.dtype, torch.float32), x.device)
+        rows = x.numel() // D if D else 0
+        # rows one stride apart (a slice of a wider tensor), else a copy
+        stride = D
+        if x.dim() == 1 or x.is_contiguous():
+            x = x if x.is_contiguous() else x.contiguous()
+        else:
+            flat = x.unsqueeze(0) if x.dim() == 2 else x.flatten(0, -3) if x.dim() > 3 else x
+            x, stride = _token_rows(flat, 1)
+        self.x = x
+        self.p = NormProblem(rows=rows, D=D, dtype=dt,
+                             res_dtype=dt if res_dtype is None else _DT.get(res_dtype, -1),
+                             w_dtype=_code(weight, "weight"),
+                             has_residual=0 if res_dtype is None else 1, quant=_FORMATS[fmt],
+                             group_size=int(group_size), eps=float(eps), x_stride=stride)
+        self.ref = ctypes.byref(self.p)
+        check(lib.gdr_rms_norm_check(self.ref, None, 0))
+
+
+def _norm_fwd(x, weight, eps, residual, fmt, group_size, need_rstd):
+    c = _Norm(x, weight, eps, None if residual is None else residual.dtype, fmt, group_size)
+    dev = x.device
+    residual = _like("residual", residual, x.shape, (x.dtype, torch.float32), dev)
+    D = x.shape[-1]
+    h = None if residual is None else torch.empty(x.shape, dtype=residual.dtype, device=dev)
+    out = {None: x.dtype, "fp8": torch.float8_e4m3fn, "int8": torch.int8}[fmt]
+    y = torch.empty(x.shape, dtype=out, device=dev)
+    scale = None
+    if fmt is not None:
+        groups = 1 if group_size == 0 else -(-D // group_size)
+        scale = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=dev)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_rstd else None
+    with _guard(x):
+        check(lib.gdr_rms_norm_fwd(c.ref, _ptr(c.x), _ptr(residual), _ptr(c.weight), _ptr(y),
+                                   _ptr(scale), _ptr(h), _ptr(rstd), _stream(x)))
+    return y, scale, h, rstd
+
+
+def rms_norm_fwd(x, weight, eps=1e-6, residual=None):
+    """:func:`rms_norm` without autograd: ``(y, h, rstd)``, ``h`` ``None``
+    without a residual, ``rstd`` (fp32, one per row) for :func:`rms_norm_bwd`."""
+    y, _, h, rstd = _norm_fwd(x, weight, eps, residual, None, 0, True)
+    return y, h, rstd
+
+
+def rms_norm_bwd(dy, h, weight, rstd, dh=None, has_residual=False):
+    """The gradient of :func:`rms_norm`: ``(dx, dresidual, dweight)``.  ``h`` is
+    what the forward normalised (its ``h`` with a residual, else x), ``dh``
+    (optional, with a residual) the gradient of the ``h`` it returned.
+    ``dresidual`` is ``None`` without a residual; of one dtype, x and the
+    residual have the same gradient and get the same tensor."""
+    if dh is not None and not has_residual:
+        raise GdrError(10, "dh is the gradient of h, which only a residual brings")
+    _need_gpu("h", h)
+    if has_residual:
+        c = _Norm(dy, weight, 0.0, h.dtype)
+        stream, stride = h.contiguous(), h.shape[-1]
+    else:
+        c = _Norm(h, weight, 0.0, None)
+        stream, stride = c.x, c.p.x_stride
+    dev = dy.device
+    c.p.x_stride = stride
+    _expect("h", h, dy.shape, (dy.dtype, torch.float32) if has_residual else (dy.dtype,), dev)
+    dy = dy.contiguous()
+    rstd = _like("rstd", rstd, dy.shape[:-1], (torch.float32,), dev)
+    dh = _like("dh", dh, dy.shape, (h.dtype,), dev)
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    dres = None
+    if has_residual and h.dtype != dy.dtype:
+        dres = torch.empty(dy.shape, dtype=h.dtype, device=dev)
+    dw = torch.empty_like(c.weight)
+    n = lib.gdr_rms_norm_bwd_workspace_size(c.ref)
+    ws = _bytes(n, dev)
+    with _guard(dy):
+        check(lib.gdr_rms_norm_bwd(c.ref, _ptr(dy), _ptr(stream), _ptr(c.weight), _ptr(rstd),
+                                   _ptr(dh), _ptr(dx), _ptr(dres), _ptr(dw), _ptr(ws), n,
+                                   _stream(dy)))
+    if not has_residual:
+        return dx, None, dw
+    return dx, dx if dres is None else dres, dw
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, eps, residual):
+        ctx.set_materialize_grads(False)
+        y, h, rstd = rms_norm_fwd(x, weight, eps, residual)
+        ctx.save_for_backward(x if h is None else h, weight, rstd)
+        ctx.has_residual, ctx.dtype = h is not None, x.dtype
+        return (y, h) if h is not None else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros(h.shape, dtype=ctx.dtype, device=h.device)
+        dx, dres, dw = rms_norm_bwd(dy, h, weight, rstd, dh, ctx.has_residual)
+        return dx, dw, None, dres
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None):
+    """Root-mean-square norm over the last dimension, with autograd:
+    ``weight * h / sqrt(mean(h^2) + eps)`` with ``h = x + residual``.
+
+    Returns y in x's dtype, or ``(y, h)`` with a residual: ``h``, rounded to the
+    residual's dtype (x's or fp32), is the stream that the next layer adds to,
+    and it is this rounded stream that is normalised.  weight ``[D]`` in x's
+    dtype or fp32; D up to 65536.  Gradients flow to x, weight and residual,
+    also from ``h``."""
+    return _RmsNorm.apply(x, weight, eps, residual)
+
+
+def rms_norm_quant(x, weight, eps=1e-6, residual=None, format="fp8", group_size=0):
+    """:func:`rms_norm` with its output in 8 bits, for a projection in 8 bits:
+    ``(q, scale, h)``.  ``format`` ``"fp8"`` (e4m3, largest 448) or ``"int8"``;
+    fp32 scales of shape ``x.shape[:-1] + (groups,)``, one per row (``group_size=0``,
+    one group) or one per 128 columns (``group_size=128``, ``ceil(D / 128)``):
+    ``scale = max(max|y| / top, 2**-126)`` and ``q = y / scale`` rounded to
+    nearest even.  ``h`` is ``None`` without a residual.  No autograd."""
+    if format is None:
+        raise GdrError(10, "format must be 'fp8' or 'int8', got None")
+    q, scale, h, _ = _norm_fwd(x, weight, eps, residual, format, group_size, False)
+    return q, scale, h

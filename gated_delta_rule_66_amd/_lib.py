@@ -39,6 +39,28 @@ class Problem(ctypes.Structure):
     ]
 
 
+class ConvProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("W", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("cu_seqlens_dev", ctypes.c_void_p),
+        ("cu_seqlens_host", ctypes.c_void_p),
+        ("dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+        ("activation", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+        ("has_residual", ctypes.c_int32), ("quant", ctypes.c_int32),
+        ("group_size", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+
 # every symbol include/gdr.h declares
 EXPORTS = [
     "gdr_status_string", "gdr_last_error", "gdr_check_supported", "gdr_check_device",
@@ -50,6 +72,9 @@ EXPORTS = [
     "gdr_plan_info", "gdr_recurrent_fwd", "gdr_chunk_bwd_gate", "gdr_chunk_fwd_noalloc",
     "gdr_chunk_bwd_states", "gdr_chunk_bwd_states_workspace_size", "gdr_chunk_fwd_states",
     "gdr_chunk_trans_size", "gdr_bwd_pipeline_info",
+    "gdr_conv1d_check", "gdr_conv1d_fwd", "gdr_conv1d_bwd_workspace_size", "gdr_conv1d_bwd",
+    "gdr_conv1d_update", "gdr_rms_norm_check", "gdr_rms_norm_fwd",
+    "gdr_rms_norm_bwd_workspace_size", "gdr_rms_norm_bwd",
 ]
 
 
@@ -121,6 +146,26 @@ def _declare_profile(lib):
     lib.gdr_plan_info.restype = ctypes.c_int
 
 
+def _declare_ops(lib):
+    P, S, st = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+
+    def fn(name, args, res=st):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
+
+    CP = ctypes.POINTER(ConvProblem)
+    fn("gdr_conv1d_check", [CP, ctypes.c_char_p, S])
+    fn("gdr_conv1d_fwd", [CP] + [P] * 7)
+    fn("gdr_conv1d_bwd_workspace_size", [CP], S)
+    fn("gdr_conv1d_bwd", [CP] + [P] * 11 + [S, P])
+    fn("gdr_conv1d_update", [CP] + [P] * 6)
+    NP = ctypes.POINTER(NormProblem)
+    fn("gdr_rms_norm_check", [NP, ctypes.c_char_p, S])
+    fn("gdr_rms_norm_fwd", [NP] + [P] * 8)
+    fn("gdr_rms_norm_bwd_workspace_size", [NP], S)
+    fn("gdr_rms_norm_bwd", [NP] + [P] * 9 + [S, P])
+
+
 def load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -129,6 +174,7 @@ def load():
     lib = ctypes.CDLL(LIB_PATH)
     _declare(lib)
     _declare_profile(lib)
+    _declare_ops(lib)
     return lib
 
 

@@ -1,0 +1,58 @@
+// ops_device.h -- device-side building blocks of the layer operators.
+#pragma once
+
+#include "../csrc/gdr_device.h"
+
+namespace gdr {
+
+// Eight (16-bit) or four (fp32) consecutive elements, 16 bytes.  Rows of odd
+// width start at any element, so the access promises only the element's own
+// alignment: global memory takes 16-byte loads and stores at any address (the
+// compiler emits one global_load_dwordx4 either way).
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+  struct __attribute__((packed, aligned(sizeof(T)))) Raw {
+    uint32_t u[4];
+  };
+  T v[n];
+
+  __device__ __forceinline__ void load(const T* p) {
+    const Raw r = *reinterpret_cast<const Raw*>(p);
+    *this = __builtin_bit_cast(Vec, r);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    *reinterpret_cast<Raw*>(p) = __builtin_bit_cast(Raw, *this);
+  }
+  // the first m elements (the row's end); the others are zero
+  __device__ __forceinline__ void load_part(const T* p, int m) {
+    if (m >= n) {
+      load(p);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < n; ++e) v[e] = e < m ? p[e] : (T)0.f;
+  }
+  __device__ __forceinline__ void store_part(T* p, int m) const {
+    if (m >= n) {
+      store(p);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < n; ++e)
+      if (e < m) p[e] = v[e];
+  }
+};
+
+// n consecutive values of a parameter held in 16 bits or fp32
+__device__ __forceinline__ float load_param(const void* p, int64_t i, int dtype) {
+  return load_scalar(p, i, dtype);
+}
+
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + __expf(-z)); }
+
+// Sum and maximum over a whole wave (every lane ends with the same bits).
+__device__ __forceinline__ float wave_sum(float v) { return sum4g(sum16(v)); }
+
+}  // namespace gdr

@@ -1,0 +1,32 @@
+// ops_internal.h -- host-side interface between the C ABI of the layer
+// operators (short convolution, selective scan, residual RMS norm) and their
+// launchers.
+#pragma once
+
+#include "../csrc/gdr_internal.h"
+
+namespace gdr {
+
+// Launch failures become a status; `what` names the operator.
+gdr_status launch_status(const char* what);
+
+// --- short causal convolution (conv1d.hip) ---
+size_t conv_bwd_workspace(const gdr_conv_problem* p);
+gdr_status launch_conv_fwd(const gdr_conv_problem* p, const void* x, const void* weight,
+                           const void* bias, const void* s0, void* y, void* s1, hipStream_t st);
+gdr_status launch_conv_bwd(const gdr_conv_problem* p, const void* x, const void* weight,
+                           const void* bias, const void* dy, const void* ds1, const void* s0,
+                           void* dx, void* dw, void* db, void* ds0, void* ws, hipStream_t st);
+gdr_status launch_conv_update(const gdr_conv_problem* p, const void* x, void* state,
+                              const void* weight, const void* bias, void* y, hipStream_t st);
+
+// --- residual RMS norm (rms_norm.hip) ---
+size_t norm_bwd_workspace(const gdr_norm_problem* p);
+gdr_status launch_norm_fwd(const gdr_norm_problem* p, const void* x, const void* res,
+                           const void* weight, void* y, void* scale, void* h, float* rstd,
+                           hipStream_t st);
+gdr_status launch_norm_bwd(const gdr_norm_problem* p, const void* dy, const void* h,
+                           const void* weight, const float* rstd, const void* dh_out, void* dx,
+                           void* dres, void* dw, void* ws, hipStream_t st);
+
+}  // namespace gdr

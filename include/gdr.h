@@ -392,6 +392,109 @@ gdr_status gdr_profile_enable(int enable);
 int gdr_profile_read(char* names, size_t name_stride, double* total_ms, int* launches,
                      int max_entries);
 
+/* ==== The operators around the recurrence in a layer =======================
+ * The short causal convolution in front of it, the selective state space scan
+ * (its sibling with one decay per head and no delta term) and the RMS norm
+ * with the residual's addition.  The conventions above hold: the caller owns
+ * buffers and streams, every argument is validated on the host before any HIP
+ * call, nothing is allocated or kept, results are deterministic.  Two calls
+ * may run at once on different streams if they share no output or workspace.
+ * Where a problem states a token stride, consecutive tokens' rows of that
+ * input lie so many elements apart (a slice of a wider tensor); every other
+ * tensor is contiguous.  These operators ask only for the alignment of one
+ * element unless a function says otherwise. */
+
+/* ---- short causal depthwise convolution ----
+ * Per channel d and token t of a sequence, with x[t'] for t' before the
+ * sequence taken from the state's W - 1 rows (zero without a state):
+ *     z[t] = bias[d] + sum_{j < W} weight[d][j] x[t - (W-1) + j][d]
+ *     y[t] = z[t], or z[t] / (1 + e^-z[t]) with activation = 1
+ *   x, y, dy, dx    [B, T, D]        dtype; x with a token stride
+ *   weight          [D, W]           w_dtype, W = 2, 3 or 4
+ *   bias            [D]              w_dtype, nullable
+ *   states          [N, W - 1, D]    dtype: the last W - 1 inputs, oldest
+ *                                    first (a shorter sequence keeps the
+ *                                    younger rows of its initial state) */
+typedef struct {
+  int32_t B, T, D, W;
+  int32_t N;                      /* sequences: B, or len(cu_seqlens) - 1 */
+  const int32_t* cu_seqlens_dev;  /* as in gdr_problem */
+  const int32_t* cu_seqlens_host;
+  gdr_dtype dtype;                /* bf16, fp16 or fp32 */
+  gdr_dtype w_dtype;              /* dtype or GDR_FP32 */
+  int32_t activation;             /* 0: none, 1: silu */
+  int64_t x_stride;               /* elements between tokens of x, >= D */
+} gdr_conv_problem;
+
+/* Host-only argument check (as gdr_check_supported). */
+gdr_status gdr_conv1d_check(const gdr_conv_problem* p, char* reason, size_t reason_len);
+
+/*   in : x, weight, bias (nullable), initial_state (nullable = zeros)
+ *   out: y; final_state (nullable = not written) */
+gdr_status gdr_conv1d_fwd(const gdr_conv_problem* p, const void* x, const void* weight,
+                          const void* bias, const void* initial_state, void* y,
+                          void* final_state, void* stream);
+
+/* The gradient: dfinal_state (nullable = zero) is the gradient of
+ * final_state.  out: dx, dweight; dbias (nullable = not written);
+ * dinitial_state (nullable = not written; only with initial_state). */
+size_t gdr_conv1d_bwd_workspace_size(const gdr_conv_problem* p);
+gdr_status gdr_conv1d_bwd(const gdr_conv_problem* p, const void* x, const void* weight,
+                          const void* bias, const void* dy, const void* dfinal_state,
+                          const void* initial_state, void* dx, void* dweight, void* dbias,
+                          void* dinitial_state, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* One or a few tokens per sequence (dense, B sequences of T tokens, B <=
+ * 65535) on cached states: y as above, and `state` [B, W-1, D] is updated in
+ * place. */
+gdr_status gdr_conv1d_update(const gdr_conv_problem* p, const void* x, void* state,
+                             const void* weight, const void* bias, void* y, void* stream);
+
+/* ---- root-mean-square norm with the residual's addition ----
+ * Per row, with h = x + residual rounded to res_dtype (h = x without one):
+ *     y = weight h / sqrt(mean(h^2) + eps)
+ * in dtype, or quantised to 8 bits: scale = max(max|y| / top, 2^-126) over the
+ * row or over each 128 columns (the last group of a row may be narrower),
+ * q = y / scale rounded to nearest even; top = 448 (e4m3, OCP) or 127 (int8).
+ * A NaN in a group makes its scale NaN (and an int8 value 0).
+ *   x, y, dy, dx [rows, D] dtype (x with a row stride); residual, h, dh,
+ *   dresidual [rows, D] res_dtype; weight, dweight [D] w_dtype; q [rows, D]
+ *   8 bits; scale [rows] or [rows, ceil(D / 128)] fp32; rstd [rows] fp32
+ * D <= 65536. */
+typedef struct {
+  int32_t rows, D;
+  gdr_dtype dtype;                /* bf16, fp16 or fp32 */
+  gdr_dtype res_dtype;            /* dtype or GDR_FP32 (read when has_residual) */
+  gdr_dtype w_dtype;              /* dtype or GDR_FP32 */
+  int32_t has_residual;
+  int32_t quant;                  /* 0: y in dtype, 1: e4m3, 2: int8 */
+  int32_t group_size;             /* columns per scale: 0 = the row, or 128 */
+  float eps;                      /* finite, >= 0 */
+  int64_t x_stride;               /* elements between rows of x, >= D */
+} gdr_norm_problem;
+
+gdr_status gdr_rms_norm_check(const gdr_norm_problem* p, char* reason, size_t reason_len);
+
+/*   in : x, weight, residual (iff has_residual)
+ *   out: y (q when quantised); scale (iff quantised); h (iff has_residual);
+ *        rstd (nullable: 1 / sqrt(mean h^2 + eps), which the gradient takes) */
+gdr_status gdr_rms_norm_fwd(const gdr_norm_problem* p, const void* x, const void* residual,
+                            const void* weight, void* y, float* scale, void* h, float* rstd,
+                            void* stream);
+
+/* The gradient (quant = 0).  h is what the forward normalised: its h with a
+ * residual, else x (with x's row stride).
+ *   in : dy, h, weight, rstd; dh (nullable = zero; iff has_residual allowed):
+ *        the gradient of the stored h
+ *   out: dx; dresidual (nullable; the same gradient in res_dtype, for
+ *        residuals of another type than x); dweight */
+size_t gdr_rms_norm_bwd_workspace_size(const gdr_norm_problem* p);
+gdr_status gdr_rms_norm_bwd(const gdr_norm_problem* p, const void* dy, const void* h,
+                            const void* weight, const float* rstd, const void* dh, void* dx,
+                            void* dresidual, void* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

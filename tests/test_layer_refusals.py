@@ -1,0 +1,133 @@
+"""Refusals of the layer operators on the host (no GPU): every argument is
+checked before any HIP call, so bad sizes, types and offsets are errors here."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_66_amd as gdr
+from gated_delta_rule_66_amd import _lib
+from gated_delta_rule_66_amd._lib import (GDR_BF16, GDR_FP16, GDR_FP32, ConvProblem, NormProblem,
+                                          lib)
+
+FAKE = 0x1000  # never dereferenced: validation happens on the host copy
+
+
+def offsets(*v):
+    return (ctypes.c_int32 * len(v))(*v)
+
+
+def addr(a):
+    return ctypes.cast(a, ctypes.c_void_p).value
+
+
+def conv(**kw):
+    base = dict(B=2, T=10, D=24, W=4, N=2, dtype=GDR_BF16, w_dtype=GDR_FP32, activation=1,
+                x_stride=24)
+    base.update(kw)
+    return ConvProblem(**base)
+
+
+def norm(**kw):
+    base = dict(rows=4, D=40, dtype=GDR_BF16, res_dtype=GDR_FP32, w_dtype=GDR_BF16, has_residual=1,
+                quant=0, group_size=0, eps=1e-6, x_stride=40)
+    base.update(kw)
+    return NormProblem(**base)
+
+
+def verdict(f, p):
+    reason = ctypes.create_string_buffer(256)
+    st = f(ctypes.byref(p) if p is not None else None, reason, 256)
+    return _lib.STATUS[st], reason.value.decode()
+
+
+CONV = [
+    (conv(W=1), "GDR_ERR_SHAPE", "width"),
+    (conv(W=5), "GDR_ERR_SHAPE", "width"),
+    (conv(T=0), "GDR_ERR_SHAPE", "positive"),
+    (conv(D=0, x_stride=0), "GDR_ERR_SHAPE", "positive"),
+    (conv(D=70000, x_stride=70000), "GDR_ERR_SHAPE", "65536"),
+    (conv(B=70000, N=70000, T=70000), "GDR_ERR_SHAPE", "too large"),
+    (conv(x_stride=23), "GDR_ERR_SHAPE", "x_stride"),
+    (conv(N=3), "GDR_ERR_SHAPE", "N == B"),
+    (conv(dtype=7), "GDR_ERR_DTYPE", "x must"),
+    (conv(w_dtype=GDR_FP16), "GDR_ERR_DTYPE", "weight"),
+    (conv(activation=2), "GDR_ERR_ARG", "activation"),
+    (conv(cu_seqlens_dev=FAKE), "GDR_ERR_VARLEN", "host copy"),
+]
+NORM = [
+    (norm(rows=0), "GDR_ERR_SHAPE", "positive"),
+    (norm(D=65537, x_stride=65537), "GDR_ERR_SHAPE", "65536"),
+    (norm(rows=1 << 28), "GDR_ERR_SHAPE", "rows"),
+    (norm(x_stride=39), "GDR_ERR_SHAPE", "x_stride"),
+    (norm(dtype=-1), "GDR_ERR_DTYPE", "x must"),
+    (norm(res_dtype=GDR_FP16), "GDR_ERR_DTYPE", "residual"),
+    (norm(w_dtype=GDR_FP16), "GDR_ERR_DTYPE", "weight"),
+    (norm(has_residual=2), "GDR_ERR_ARG", "has_residual"),
+    (norm(quant=3), "GDR_ERR_ARG", "quant"),
+    (norm(quant=1, group_size=64), "GDR_ERR_ARG", "group_size"),
+    (norm(group_size=128), "GDR_ERR_ARG", "quantised"),
+    (norm(eps=-1.0), "GDR_ERR_ARG", "eps"),
+    (norm(eps=float("nan")), "GDR_ERR_ARG", "eps"),
+]
+
+
+def test_accepted():
+    assert verdict(lib.gdr_conv1d_check, conv()) == ("GDR_OK", "")
+    assert verdict(lib.gdr_conv1d_check, conv(dtype=GDR_FP32, W=2))[0] == "GDR_OK"
+    assert verdict(lib.gdr_rms_norm_check, norm()) == ("GDR_OK", "")
+    assert verdict(lib.gdr_rms_norm_check, norm(quant=2, group_size=128))[0] == "GDR_OK"
+
+
+@pytest.mark.parametrize("p,status,msg", CONV)
+def test_conv_rejections(p, status, msg):
+    st, reason = verdict(lib.gdr_conv1d_check, p)
+    assert st == status and msg in reason and msg in lib.gdr_last_error().decode()
+    assert lib.gdr_conv1d_bwd_workspace_size(ctypes.byref(p)) == 0
+
+
+@pytest.mark.parametrize("p,status,msg", NORM)
+def test_norm_rejections(p, status, msg):
+    st, reason = verdict(lib.gdr_rms_norm_check, p)
+    assert st == status and msg in reason
+    assert lib.gdr_rms_norm_bwd_workspace_size(ctypes.byref(p)) == 0
+
+
+@pytest.mark.parametrize("cu", [(1, 4, 10), (0, 6, 4, 10), (0, 4, 9)])
+def test_bad_offsets(cu):
+    host = offsets(*cu)
+    p = conv(B=1, N=len(cu) - 1, cu_seqlens_dev=FAKE, cu_seqlens_host=addr(host))
+    assert verdict(lib.gdr_conv1d_check, p)[0] == "GDR_ERR_VARLEN"
+    p.B = 2
+    assert verdict(lib.gdr_conv1d_check, p)[0] == "GDR_ERR_VARLEN"
+
+
+def test_null_pointers_and_workspaces():
+    p = conv()
+    assert lib.gdr_conv1d_fwd(ctypes.byref(p), None, FAKE, None, None, FAKE, None, None) == 1
+    assert lib.gdr_conv1d_fwd(ctypes.byref(p), FAKE, FAKE, None, FAKE, FAKE, FAKE, None) == 10
+    assert lib.gdr_conv1d_update(ctypes.byref(p), FAKE, None, FAKE, None, FAKE, None) == 1
+    assert lib.gdr_conv1d_update(ctypes.byref(conv(B=65536, N=65536)), FAKE, FAKE, FAKE, None, FAKE,
+                                 None) == 2
+    n = lib.gdr_conv1d_bwd_workspace_size(ctypes.byref(p))
+    assert n >= 5 * 24 * 4
+    args = [FAKE, FAKE, None, FAKE, None, None, FAKE, FAKE, None, None]
+    assert lib.gdr_conv1d_bwd(ctypes.byref(p), *args, FAKE, n - 1, None) == 7
+    assert lib.gdr_conv1d_bwd(ctypes.byref(p), *args[:-1], FAKE, FAKE, n, None) == 10
+    q = norm()
+    assert lib.gdr_rms_norm_fwd(ctypes.byref(q), FAKE, None, FAKE, FAKE, None, FAKE, None, None) == 1
+    assert lib.gdr_rms_norm_fwd(ctypes.byref(q), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None) == 1
+    n = lib.gdr_rms_norm_bwd_workspace_size(ctypes.byref(q))
+    args = [FAKE] * 4 + [None, FAKE, None, FAKE]
+    assert lib.gdr_rms_norm_bwd(ctypes.byref(q), *args, FAKE, n - 1, None) == 7
+    assert lib.gdr_rms_norm_bwd(ctypes.byref(norm(quant=1)), *args, FAKE, n, None) == 10
+    assert verdict(lib.gdr_rms_norm_check, None)[0] == "GDR_ERR_NULL"
+
+
+def test_tensors_on_the_host_are_refused():
+    x, w = torch.zeros(2, 5, 8), torch.zeros(8, 4)
+    for call in (lambda: gdr.causal_conv1d(x, w), lambda: gdr.causal_conv1d_update(x, x, w),
+                 lambda: gdr.rms_norm(x, w[:, 0]), lambda: gdr.rms_norm_quant(x, w[:, 0])):
+        with pytest.raises(gdr.GdrError) as e:
+            call()
+        assert e.value.name == "GDR_ERR_DEVICE"
