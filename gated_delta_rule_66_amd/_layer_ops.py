@@ -1,5 +1,6 @@
 """The operators around the recurrence in a layer: the short causal
-convolution and the RMS norm with the residual's addition.
+convolution, the selective state space scan and the RMS norm with the
+residual's addition.
 
 Thin bindings over libgdr.so, re-exported by the package: PyTorch provides
 device memory, the current stream and autograd; every computation runs in the
@@ -14,7 +15,8 @@ import ctypes
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import (GDR_BF16, GDR_FP16, GDR_FP32, ConvProblem, GdrError, NormProblem, check, lib)
+from ._lib import (GDR_BF16, GDR_FP16, GDR_FP32, ConvProblem, GdrError, NormProblem, SsmProblem, check,
+                   lib)
 
 _DT = {torch.bfloat16: GDR_BF16, torch.float16: GDR_FP16, torch.float32: GDR_FP32}
 _NULL_GUARD = contextlib.nullcontext()
@@ -230,6 +232,92 @@ def causal_conv1d_update(x, conv_state, weight, bias=None, activation="silu"):
         check(lib.gdr_conv1d_update(c.ref, _ptr(c.x), _ptr(conv_state), _ptr(c.weight),
                                     _ptr(c.bias), _ptr(y), _stream(x)))
     return y.squeeze(1) if squeeze else y
+
+
+# ---- selective state space scan --------------------------------------------------
+
+class _Ssm:
+    """The checked arguments of one scan call."""
+
+    def __init__(self, x, dt, A_log, B, C, D, dt_bias, dt_softplus, state, cu_seqlens,
+                 cu_seqlens_cpu):
+        if x.dim() != 4 or B.dim() != 4:
+            raise GdrError(2, "x must be [B, T, H, V] and B [B, T, G, K], got %s and %s"
+                           % (tuple(x.shape), tuple(B.shape)))
+        _need_gpu("x", x)
+        b, T, H, V = x.shape
+        G, K = B.shape[2], B.shape[3]
+        dev = x.device
+        code = _code(x, "x")
+        _expect("B", B, (b, T, G, K), (x.dtype,), dev)
+        _expect("C", C, (b, T, G, K), (x.dtype,), dev)
+        self.dt = _like("dt", dt, (b, T, H), (x.dtype, torch.float32), dev)
+        self.A_log = _like("A_log", A_log, (H,), (x.dtype, torch.float32), dev)
+        self.D = _like("D", D, (H,), (A_log.dtype,), dev)
+        self.dt_bias = _like("dt_bias", dt_bias, (H,), (A_log.dtype,), dev)
+        N, self.cu, self.cu_host = _seqs(x, cu_seqlens, cu_seqlens_cpu)
+        self.state_shape = (N, H, K, V)
+        self.state = _aligned(_like("initial_state", state, self.state_shape, (torch.float32,), dev))
+        self.x, xs = _token_rows(x, 2)
+        self.B, bs = _token_rows(B, 2)
+        self.C, cs = _token_rows(C, 2)
+        self.p = SsmProblem(B=b, T=T, H=H, G=G, K=K, V=V, N=N, cu_seqlens_dev=_ptr(self.cu),
+                            cu_seqlens_host=_ptr(self.cu_host), in_dtype=code,
+                            dt_dtype=_DT[dt.dtype], p_dtype=_DT[A_log.dtype],
+                            dt_softplus=1 if dt_softplus else 0, x_stride=xs, b_stride=bs,
+                            c_stride=cs)
+        self.ref = ctypes.byref(self.p)
+        check(lib.gdr_ssm_check(self.ref, None, 0))
+
+    def inputs(self):
+        return (_ptr(self.x), _ptr(self.dt), _ptr(self.A_log), _ptr(self.B), _ptr(self.C),
+                _ptr(self.D), _ptr(self.dt_bias))
+
+
+def _aligned(t):
+    """States are read 16 bytes at a time."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
+def chunk_selective_scan_fwd(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
+                             initial_state=None, output_final_state=True, cu_seqlens=None,
+                             cu_seqlens_cpu=None):
+    """:func:`chunk_selective_scan` without autograd: ``(y, final_state)``."""
+    c = _Ssm(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens,
+             cu_seqlens_cpu)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    last = None
+    if output_final_state:
+        last = torch.empty(c.state_shape, dtype=torch.float32, device=x.device)
+    n = lib.gdr_ssm_fwd_workspace_size(c.ref)
+    ws = _bytes(n, x.device) if n else None
+    with _guard(x):
+        check(lib.gdr_ssm_fwd(c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last), _ptr(ws), n,
+                              _stream(x)))
+    return y, last
+
+
+def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
+                                   initial_state=None, output_final_state=True, cu_seqlens=None,
+                                   cu_seqlens_cpu=None, inplace_final_state=False):
+    """The scan one token at a time (decode steps, a few speculative tokens):
+    ``(y, final_state)`` of :func:`chunk_selective_scan`, the state read once
+    and written once.  With ``inplace_final_state`` the fp32 ``initial_state``
+    is updated in place and returned.  No autograd."""
+    if inplace_final_state and (initial_state is None or not initial_state.is_contiguous()
+                                or initial_state.data_ptr() % 16):
+        raise GdrError(10, "inplace_final_state needs a contiguous, 16-byte aligned initial_state")
+    c = _Ssm(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens,
+             cu_seqlens_cpu)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    last = None
+    if inplace_final_state:
+        last = initial_state
+    elif output_final_state:
+        last = torch.empty(c.state_shape, dtype=torch.float32, device=x.device)
+    with _guard(x):
+        check(lib.gdr_ssm_step(c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last), _stream(x)))
+    return y, last
 
 
 # ---- RMS norm with the residual's addition ----------------------------------------

@@ -51,6 +51,18 @@ class ConvProblem(ctypes.Structure):
     ]
 
 
+class SsmProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("G", ctypes.c_int32),
+        ("K", ctypes.c_int32), ("V", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("cu_seqlens_dev", ctypes.c_void_p),
+        ("cu_seqlens_host", ctypes.c_void_p),
+        ("in_dtype", ctypes.c_int), ("dt_dtype", ctypes.c_int), ("p_dtype", ctypes.c_int),
+        ("dt_softplus", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+    ]
+
+
 class NormProblem(ctypes.Structure):
     _fields_ = [
         ("rows", ctypes.c_int32), ("D", ctypes.c_int32),
@@ -75,6 +87,7 @@ EXPORTS = [
     "gdr_conv1d_check", "gdr_conv1d_fwd", "gdr_conv1d_bwd_workspace_size", "gdr_conv1d_bwd",
     "gdr_conv1d_update", "gdr_rms_norm_check", "gdr_rms_norm_fwd",
     "gdr_rms_norm_bwd_workspace_size", "gdr_rms_norm_bwd",
+    "gdr_ssm_check", "gdr_ssm_fwd_workspace_size", "gdr_ssm_fwd", "gdr_ssm_step",
 ]
 
 
@@ -159,6 +172,11 @@ def _declare_ops(lib):
     fn("gdr_conv1d_bwd_workspace_size", [CP], S)
     fn("gdr_conv1d_bwd", [CP] + [P] * 11 + [S, P])
     fn("gdr_conv1d_update", [CP] + [P] * 6)
+    SP = ctypes.POINTER(SsmProblem)
+    fn("gdr_ssm_check", [SP, ctypes.c_char_p, S])
+    fn("gdr_ssm_fwd_workspace_size", [SP], S)
+    fn("gdr_ssm_fwd", [SP] + [P] * 11 + [S, P])
+    fn("gdr_ssm_step", [SP] + [P] * 11)
     NP = ctypes.POINTER(NormProblem)
     fn("gdr_rms_norm_check", [NP, ctypes.c_char_p, S])
     fn("gdr_rms_norm_fwd", [NP] + [P] * 8)

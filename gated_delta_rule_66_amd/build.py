@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB = os.path.join(HERE, "libgdr.so")
 # csrc: the gated delta rule; csrc_ops: the operators around it in a layer
 SOURCES = ["csrc/gdr_api.cpp", "csrc/gdr_fwd.hip", "csrc/gdr_bwd.hip", "csrc/gdr_recurrent.hip",
-           "csrc_ops/ops_api.cpp", "csrc_ops/conv1d.hip", "csrc_ops/rms_norm.hip"]
+           "csrc_ops/ops_api.cpp", "csrc_ops/conv1d.hip", "csrc_ops/rms_norm.hip",
+           "csrc_ops/ssm_fwd.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -113,6 +113,41 @@ static gdr_status validate(const gdr_norm_problem* p, char* reason, size_t len) 
   return GDR_OK;
 }
 
+static gdr_status validate(const gdr_ssm_problem* p, char* reason, size_t len) {
+  if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
+  if ((p->K != 64 && p->K != 128) || (p->V != 64 && p->V != 128))
+    return fail(GDR_ERR_HEAD_DIM, reason, len, "K and V must be 64 or 128, got K=%d V=%d", p->K,
+                p->V);
+  if (p->in_dtype != GDR_BF16 && p->in_dtype != GDR_FP16)
+    return fail(GDR_ERR_DTYPE, reason, len, "x, B and C must be bf16 or fp16 (got code %d)",
+                (int)p->in_dtype);
+  if (p->dt_dtype != p->in_dtype && p->dt_dtype != GDR_FP32)
+    return fail(GDR_ERR_DTYPE, reason, len, "dt must have x's dtype or fp32 (got code %d)",
+                (int)p->dt_dtype);
+  if (p->p_dtype != p->in_dtype && p->p_dtype != GDR_FP32)
+    return fail(GDR_ERR_DTYPE, reason, len,
+                "A_log, D and dt_bias must have x's dtype or fp32 (got code %d)", (int)p->p_dtype);
+  if (p->B < 1 || p->T < 1 || p->H < 1 || p->G < 1)
+    return fail(GDR_ERR_SHAPE, reason, len, "sizes must be positive (B=%d T=%d H=%d G=%d)", p->B,
+                p->T, p->H, p->G);
+  if (p->G > p->H || p->H % p->G != 0)
+    return fail(GDR_ERR_HEADS, reason, len, "heads must be a multiple of groups (H=%d G=%d)", p->H,
+                p->G);
+  if ((int64_t)p->B * p->T > 0x7fffff00 || p->H > 65536 || (int64_t)p->N * p->H > (1 << 22) ||
+      (int64_t)p->B * p->T * p->H > ((int64_t)1 << 33))
+    return fail(GDR_ERR_SHAPE, reason, len, "problem too large");
+  if (p->x_stride < (int64_t)p->H * p->V || p->b_stride < (int64_t)p->G * p->K ||
+      p->c_stride < (int64_t)p->G * p->K)
+    return fail(GDR_ERR_SHAPE, reason, len,
+                "token strides must cover a token's heads (x %lld, B %lld, C %lld)",
+                (long long)p->x_stride, (long long)p->b_stride, (long long)p->c_stride);
+  if (!is_flag(p->dt_softplus))
+    return fail(GDR_ERR_ARG, reason, len, "dt_softplus must be 0 or 1");
+  return check_seqs(p->B, p->T, p->N, p->cu_seqlens_dev, p->cu_seqlens_host, reason, len);
+}
+
+static bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
+
 }  // namespace gdr
 
 using namespace gdr;
@@ -174,6 +209,51 @@ gdr_status gdr_conv1d_update(const gdr_conv_problem* p, const void* x, void* sta
     return fail(GDR_ERR_NULL, nullptr, 0, "a required convolution-update pointer is NULL");
   if ((s = gdr_check_device()) != GDR_OK) return s;
   return launch_conv_update(p, x, state, weight, bias, y, (hipStream_t)stream);
+}
+
+gdr_status gdr_ssm_check(const gdr_ssm_problem* p, char* reason, size_t reason_len) {
+  const gdr_status s = validate(p, reason, reason_len);
+  if (s == GDR_OK && reason && reason_len) reason[0] = '\0';
+  return s;
+}
+
+size_t gdr_ssm_fwd_workspace_size(const gdr_ssm_problem* p) {
+  return validate(p, nullptr, 0) == GDR_OK ? ssm_fwd_workspace(p, ssm_plan(p)) : 0;
+}
+
+gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
+                       const void* B, const void* C, const void* D, const void* dt_bias,
+                       const float* initial_state, void* y, float* final_state, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (!x || !dt || !A_log || !B || !C || !y)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required scan pointer is NULL");
+  if (final_state && final_state == initial_state)
+    return fail(GDR_ERR_ARG, nullptr, 0,
+                "final_state may not be initial_state (gdr_ssm_step works in place)");
+  if (misaligned(initial_state) || misaligned(final_state) || misaligned(workspace))
+    return fail(GDR_ERR_ARG, nullptr, 0, "states and workspace must be 16-byte aligned");
+  const SsmPlan pl = ssm_plan(p);
+  s = need_workspace(ssm_fwd_workspace(p, pl), workspace, workspace_bytes, "scan");
+  if (s != GDR_OK) return s;
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_ssm_fwd(p, pl, x, dt, A_log, B, C, D, dt_bias, initial_state, y, final_state,
+                        workspace, (hipStream_t)stream);
+}
+
+gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
+                        const void* B, const void* C, const void* D, const void* dt_bias,
+                        const float* initial_state, void* y, float* final_state, void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (!x || !dt || !A_log || !B || !C || !y)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required scan pointer is NULL");
+  if (misaligned(initial_state) || misaligned(final_state))
+    return fail(GDR_ERR_ARG, nullptr, 0, "states must be 16-byte aligned");
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_ssm_step(p, x, dt, A_log, B, C, D, dt_bias, initial_state, y, final_state,
+                         (hipStream_t)stream);
 }
 
 gdr_status gdr_rms_norm_check(const gdr_norm_problem* p, char* reason, size_t reason_len) {

@@ -29,4 +29,21 @@ gdr_status launch_norm_bwd(const gdr_norm_problem* p, const void* dy, const void
                            const void* weight, const float* rstd, const void* dh_out, void* dx,
                            void* dres, void* dw, void* ws, hipStream_t st);
 
+// --- selective state space scan (ssm_fwd.hip, ssm_bwd.hip) ---
+struct SsmPlan {
+  int seg;     // tokens per segment, a multiple of 64
+  int nids;    // segment ids
+  bool split;  // some sequence has more than one segment
+};
+SsmPlan ssm_plan(const gdr_ssm_problem* p);
+size_t ssm_fwd_workspace(const gdr_ssm_problem* p, const SsmPlan& pl);
+gdr_status launch_ssm_fwd(const gdr_ssm_problem* p, const SsmPlan& pl, const void* x,
+                          const void* dt, const void* A_log, const void* B, const void* C,
+                          const void* D, const void* dt_bias, const float* h0, void* y, float* ht,
+                          void* ws, hipStream_t st);
+gdr_status launch_ssm_step(const gdr_ssm_problem* p, const void* x, const void* dt,
+                           const void* A_log, const void* B, const void* C, const void* D,
+                           const void* dt_bias, const float* h0, void* y, float* ht,
+                           hipStream_t st);
+
 }  // namespace gdr

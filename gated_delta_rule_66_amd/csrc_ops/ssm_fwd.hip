@@ -1,0 +1,491 @@
+// ssm_fwd.hip -- the selective state space scan on gfx950: prompts chunk by
+// chunk on matrix instructions, single tokens on cached states.
+//
+// A prompt moves 4 V bytes of x and y per token and head (16 bits) and needs
+// about 2 K V multiply-adds: on this card memory and the matrix units take
+// about the same time, and few heads leave CUs idle.  So sequences are cut
+// into segments until the launch fills the chip: ssm_state_kernel forms what
+// every segment but the last adds to the state (reads x and B only),
+// ssm_combine_kernel adds them up along each sequence, and ssm_out_kernel
+// walks each segment from its start state.
+#include <algorithm>
+
+#include "ssm_device.h"
+
+namespace gdr {
+
+namespace {
+
+constexpr int kNT = 256;
+
+// The ten 16 x 16 tiles on or below the diagonal of a 64 x 64 matrix over four
+// waves (3, 3, 2, 2): 4 bits each, row block * 4 + column block.
+constexpr uint64_t kTiles = 0xC | (0xDull << 4) | (0x0ull << 8) |        // wave 0
+                            (0xEull << 12) | (0xFull << 16) | (0x5ull << 20) |  // wave 1
+                            (0x8ull << 24) | (0x9ull << 28) |            // wave 2
+                            (0xAull << 36) | (0x4ull << 40);             // wave 3
+__device__ __forceinline__ int tile_of(int w, int s) { return (int)(kTiles >> (12 * w + 4 * s)) & 15; }
+__device__ __forceinline__ int tiles_of(int w) { return w < 2 ? 3 : 2; }
+
+template <typename T, int K, int V>
+struct OutSmem {
+  static constexpr int LK = K + 8, LV = V + 8, LM = 64 + 8;
+  T C[64 * LK];
+  T B[64 * LK];
+  T X[64 * LV];
+  T M[64 * LM];
+  float gam[64], eg[64], wt[64], dts[64];
+};
+
+// OUT: the segment's outputs from its start state; else what it adds to the
+// state.  Four waves, each with V / 4 state columns in MFMA accumulators.
+template <typename T, int K, int V, bool OUT>
+__global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
+  typedef typename VT<T>::x8 x8;
+  typedef OutSmem<T, K, V> Smem;
+  constexpr int LK = Smem::LK, LV = Smem::LV, LM = Smem::LM;
+  constexpr int NT = K / 16, PT = V / 64;
+  constexpr bool kScaled = !__is_same(T, __bf16);
+  __shared__ Smem s;
+  const int L = xcd_order(blockIdx.x, gridDim.x);
+  const int id = L / a.H, h = L % a.H, grp_h = h / (a.H / a.G);
+  const Segment sg = segment_of(a, id);
+  if (sg.count == 0) return;
+  if (!OUT && sg.j + 1 >= sg.count) return;
+  const int w = threadIdx.x >> 6, l = lane_id(), g4 = l >> 4, col = l & 15;
+
+  const T* xg = reinterpret_cast<const T*>(a.x) + (int64_t)h * V;
+  const T* bg = reinterpret_cast<const T*>(a.B) + (int64_t)grp_h * K;
+  const T* cg = reinterpret_cast<const T*>(a.C) + (int64_t)grp_h * K;
+  const float rate = -expf(load_scalar(a.A_log, h, a.p_dtype));
+  const float bias = param(a.dt_bias, h, a.p_dtype), skip = param(a.D, h, a.p_dtype);
+
+  // the state in accumulators
+  f32x4 S[PT][NT];
+  const int64_t unit = ((int64_t)sg.n * a.H + h) * K * V;
+  const int64_t slot = ((int64_t)id * a.H + h) * K * V;
+  if (OUT && sg.j > 0) {
+    const float* src = a.seg_state + slot - (int64_t)a.H * K * V;
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        S[pt][nt] = *reinterpret_cast<const f32x4*>(src + (((w * PT + pt) * NT + nt) * 64 + l) * 4);
+  } else {
+    const bool from = OUT && a.h0;
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          S[pt][nt][e] = from ? a.h0[unit + (int64_t)state_k<V>(nt, e) * V + state_v<V>(w, pt)] : 0.f;
+  }
+  if (OUT) {  // tiles above the diagonal that the product with M reads: (0, 1) and (2, 3)
+    for (int i = threadIdx.x; i < 512; i += kNT) {
+      const int r = (i >> 8) * 32 + ((i >> 4) & 15), c = (i >> 8) * 32 + 16 + (i & 15);
+      s.M[r * LM + c] = (T)0.f;
+    }
+  }
+
+  Rows64<T, K, kNT> rb, rc;
+  Rows64<T, V, kNT> rx;
+  float raw = 0.f, total = 0.f;
+  auto request = [&](int64_t t) {
+    const int rows = (int)min((int64_t)64, sg.t1 - t);
+    rx.load(xg + t * a.xs, a.xs, rows);
+    rb.load(bg + t * a.bs, a.bs, rows);
+    if (OUT) rc.load(cg + t * a.cs, a.cs, rows);
+    raw = l < rows ? load_scalar(a.dt, (t + l) * a.H + h, a.dt_dtype) : 0.f;
+  };
+  if (sg.t0 < sg.t1) request(sg.t0);
+
+  for (int64_t t = sg.t0; t < sg.t1; t += 64) {
+    const int rows = (int)min((int64_t)64, sg.t1 - t);
+    // the chunk's gate, one token per lane (every wave forms it; the first
+    // one stores it); tokens past the end have step size 0
+    const float step = l < rows ? ssm_step_size(raw, bias, a.softplus) : 0.f;
+    const float g = rate * step;
+    const float gam = wave_inclusive_scan(g), suf = wave_suffix_excl(g);
+    const float all = __shfl(gam, 63, 64);
+    total += all;
+    if (w == 0) {
+      s.gam[l] = gam;
+      s.eg[l] = __expf(gam);
+      s.wt[l] = step * __expf(suf);
+      s.dts[l] = step;
+    }
+    rx.store(s.X, LV);
+    rb.store(s.B, LK);
+    if (OUT) rc.store(s.C, LK);
+    __syncthreads();
+    if (t + 64 < sg.t1) request(t + 64);
+
+    f32x4 acc[PT][4];
+    if (OUT) {
+      // M = (C B^T) o L diag(dt), rounded to T as an operand
+      const int nt = tiles_of(w);
+      for (int k = 0; k < nt; ++k) {
+        const int ti = tile_of(w, k), rbk = ti >> 2, cbk = ti & 3;
+        f32x4 m = zero4();
+#pragma unroll
+        for (int kb = 0; kb < K / 32; ++kb)
+          m = mfma16(frag_row(s.C + 16 * rbk * LK + 32 * kb, LK),
+                     frag_row(s.B + 16 * cbk * LK + 32 * kb, LK), m);
+        const int i = 16 * cbk + col;
+        const float gi = s.gam[i], di = s.dts[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * rbk + 4 * g4 + e;
+          const float v = r >= i ? m[e] * __expf(s.gam[r] - gi) * di : 0.f;
+          s.M[r * LM + i] = from_f<T>(v);
+        }
+      }
+      // the state's part of the output, transposed: rows v, columns t
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[pt][r] = zero4();
+#pragma unroll
+      for (int kb = 0; kb < K / 32; ++kb) {
+        x8 sf[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) sf[pt] = pack8<T>(S[pt][2 * kb], S[pt][2 * kb + 1]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const x8 cf = frag_row(s.C + 16 * r * LK + 32 * kb, LK);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[pt][r] = mfma16(sf[pt], cf, acc[pt][r]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float eg = s.eg[16 * r + col];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) acc[pt][r] *= eg;
+      }
+      __syncthreads();
+    }
+
+    // x^T fragments serve the product with M and, weighted, the state's
+    // update; with fp16 the state's columns are scaled while it is added
+    const float decay = __expf(all);
+    x8 xf[2][PT];
+    float wt[2][8], scale[PT];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wt[tb][e] = s.wt[32 * tb + 8 * g4 + e];
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+        xf[tb][pt] = frag_tr(s.X + 32 * tb * LV + w * (V / 4) + 16 * pt, LV);
+    }
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) {
+      scale[pt] = 1.f;
+      if (kScaled) {
+        float m = 0.f;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(to_f(xf[tb][pt][e]) * wt[tb][e]));
+        scale[pt] = ldexpf(1.f, column_exponent(m));
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= decay * scale[pt];
+    }
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+      x8 hi[PT], lo[PT];
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        if (OUT) {
+#pragma unroll
+          for (int r = 2 * tb; r < 4; ++r)
+            acc[pt][r] = mfma16(xf[tb][pt], frag_row(s.M + 16 * r * LM + 32 * tb, LM), acc[pt][r]);
+        }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = to_f(xf[tb][pt][e]) * wt[tb][e] * scale[pt];
+        split8<T>(v, hi[pt], lo[pt]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const x8 bf = frag_tr_pair(s.B + 32 * tb * LK + 32 * (nt >> 1) + 4 * (nt & 1), LK);
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          S[pt][nt] = mfma16(bf, hi[pt], S[pt][nt]);
+          S[pt][nt] = mfma16(bf, lo[pt], S[pt][nt]);
+        }
+      }
+    }
+    if (kScaled) {
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        const float back = 1.f / scale[pt];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= back;
+      }
+    }
+
+    if (OUT) {
+      typedef typename VT<T>::x4 x4;
+      struct __attribute__((packed, aligned(sizeof(T)))) Raw {
+        uint32_t u[2];
+      };
+      T* y = reinterpret_cast<T*>(a.y) + ((t * a.H) + h) * V;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * r + col;
+        if (row < rows) {
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) {
+            const int v0 = w * (V / 4) + 16 * pt + 4 * g4;
+            const x4 xv = *reinterpret_cast<const x4*>(s.X + row * LV + v0);
+            x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = from_f<T>(acc[pt][r][e] + skip * to_f(xv[e]));
+            *reinterpret_cast<Raw*>(y + (int64_t)row * a.H * V + v0) = __builtin_bit_cast(Raw, o);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  if (!OUT) {
+    float* dst = a.seg_state + slot;
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<f32x4*>(dst + (((w * PT + pt) * NT + nt) * 64 + l) * 4) = S[pt][nt];
+    if (threadIdx.x == 0) a.seg_decay[(int64_t)id * a.H + h] = total;
+  } else if (a.ht && sg.j + 1 == sg.count) {
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          a.ht[unit + (int64_t)state_k<V>(nt, e) * V + state_v<V>(w, pt)] = S[pt][nt][e];
+  }
+}
+
+// Segment j's end state over what it added: E_j = e^{decay_j} E_{j-1} + add_j,
+// E_{-1} the initial state; one thread per four state elements walks the
+// sequence's segments (all but the last).
+template <int K, int V>
+__global__ __launch_bounds__(256) void ssm_combine_kernel(SsmArgs a) {
+  constexpr int parts = K * V / 1024;
+  const int part = blockIdx.x % parts;
+  const int u = blockIdx.x / parts, n = u / a.H, h = u % a.H;
+  int id0;
+  int64_t len;
+  if (a.cu) {
+    id0 = n + a.cu[n] / a.seg;
+    len = a.cu[n + 1] - a.cu[n];
+  } else {
+    id0 = n * ((a.T + a.seg - 1) / a.seg);
+    len = a.T;
+  }
+  const int m = (int)((len + a.seg - 1) / a.seg);
+  if (m < 2) return;
+  const int at = (part * 256 + threadIdx.x) * 4;      // element in the register order
+  f32x4 E = zero4();
+  if (a.h0) {
+    // register order: [wave][pt][nt][lane][e]
+    constexpr int NT = K / 16, PT = V / 64;
+    const int lane = (at >> 2) & 63, q = at >> 8, nt = q % NT, pt = (q / NT) % PT, w = q / (NT * PT);
+    const int v = w * (V / 4) + 16 * pt + (lane & 15);
+    const int k = 32 * (nt >> 1) + 8 * (lane >> 4) + 4 * (nt & 1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) E[e] = a.h0[((int64_t)n * a.H + h) * K * V + (int64_t)(k + e) * V + v];
+  }
+  const int64_t step = (int64_t)a.H * K * V;
+  float* p = a.seg_state + ((int64_t)id0 * a.H + h) * K * V + at;
+  const float* dec = a.seg_decay + (int64_t)id0 * a.H + h;
+  f32x4 next = *reinterpret_cast<const f32x4*>(p);
+  for (int j = 0; j + 1 < m; ++j) {
+    const f32x4 add = next;
+    if (j + 2 < m) next = *reinterpret_cast<const f32x4*>(p + step);
+    E = E * __expf(dec[(int64_t)j * a.H]) + add;
+    *reinterpret_cast<f32x4*>(p) = E;
+    p += step;
+  }
+}
+
+// Single tokens (or a few) on a cached state: 256 threads hold 32 columns of
+// one head's state, read once and written once; thread (c, r) has columns
+// 4 c .. 4 c + 3 of rows r, r + 32, ...  The state's bytes bound it.
+template <typename T, int K, int V>
+__global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
+  constexpr int R = K / 32;
+  __shared__ f32x4 red[2][4][8];
+  const int blocks = V / 32;
+  const int vb = blockIdx.x % blocks, u = blockIdx.x / blocks, n = u / a.H, h = u % a.H;
+  const int grp_h = h / (a.H / a.G);
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, w = threadIdx.x >> 6;
+  const int64_t base = ((int64_t)n * a.H + h) * K * V + 32 * vb + 4 * c;
+  int64_t t0, t1;
+  if (a.cu) {
+    t0 = a.cu[n];
+    t1 = a.cu[n + 1];
+  } else {
+    t0 = (int64_t)n * a.T;
+    t1 = t0 + a.T;
+  }
+  f32x4 S[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    S[i] = a.h0 ? *reinterpret_cast<const f32x4*>(a.h0 + base + (int64_t)(r + 32 * i) * V) : zero4();
+  const float rate = -expf(load_scalar(a.A_log, h, a.p_dtype));
+  const float bias = param(a.dt_bias, h, a.p_dtype), skip = param(a.D, h, a.p_dtype);
+  const T* xg = reinterpret_cast<const T*>(a.x) + (int64_t)h * V + 32 * vb + 4 * c;
+  const T* bg = reinterpret_cast<const T*>(a.B) + (int64_t)grp_h * K + r;
+  const T* cg = reinterpret_cast<const T*>(a.C) + (int64_t)grp_h * K + r;
+  T* yg = reinterpret_cast<T*>(a.y) + (int64_t)h * V + 32 * vb + 4 * c;
+  for (int64_t t = t0; t < t1; ++t) {
+    const float step = ssm_step_size(load_scalar(a.dt, t * a.H + h, a.dt_dtype), bias, a.softplus);
+    const float decay = __expf(rate * step);
+    f32x4 x, y = zero4();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = to_f(xg[t * a.xs + e]);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float b = step * to_f(bg[t * a.bs + 32 * i]), q = to_f(cg[t * a.cs + 32 * i]);
+      S[i] = S[i] * decay + b * x;
+      y += q * S[i];
+    }
+    // over the 8 row groups of the wave, then over the waves
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v = y[e];
+      v += __shfl_xor(v, 8, 64);
+      v = sum4g(v);
+      y[e] = v;
+    }
+    const int par = (int)(t & 1);
+    if ((threadIdx.x & 63) < 8) red[par][w][c] = y;
+    __syncthreads();
+    if (threadIdx.x < 8) {
+      const f32x4 o = (red[par][0][c] + red[par][1][c]) + (red[par][2][c] + red[par][3][c]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) yg[t * a.H * V + e] = from_f<T>(o[e] + skip * x[e]);
+    }
+  }
+  if (a.ht) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      *reinterpret_cast<f32x4*>(a.ht + base + (int64_t)(r + 32 * i) * V) = S[i];
+  }
+}
+
+SsmArgs args_of(const gdr_ssm_problem* p, const SsmPlan& pl) {
+  SsmArgs a{};
+  a.cu = p->cu_seqlens_dev;
+  a.xs = p->x_stride;
+  a.bs = p->b_stride;
+  a.cs = p->c_stride;
+  a.N = p->N;
+  a.T = p->T;
+  a.H = p->H;
+  a.G = p->G;
+  a.seg = pl.seg;
+  a.nids = pl.nids;
+  a.dt_dtype = (int)p->dt_dtype;
+  a.p_dtype = (int)p->p_dtype;
+  a.softplus = p->dt_softplus;
+  return a;
+}
+
+}  // namespace
+
+// How sequences are cut.  Uncut, a launch takes the longest sequence's chunks;
+// cut, every chunk's x and B are read twice and two launches are added, worth
+// about four chunks.  `slots` workgroups run at once.
+SsmPlan ssm_plan(const gdr_ssm_problem* p) {
+  const int64_t slots = p->V == 64 ? 768 : 512;
+  int64_t chunks = 0, longest = 0, tokens = 0;
+  for (int n = 0; n < (p->cu_seqlens_host ? p->N : 1); ++n) {
+    const int64_t len = p->cu_seqlens_host
+                            ? (int64_t)p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n]
+                            : p->T;
+    chunks += (len + 63) / 64;
+    longest = std::max(longest, (len + 63) / 64);
+    tokens += len;
+  }
+  if (!p->cu_seqlens_host) chunks *= p->B;
+  const int64_t ideal = std::max<int64_t>(4, (chunks * p->H + slots - 1) / slots);
+  SsmPlan pl;
+  pl.split = 2 * longest > 3 * ideal + 8;
+  int64_t sc = pl.split ? ideal : std::max<int64_t>(1, longest);
+  pl.seg = (int)(sc * 64);
+  pl.nids = p->cu_seqlens_host ? (int)(p->N + tokens / pl.seg)
+                               : (int)(p->B * ((p->T + (int64_t)pl.seg - 1) / pl.seg));
+  return pl;
+}
+
+size_t ssm_fwd_workspace(const gdr_ssm_problem* p, const SsmPlan& pl) {
+  if (!pl.split) return 0;
+  return align256((size_t)pl.nids * p->H * p->K * p->V * sizeof(float)) +
+         align256((size_t)pl.nids * p->H * sizeof(float));
+}
+
+template <typename F>
+static void by_shape(const gdr_ssm_problem* p, F f) {
+  auto type = [&](auto t) {
+    using T = decltype(t);
+    auto c64 = std::integral_constant<int, 64>();
+    auto c128 = std::integral_constant<int, 128>();
+    if (p->K == 64 && p->V == 64) f(T(), c64, c64);
+    else if (p->K == 64) f(T(), c64, c128);
+    else if (p->V == 64) f(T(), c128, c64);
+    else f(T(), c128, c128);
+  };
+  if (p->in_dtype == GDR_BF16) type(__bf16());
+  else type(_Float16());
+}
+
+gdr_status launch_ssm_fwd(const gdr_ssm_problem* p, const SsmPlan& pl, const void* x,
+                          const void* dt, const void* A_log, const void* B, const void* C,
+                          const void* D, const void* dt_bias, const float* h0, void* y, float* ht,
+                          void* ws, hipStream_t st) {
+  SsmArgs a = args_of(p, pl);
+  a.x = x; a.dt = dt; a.A_log = A_log; a.B = B; a.C = C; a.D = D; a.dt_bias = dt_bias;
+  a.h0 = h0; a.y = y; a.ht = ht;
+  if (pl.split) {
+    a.seg_state = reinterpret_cast<float*>(ws);
+    a.seg_decay = reinterpret_cast<float*>(
+        reinterpret_cast<char*>(ws) + align256((size_t)pl.nids * p->H * p->K * p->V * sizeof(float)));
+  }
+  const dim3 grid((unsigned)((int64_t)pl.nids * p->H));
+  by_shape(p, [&](auto t, auto k, auto v) {
+    using T = decltype(t);
+    constexpr int K = k.value, V = v.value;
+    if (pl.split) {
+      GDR_LAUNCH("ssm_state", (ssm_walk_kernel<T, K, V, false>), grid, dim3(kNT), st, a);
+      GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V>),
+                 dim3((unsigned)((int64_t)p->N * p->H * (K * V / 1024))), dim3(256), st, a);
+    }
+    GDR_LAUNCH("ssm_out", (ssm_walk_kernel<T, K, V, true>), grid, dim3(kNT), st, a);
+  });
+  return launch_status("ssm_fwd");
+}
+
+gdr_status launch_ssm_step(const gdr_ssm_problem* p, const void* x, const void* dt,
+                           const void* A_log, const void* B, const void* C, const void* D,
+                           const void* dt_bias, const float* h0, void* y, float* ht,
+                           hipStream_t st) {
+  SsmArgs a = args_of(p, SsmPlan{64, 0, false});
+  a.x = x; a.dt = dt; a.A_log = A_log; a.B = B; a.C = C; a.D = D; a.dt_bias = dt_bias;
+  a.h0 = h0; a.y = y; a.ht = ht;
+  by_shape(p, [&](auto t, auto k, auto v) {
+    constexpr int K = k.value, V = v.value;
+    GDR_LAUNCH("ssm_step", (ssm_step_kernel<decltype(t), K, V>),
+               dim3((unsigned)((int64_t)p->N * p->H * (V / 32))), dim3(256), st, a);
+  });
+  return launch_status("ssm_step");
+}
+
+}  // namespace gdr

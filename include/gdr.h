@@ -451,6 +451,56 @@ gdr_status gdr_conv1d_bwd(const gdr_conv_problem* p, const void* x, const void* 
 gdr_status gdr_conv1d_update(const gdr_conv_problem* p, const void* x, void* state,
                              const void* weight, const void* bias, void* y, void* stream);
 
+/* ---- selective state space scan ----
+ * Per sequence and head h (group h / (H / G)), with a K x V fp32 state S,
+ * rate = -exp(A_log[h]), dt_t = softplus(raw_t + dt_bias[h]) with dt_softplus
+ * (raw_t + dt_bias[h] without):
+ *     S_t = exp(rate dt_t) S_{t-1} + dt_t B_t x_t^T
+ *     y_t = S_t^T C_t + D[h] x_t
+ * the recurrence of Mamba-2 layers: the gated delta rule's sibling with the
+ * same gate and no delta term (C, B and x in the places of q, k and v).
+ *   x, y, dy, dx   [B, T, H, V]   in_dtype; x with a token stride
+ *   B, C, dB, dC   [B, T, G, K]   in_dtype; B, C with a token stride
+ *   dt, ddt        [B, T, H]      dt_dtype
+ *   A_log, D, dt_bias [H]         p_dtype; D and dt_bias nullable (zero)
+ *   states         [N, H, K, V]   fp32, 16-byte aligned
+ * K and V are 64 or 128.  Products run on 16-bit operands with fp32 sums; the
+ * states and their gradients are as exact as fp32 inputs would make them, the
+ * products inside a chunk (64 tokens) round their decayed scores to in_dtype:
+ * with fp16 their magnitude |C_t . B_s| dt_s, and the state's, must stay below
+ * 65504. */
+typedef struct {
+  int32_t B, T, H, G, K, V;
+  int32_t N;                      /* sequences: B, or len(cu_seqlens) - 1 */
+  const int32_t* cu_seqlens_dev;  /* as in gdr_problem */
+  const int32_t* cu_seqlens_host;
+  gdr_dtype in_dtype;             /* bf16 or fp16 */
+  gdr_dtype dt_dtype;             /* in_dtype or GDR_FP32 */
+  gdr_dtype p_dtype;              /* in_dtype or GDR_FP32 */
+  int32_t dt_softplus;            /* 0 or 1 */
+  int64_t x_stride;               /* elements between tokens, >= H * V */
+  int64_t b_stride, c_stride;     /* the same for B and C, >= G * K */
+} gdr_ssm_problem;
+
+gdr_status gdr_ssm_check(const gdr_ssm_problem* p, char* reason, size_t reason_len);
+
+/* Forward over whole sequences: initial_state (nullable = zeros), y,
+ * final_state (nullable = not written; not initial_state).  Long sequences
+ * are cut into segments that run in parallel; the cuts depend on the shapes
+ * and lengths only. */
+size_t gdr_ssm_fwd_workspace_size(const gdr_ssm_problem* p);
+gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
+                       const void* B, const void* C, const void* D, const void* dt_bias,
+                       const float* initial_state, void* y, float* final_state, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Token by token for decode steps: the same y and final_state, the state read
+ * once and written once; final_state may be initial_state (updated in
+ * place). */
+gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
+                        const void* B, const void* C, const void* D, const void* dt_bias,
+                        const float* initial_state, void* y, float* final_state, void* stream);
+
 /* ---- root-mean-square norm with the residual's addition ----
  * Per row, with h = x + residual rounded to res_dtype (h = x without one):
  *     y = weight h / sqrt(mean(h^2) + eps)

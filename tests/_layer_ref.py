@@ -100,3 +100,81 @@ def held(name, got, ref, mag, dtype, slack):
     off = (got - ref).abs()
     bad = ~(off <= bar)
     assert not bad.any(), (name, int(bad.sum()), float((off / bar).nan_to_num(9e9).max()))
+
+
+def scan(x, raw, A_log, B, C, D=None, bias=None, softplus=True, state=None, cu=None, dy=None,
+         dlast=None):
+    """The selective scan token by token.  y, last and, with dy, the gradients;
+    a name with m is the magnitude that the value's terms add up to."""
+    x, raw, A_log, B, C, D, bias, state, dy, dlast = (
+        d(t) for t in (x, raw, A_log, B, C, D, bias, state, dy, dlast))
+    H, V = x.shape[2:]
+    G, K = B.shape[2:]
+    R = H // G
+    z = raw if bias is None else raw + bias
+    step = torch.nn.functional.softplus(z, threshold=1e9) if softplus else z
+    dz = torch.sigmoid(z) if softplus else torch.ones_like(z)
+    rate = -torch.exp(A_log)
+    n = len(spans(x, cu))
+    y, ym = torch.zeros_like(x), torch.zeros_like(x)
+    last = x.new_zeros(n, H, K, V)
+    lastm = torch.zeros_like(last)
+    out = {}
+    if dy is not None:
+        dx, dxm = torch.zeros_like(x), torch.zeros_like(x)
+        dstep, dstepm = torch.zeros_like(step), torch.zeros_like(step)
+        dB, dBm, dC, dCm = (torch.zeros_like(B) for _ in range(4))
+        ds, dsm = torch.zeros_like(last), torch.zeros_like(last)
+        dA, dAm = torch.zeros_like(rate), torch.zeros_like(rate)
+        group = lambda v: v.reshape(G, R, K).sum(1)  # noqa: E731
+    for row, a, b, i in spans(x, cu):
+        S = x.new_zeros(H, K, V) if state is None else state[i]
+        Sm = S.abs()
+        S_all, Sm_all = [S], [Sm]
+        for t in range(a, b):
+            e = torch.exp(rate * step[row, t])[:, None, None]
+            add = (step[row, t, :, None] * B[row, t].repeat_interleave(R, 0))[:, :, None] * x[row, t][:, None]
+            S, Sm = e * S + add, e * Sm + add.abs()
+            c = C[row, t].repeat_interleave(R, 0)
+            y[row, t] = (c[:, :, None] * S).sum(1)
+            ym[row, t] = (c.abs()[:, :, None] * Sm).sum(1)
+            if D is not None:
+                y[row, t] += D[:, None] * x[row, t]
+                ym[row, t] += (D[:, None] * x[row, t]).abs()
+            S_all.append(S)
+            Sm_all.append(Sm)
+        last[i], lastm[i] = S, Sm
+        if dy is None:
+            continue
+        P = x.new_zeros(H, K, V) if dlast is None else dlast[i]
+        Pm = P.abs()
+        for t in reversed(range(a, b)):
+            st, xt, g = step[row, t], x[row, t], dy[row, t]
+            bt, c = B[row, t].repeat_interleave(R, 0), C[row, t].repeat_interleave(R, 0)
+            S, Sm, S0, Sm0 = S_all[t - a + 1], Sm_all[t - a + 1], S_all[t - a], Sm_all[t - a]
+            dC[row, t] = group((S * g[:, None]).sum(-1))
+            dCm[row, t] = group((Sm * g.abs()[:, None]).sum(-1))
+            cg = c[:, :, None] * g[:, None]
+            P, Pm = P + cg, Pm + cg.abs()
+            px, pxm = (P * xt[:, None]).sum(-1), (Pm * xt.abs()[:, None]).sum(-1)
+            dB[row, t], dBm[row, t] = group(st[:, None] * px), group(st.abs()[:, None] * pxm)
+            u, um = (P * bt[:, :, None]).sum(1), (Pm * bt.abs()[:, :, None]).sum(1)
+            dx[row, t], dxm[row, t] = st[:, None] * u, st.abs()[:, None] * um
+            if D is not None:
+                dx[row, t] += D[:, None] * g
+                dxm[row, t] += (D[:, None] * g).abs()
+            e = torch.exp(rate * st)
+            da, dam = (P * S0).sum((1, 2)) * e, (Pm * Sm0).sum((1, 2)) * e
+            dstep[row, t] = (xt * u).sum(-1) + rate * da
+            dstepm[row, t] = (xt.abs() * um).sum(-1) + rate.abs() * dam
+            dA += rate * st * da
+            dAm += (rate * st).abs() * dam
+            P, Pm = e[:, None, None] * P, e[:, None, None] * Pm
+        ds[i], dsm[i] = P, Pm
+    out.update(y=y, ym=ym, last=last, lastm=lastm)
+    if dy is not None:
+        draw, drawm = dstep * dz, dstepm * dz
+        out.update(dx=dx, dxm=dxm, ddt=draw, ddtm=drawm, dB=dB, dBm=dBm, dC=dC, dCm=dCm, ds=ds,
+                   dsm=dsm, dA=dA, dAm=dAm, dbias=draw.sum((0, 1)), dbiasm=drawm.sum((0, 1)),
+                   dD=(dy * x).sum((0, 1, 3)), dDm=(dy * x).abs().sum((0, 1, 3)))
+    return out
