@@ -22,7 +22,8 @@ from typing import Optional
 import torch
 
 from ._layer_ops import (causal_conv1d, causal_conv1d_bwd, causal_conv1d_fwd,
-                         causal_conv1d_update, chunk_selective_scan_fwd,
+                         causal_conv1d_update, chunk_selective_scan,
+                         chunk_selective_scan_bwd, chunk_selective_scan_fwd,
                          fused_recurrent_selective_scan, rms_norm, rms_norm_bwd, rms_norm_fwd,
                          rms_norm_quant)
 from ._lib import (GDR_BF16, GDR_FP16, GDR_FP32, GdrError, Problem, check, lib)
@@ -33,7 +34,8 @@ __all__ = [
     "fused_recurrent_gated_delta_rule", "prepare_lens", "prepare_chunk_indices",
     "prepare_chunk_offsets", "unpack_states", "GdrError",
     "causal_conv1d", "causal_conv1d_fwd", "causal_conv1d_bwd", "causal_conv1d_update",
-    "chunk_selective_scan_fwd", "fused_recurrent_selective_scan",
+    "chunk_selective_scan", "chunk_selective_scan_fwd", "chunk_selective_scan_bwd",
+    "fused_recurrent_selective_scan",
     "rms_norm", "rms_norm_fwd", "rms_norm_bwd", "rms_norm_quant",
 ]
 

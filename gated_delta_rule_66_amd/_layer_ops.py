@@ -297,6 +297,73 @@ def chunk_selective_scan_fwd(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softpl
     return y, last
 
 
+def chunk_selective_scan_bwd(x, dt, A_log, B, C, dy, D=None, dt_bias=None, dt_softplus=True,
+                             dht=None, initial_state=None, cu_seqlens=None, cu_seqlens_cpu=None):
+    """The gradient of :func:`chunk_selective_scan`: ``(dx, ddt, dA_log, dB, dC,
+    dD, ddt_bias, dh0)``, ``None`` in the place of an input that is ``None``.
+    ``dht`` (optional) is the gradient of the final state."""
+    c = _Ssm(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens,
+             cu_seqlens_cpu)
+    dev = x.device
+    dy = _like("dy", dy, x.shape, (x.dtype,), dev)
+    dht = _aligned(_like("dht", dht, c.state_shape, (torch.float32,), dev))
+    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)  # noqa: E731
+    dx, ddt, dA, dB, dC, dD, db, dh0 = (new(t) for t in (x, dt, A_log, B, C, D, dt_bias,
+                                                         initial_state))
+    n = lib.gdr_ssm_bwd_workspace_size(c.ref)
+    ws = _bytes(n, dev)
+    with _guard(x):
+        check(lib.gdr_ssm_bwd(c.ref, *c.inputs(), _ptr(dy), _ptr(dht), _ptr(c.state), _ptr(dx),
+                              _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(db), _ptr(dh0),
+                              _ptr(ws), n, _stream(x)))
+    return dx, ddt, dA, dB, dC, dD, db, dh0
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state,
+                output_final_state, cu_seqlens, cu_seqlens_cpu):
+        ctx.set_materialize_grads(False)
+        if cu_seqlens is not None and cu_seqlens_cpu is None:
+            cu_seqlens_cpu = cu_seqlens.detach().to("cpu")
+        y, last = chunk_selective_scan_fwd(x, dt, A_log, B, C, D, dt_bias, dt_softplus,
+                                           initial_state, output_final_state, cu_seqlens,
+                                           cu_seqlens_cpu)
+        ctx.save_for_backward(x, dt, A_log, B, C, D, dt_bias, initial_state, cu_seqlens,
+                              cu_seqlens_cpu)
+        ctx.dt_softplus = dt_softplus
+        return y, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dlast):
+        x, dt, A_log, B, C, D, dt_bias, state, cu, cu_cpu = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        dx, ddt, dA, dB, dC, dD, db, dh0 = chunk_selective_scan_bwd(
+            x, dt, A_log, B, C, dy, D, dt_bias, ctx.dt_softplus, dlast, state, cu, cu_cpu)
+        return dx, ddt, dA, dB, dC, dD, db, None, dh0, None, None, None
+
+
+def chunk_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
+                         initial_state=None, output_final_state=False, cu_seqlens=None,
+                         cu_seqlens_cpu=None):
+    """Selective state space scan (one decay per head) with autograd: ``(y,
+    final_state)``.
+
+    Per head with state S ``[K, V]``: ``S_t = exp(-exp(A_log) dt_t) S_{t-1} + dt_t
+    B_t x_t^T`` and ``y_t = S_t^T C_t + D x_t``, ``dt_t = softplus(dt + dt_bias)`` (the
+    sum itself with ``dt_softplus=False``): the recurrence of Mamba-2 layers, the
+    gated delta rule's gate without its delta term.  x ``[B, T, H, V]``, B and C
+    ``[B, T, G, K]`` in bf16 or fp16 (slices of one projection are read in
+    place), H a multiple of G, K and V 64 or 128; dt ``[B, T, H]`` in x's dtype or
+    fp32; A_log, D, dt_bias ``[H]`` in x's dtype or fp32; states ``[N, H, K, V]``
+    fp32.  ``cu_seqlens``: packed sequences (``B == 1``), which may be empty.
+    Gradients flow to every tensor; the forward keeps only its inputs."""
+    return _SelectiveScan.apply(x, dt, A_log, B, C, D, dt_bias, bool(dt_softplus), initial_state,
+                                bool(output_final_state), cu_seqlens, cu_seqlens_cpu)
+
+
 def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
                                    initial_state=None, output_final_state=True, cu_seqlens=None,
                                    cu_seqlens_cpu=None, inplace_final_state=False):

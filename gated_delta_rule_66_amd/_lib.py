@@ -88,6 +88,7 @@ EXPORTS = [
     "gdr_conv1d_update", "gdr_rms_norm_check", "gdr_rms_norm_fwd",
     "gdr_rms_norm_bwd_workspace_size", "gdr_rms_norm_bwd",
     "gdr_ssm_check", "gdr_ssm_fwd_workspace_size", "gdr_ssm_fwd", "gdr_ssm_step",
+    "gdr_ssm_bwd_workspace_size", "gdr_ssm_bwd",
 ]
 
 
@@ -177,6 +178,8 @@ def _declare_ops(lib):
     fn("gdr_ssm_fwd_workspace_size", [SP], S)
     fn("gdr_ssm_fwd", [SP] + [P] * 11 + [S, P])
     fn("gdr_ssm_step", [SP] + [P] * 11)
+    fn("gdr_ssm_bwd_workspace_size", [SP], S)
+    fn("gdr_ssm_bwd", [SP] + [P] * 19 + [S, P])
     NP = ctypes.POINTER(NormProblem)
     fn("gdr_rms_norm_check", [NP, ctypes.c_char_p, S])
     fn("gdr_rms_norm_fwd", [NP] + [P] * 8)

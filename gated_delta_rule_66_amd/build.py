@@ -12,7 +12,8 @@ LIB = os.path.join(HERE, "libgdr.so")
 # csrc: the gated delta rule; csrc_ops: the operators around it in a layer
 SOURCES = ["csrc/gdr_api.cpp", "csrc/gdr_fwd.hip", "csrc/gdr_bwd.hip", "csrc/gdr_recurrent.hip",
            "csrc_ops/ops_api.cpp", "csrc_ops/conv1d.hip", "csrc_ops/rms_norm.hip",
-           "csrc_ops/ssm_fwd.hip"]
+           "csrc_ops/ssm_fwd.hip", "csrc_ops/ssm_bwd.hip", "csrc_ops/ssm_bwd_bf16.hip",
+           "csrc_ops/ssm_bwd_fp16.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -218,7 +218,7 @@ gdr_status gdr_ssm_check(const gdr_ssm_problem* p, char* reason, size_t reason_l
 }
 
 size_t gdr_ssm_fwd_workspace_size(const gdr_ssm_problem* p) {
-  return validate(p, nullptr, 0) == GDR_OK ? ssm_fwd_workspace(p, ssm_plan(p)) : 0;
+  return validate(p, nullptr, 0) == GDR_OK ? ssm_fwd_workspace(p, ssm_fwd_plan(p)) : 0;
 }
 
 gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
@@ -234,12 +234,39 @@ gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
                 "final_state may not be initial_state (gdr_ssm_step works in place)");
   if (misaligned(initial_state) || misaligned(final_state) || misaligned(workspace))
     return fail(GDR_ERR_ARG, nullptr, 0, "states and workspace must be 16-byte aligned");
-  const SsmPlan pl = ssm_plan(p);
+  const SsmPlan pl = ssm_fwd_plan(p);
   s = need_workspace(ssm_fwd_workspace(p, pl), workspace, workspace_bytes, "scan");
   if (s != GDR_OK) return s;
   if ((s = gdr_check_device()) != GDR_OK) return s;
   return launch_ssm_fwd(p, pl, x, dt, A_log, B, C, D, dt_bias, initial_state, y, final_state,
                         workspace, (hipStream_t)stream);
+}
+
+size_t gdr_ssm_bwd_workspace_size(const gdr_ssm_problem* p) {
+  return validate(p, nullptr, 0) == GDR_OK ? ssm_bwd_workspace(p) : 0;
+}
+
+gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
+                       const void* B, const void* C, const void* D, const void* dt_bias,
+                       const void* dy, const float* dfinal_state, const float* initial_state,
+                       void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
+                       void* ddt_bias, float* dinitial_state, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (!x || !dt || !A_log || !B || !C || !dy || !dx || !ddt || !dA_log || !dB || !dC)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required scan-gradient pointer is NULL");
+  if ((dD && !D) || (ddt_bias && !dt_bias) || (dinitial_state && !initial_state))
+    return fail(GDR_ERR_ARG, nullptr, 0, "dD, ddt_bias and dinitial_state need their inputs");
+  if (misaligned(initial_state) || misaligned(dfinal_state) || misaligned(dinitial_state) ||
+      misaligned(workspace))
+    return fail(GDR_ERR_ARG, nullptr, 0, "states and workspace must be 16-byte aligned");
+  s = need_workspace(ssm_bwd_workspace(p), workspace, workspace_bytes, "scan-gradient");
+  if (s != GDR_OK) return s;
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_ssm_bwd(p, x, dt, A_log, B, C, D, dt_bias, dy, dfinal_state, initial_state, dx, ddt,
+                        dA_log, dB, dC, dD, ddt_bias, dinitial_state, workspace,
+                        (hipStream_t)stream);
 }
 
 gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,

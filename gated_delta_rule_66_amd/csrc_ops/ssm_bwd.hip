@@ -1,0 +1,236 @@
+// ssm_bwd.hip -- the selective scan's gradient: the step sizes' part, the sums
+// over segments and workgroups, and the launches (the walks: ssm_bwd.h).
+#include <algorithm>
+
+#include "ssm_bwd.h"
+
+namespace gdr {
+
+namespace {
+
+// dg is the suffix sum of row - dt q along a segment plus what spans its end;
+// from it the raw step sizes' gradient and the segment's shares of dA_log and
+// ddt_bias.  One workgroup per (segment, head), 1024 tokens at a time from
+// the end, four per thread.
+template <typename DT>
+__global__ __launch_bounds__(256) void ssm_dt_kernel(SsmGradArgs ga, DT* ddt, float* part_dA,
+                                                     float* part_db) {
+  __shared__ float tot[4], red[2][4];
+  const SsmArgs& a = ga.f;
+  const int id = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const Segment sg = segment_of(a, id);
+  const int64_t out = (int64_t)id * a.H + h;
+  if (sg.count == 0) {
+    if (threadIdx.x == 0) part_dA[out] = part_db[out] = 0.f;
+    return;
+  }
+  const int l = lane_id(), w = threadIdx.x >> 6;
+  const float rate = -expf(load_scalar(a.A_log, h, a.p_dtype));
+  const float bias = param(a.dt_bias, h, a.p_dtype);
+  const float* row = ga.row + (int64_t)h * ga.tokens;
+  const float* q = ga.q + (int64_t)h * ga.tokens;
+  float carry = ga.span[out], dA = 0.f, db = 0.f;
+  const int64_t len = sg.t1 - sg.t0;
+  for (int64_t b = (len - 1) / 1024; b >= 0; --b) {
+    const int64_t t0 = sg.t0 + 1024 * b + 4 * threadIdx.x;
+    float raw[4], step[4], qv[4], sum[4];
+#pragma unroll
+    for (int e = 3; e >= 0; --e) {
+      const bool live = t0 + e < sg.t1;
+      raw[e] = live ? load_scalar(a.dt, (t0 + e) * a.H + h, a.dt_dtype) : 0.f;
+      step[e] = live ? ssm_step_size(raw[e], bias, a.softplus) : 0.f;
+      qv[e] = live ? q[t0 + e] : 0.f;
+      sum[e] = (live ? row[t0 + e] - step[e] * qv[e] : 0.f) + (e < 3 ? sum[e < 3 ? e + 1 : 3] : 0.f);
+    }
+    const float above = wave_suffix_excl(sum[0]);
+    if (l == 0) tot[w] = above + sum[0];
+    __syncthreads();
+    float later = carry, all = 0.f;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      if (i > w) later += tot[i];
+      all += tot[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (t0 + e < sg.t1) {
+        const float dg = later + above + sum[e];
+        float d = rate * dg + qv[e];
+        if (a.softplus) d *= sigmoid(raw[e] + bias);
+        ddt[(t0 + e) * a.H + h] = from_f<DT>(d);
+        dA += dg * rate * step[e];
+        db += d;
+      }
+    }
+    carry += all;
+    __syncthreads();
+  }
+  dA = wave_sum(dA);
+  db = wave_sum(db);
+  if (l == 0) {
+    red[0][w] = dA;
+    red[1][w] = db;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    part_dA[out] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+    part_db[out] = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  }
+}
+
+// The parameters' gradients over all segments: one workgroup per head and
+// parameter (A_log, dt_bias, D).
+__global__ __launch_bounds__(256) void ssm_param_kernel(const float* part, int64_t stride, int nids,
+                                                        int H, void* dA, void* db, void* dD,
+                                                        int dtype) {
+  __shared__ float red[4];
+  const int which = blockIdx.x / H, h = blockIdx.x % H;
+  void* out = which == 0 ? dA : which == 1 ? db : dD;
+  if (!out) return;
+  const float* p = part + which * stride + h;
+  float v = 0.f;
+  for (int64_t i = threadIdx.x; i < nids; i += 256) v += p[i * H];
+  v = wave_sum(v);
+  if (lane_id() == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) store_scalar(out, h, dtype, (red[0] + red[1]) + (red[2] + red[3]));
+}
+
+// dB and dC over a group's workgroups, in order, four values per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void ssm_group_kernel(const float* pB, const float* pC, int slots,
+                                                        int64_t n, T* dB, T* dC) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const bool second = i >= n;
+  const int64_t k = second ? i - n : i;
+  if (k >= n) return;
+  const float* p = (second ? pC : pB) + k;
+  f32x4 v = *reinterpret_cast<const f32x4*>(p);
+  for (int s = 1; s < slots; ++s) v += *reinterpret_cast<const f32x4*>(p + s * n);
+  struct __attribute__((packed, aligned(sizeof(T)))) Raw {
+    uint32_t u[2];
+  };
+  typename VT<T>::x4 o{from_f<T>(v[0]), from_f<T>(v[1]), from_f<T>(v[2]), from_f<T>(v[3])};
+  *reinterpret_cast<Raw*>((second ? dC : dB) + k) = __builtin_bit_cast(Raw, o);
+}
+
+// Heads per workgroup (those of one group share its B, C and C B^T and add
+// their dB, dC in registers), workgroups per group and the cut.
+struct GradPlan {
+  int heads, slots;
+  SsmPlan cut;
+};
+GradPlan grad_plan(const gdr_ssm_problem* p) {
+  GradPlan g;
+  const int R = p->H / p->G;
+  g.heads = R >= 2 ? 2 : 1;
+  g.slots = (R + g.heads - 1) / g.heads;
+  g.cut = ssm_plan(p, (int64_t)p->G * g.slots, p->V == 64 ? 512 : 256);
+  return g;
+}
+
+// Byte offsets in the workspace.
+struct GradLayout {
+  size_t state, grad, sdec, gdec, row, q, span, params, pB, pC, total;
+};
+GradLayout layout(const gdr_ssm_problem* p, const GradPlan& g) {
+  GradLayout o{};
+  const size_t tokens = (size_t)p->B * p->T, ids = (size_t)g.cut.nids * p->H;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  if (g.cut.split) {
+    o.state = take(ids * p->K * p->V * sizeof(float));
+    o.grad = take(ids * p->K * p->V * sizeof(float));
+    o.sdec = take(ids * sizeof(float));
+    o.gdec = take(ids * sizeof(float));
+  }
+  o.row = take(tokens * p->H * sizeof(float));
+  o.q = take(tokens * p->H * sizeof(float));
+  o.span = take(ids * sizeof(float));
+  o.params = take(3 * ids * sizeof(float));
+  if (g.slots > 1) {
+    o.pB = take(tokens * p->G * p->K * g.slots * sizeof(float));
+    o.pC = take(tokens * p->G * p->K * g.slots * sizeof(float));
+  }
+  o.total = at;
+  return o;
+}
+
+}  // namespace
+
+size_t ssm_bwd_workspace(const gdr_ssm_problem* p) { return layout(p, grad_plan(p)).total; }
+
+gdr_status launch_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt,
+                          const void* A_log, const void* B, const void* C, const void* D,
+                          const void* dt_bias, const void* dy, const float* dht, const float* h0,
+                          void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
+                          void* ddt_bias, float* dh0, void* ws, hipStream_t st) {
+  const GradPlan g = grad_plan(p);
+  const GradLayout o = layout(p, g);
+  char* base = reinterpret_cast<char*>(ws);
+  auto f32 = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
+  SsmGradArgs a{};
+  a.f = ssm_args(p, g.cut);
+  a.f.x = x; a.f.dt = dt; a.f.A_log = A_log; a.f.B = B; a.f.C = C; a.f.D = D; a.f.dt_bias = dt_bias;
+  a.f.h0 = h0;
+  if (g.cut.split) {
+    a.f.seg_state = f32(o.state);
+    a.f.seg_decay = f32(o.sdec);
+    launch_ssm_states(p, a.f, false, st);
+    SsmArgs r = a.f;
+    r.x = dy; r.xs = (int64_t)p->H * p->V;
+    r.B = C; r.bs = p->c_stride;
+    r.h0 = dht;
+    r.seg_state = f32(o.grad);
+    r.seg_decay = f32(o.gdec);
+    launch_ssm_states(p, r, true, st);
+    a.seg_grad = r.seg_state;
+  }
+  const int64_t ids = (int64_t)g.cut.nids * p->H;
+  float* params = f32(o.params);
+  a.dy = dy; a.dht = dht; a.dx = dx; a.dB = dB; a.dC = dC; a.dh0 = dh0;
+  if (g.slots > 1) {
+    a.part_dB = f32(o.pB);
+    a.part_dC = f32(o.pC);
+  }
+  a.row = f32(o.row);
+  a.q = f32(o.q);
+  a.span = f32(o.span);
+  a.part_dD = params + 2 * ids;
+  a.slots = g.slots;
+  a.tokens = (int64_t)p->B * p->T;
+  const unsigned grid = (unsigned)((int64_t)g.cut.nids * p->G * g.slots);
+  ssm_by_shape(p, [&](auto t, auto k, auto v) {
+    using T = decltype(t);
+    constexpr int K = k.value, V = v.value;
+    if (g.heads == 2) {
+      launch_ssm_grad<T, K, V, 2, false>(a, grid, st);
+      launch_ssm_grad<T, K, V, 2, true>(a, grid, st);
+    } else {
+      launch_ssm_grad<T, K, V, 1, false>(a, grid, st);
+      launch_ssm_grad<T, K, V, 1, true>(a, grid, st);
+    }
+    const dim3 dgrid((unsigned)ids);
+    if (p->dt_dtype == GDR_FP32)
+      GDR_LAUNCH("ssm_dt", (ssm_dt_kernel<float>), dgrid, dim3(256), st, a,
+                 reinterpret_cast<float*>(ddt), params, params + ids);
+    else
+      GDR_LAUNCH("ssm_dt", (ssm_dt_kernel<T>), dgrid, dim3(256), st, a, reinterpret_cast<T*>(ddt),
+                 params, params + ids);
+    if (g.slots > 1) {
+      const int64_t n = a.tokens * p->G * K;
+      GDR_LAUNCH("ssm_group", (ssm_group_kernel<T>), dim3((unsigned)((2 * n / 4 + 255) / 256)),
+                 dim3(256), st, a.part_dB, a.part_dC, g.slots, n, reinterpret_cast<T*>(dB),
+                 reinterpret_cast<T*>(dC));
+    }
+  });
+  GDR_LAUNCH("ssm_param", ssm_param_kernel, dim3(3 * p->H), dim3(256), st, params, ids, g.cut.nids,
+             p->H, dA_log, ddt_bias, dD, (int)p->p_dtype);
+  return launch_status("ssm_bwd");
+}
+
+}  // namespace gdr

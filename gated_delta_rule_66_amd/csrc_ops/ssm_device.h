@@ -13,6 +13,8 @@
 // parallel and added up with one scalar decay each.
 #pragma once
 
+#include <type_traits>
+
 #include "ops_device.h"
 #include "ops_internal.h"
 
@@ -198,6 +200,25 @@ __device__ __forceinline__ int state_k(int nt, int e) {
 template <int V>
 __device__ __forceinline__ int state_v(int w, int pt) {
   return w * (V / 4) + 16 * pt + (lane_id() & 15);
+}
+
+// Host side: the problem's arguments, its element type and sizes as types.
+SsmArgs ssm_args(const gdr_ssm_problem* p, const SsmPlan& pl);
+void launch_ssm_states(const gdr_ssm_problem* p, const SsmArgs& a, bool grad, hipStream_t st);
+
+template <typename F>
+inline void ssm_by_shape(const gdr_ssm_problem* p, F f) {
+  auto type = [&](auto t) {
+    using T = decltype(t);
+    auto c64 = std::integral_constant<int, 64>();
+    auto c128 = std::integral_constant<int, 128>();
+    if (p->K == 64 && p->V == 64) f(T(), c64, c64);
+    else if (p->K == 64) f(T(), c64, c128);
+    else if (p->V == 64) f(T(), c128, c64);
+    else f(T(), c128, c128);
+  };
+  if (p->in_dtype == GDR_BF16) type(__bf16());
+  else type(_Float16());
 }
 
 }  // namespace gdr

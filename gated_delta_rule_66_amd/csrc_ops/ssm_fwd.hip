@@ -18,8 +18,8 @@ namespace {
 
 constexpr int kNT = 256;
 
-// The ten 16 x 16 tiles on or below the diagonal of a 64 x 64 matrix over four
-// waves (3, 3, 2, 2): 4 bits each, row block * 4 + column block.
+// The ten tiles on or below the diagonal of a 64 x 64 matrix over four waves
+// (3, 3, 2, 2): 4 bits each, row block * 4 + column block.
 constexpr uint64_t kTiles = 0xC | (0xDull << 4) | (0x0ull << 8) |        // wave 0
                             (0xEull << 12) | (0xFull << 16) | (0x5ull << 20) |  // wave 1
                             (0x8ull << 24) | (0x9ull << 28) |            // wave 2
@@ -37,21 +37,27 @@ struct OutSmem {
   float gam[64], eg[64], wt[64], dts[64];
 };
 
-// OUT: the segment's outputs from its start state; else what it adds to the
-// state.  Four waves, each with V / 4 state columns in MFMA accumulators.
-template <typename T, int K, int V, bool OUT>
+// kOut: the segment's outputs from its start state.  kState: what it adds to
+// the state.  kGrad: what it adds to the state's gradient at its start, the
+// same with dy and C for x and B (the caller passes them so), e^gamma for the
+// weights, and the chunks from the last to the first.  Four waves, each with
+// V / 4 state columns in MFMA accumulators.
+enum { kOut, kState, kGrad };
+template <typename T, int K, int V, int MODE>
 __global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
   typedef typename VT<T>::x8 x8;
   typedef OutSmem<T, K, V> Smem;
   constexpr int LK = Smem::LK, LV = Smem::LV, LM = Smem::LM;
   constexpr int NT = K / 16, PT = V / 64;
+  constexpr bool OUT = MODE == kOut;
   constexpr bool kScaled = !__is_same(T, __bf16);
   __shared__ Smem s;
   const int L = xcd_order(blockIdx.x, gridDim.x);
   const int id = L / a.H, h = L % a.H, grp_h = h / (a.H / a.G);
   const Segment sg = segment_of(a, id);
   if (sg.count == 0) return;
-  if (!OUT && sg.j + 1 >= sg.count) return;
+  if (MODE == kState && sg.j + 1 >= sg.count) return;
+  if (MODE == kGrad && sg.j == 0) return;
   const int w = threadIdx.x >> 6, l = lane_id(), g4 = l >> 4, col = l & 15;
 
   const T* xg = reinterpret_cast<const T*>(a.x) + (int64_t)h * V;
@@ -98,9 +104,12 @@ __global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
     if (OUT) rc.load(cg + t * a.cs, a.cs, rows);
     raw = l < rows ? load_scalar(a.dt, (t + l) * a.H + h, a.dt_dtype) : 0.f;
   };
-  if (sg.t0 < sg.t1) request(sg.t0);
+  const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
+  auto token = [&](int c) { return sg.t0 + 64ll * (MODE == kGrad ? nch - 1 - c : c); };
+  if (nch > 0) request(token(0));
 
-  for (int64_t t = sg.t0; t < sg.t1; t += 64) {
+  for (int c = 0; c < nch; ++c) {
+    const int64_t t = token(c);
     const int rows = (int)min((int64_t)64, sg.t1 - t);
     // the chunk's gate, one token per lane (every wave forms it; the first
     // one stores it); tokens past the end have step size 0
@@ -112,14 +121,14 @@ __global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
     if (w == 0) {
       s.gam[l] = gam;
       s.eg[l] = __expf(gam);
-      s.wt[l] = step * __expf(suf);
+      s.wt[l] = MODE == kGrad ? __expf(gam) : step * __expf(suf);
       s.dts[l] = step;
     }
     rx.store(s.X, LV);
     rb.store(s.B, LK);
     if (OUT) rc.store(s.C, LK);
     __syncthreads();
-    if (t + 64 < sg.t1) request(t + 64);
+    if (c + 1 < nch) request(token(c + 1));
 
     f32x4 acc[PT][4];
     if (OUT) {
@@ -272,10 +281,12 @@ __global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
   }
 }
 
-// Segment j's end state over what it added: E_j = e^{decay_j} E_{j-1} + add_j,
-// E_{-1} the initial state; one thread per four state elements walks the
-// sequence's segments (all but the last).
-template <int K, int V>
+// Segment j's end state over what it added, E_j = e^{decay_j} E_{j-1} +
+// add_j with E_{-1} the initial state, for all but the last segment; REV: the
+// state's gradient at segment j's start, F_j = e^{decay_j} F_{j+1} + add_j
+// with F past the last segment the final state's gradient, for all but the
+// first.  One thread walks four state elements along the sequence.
+template <int K, int V, bool REV>
 __global__ __launch_bounds__(256) void ssm_combine_kernel(SsmArgs a) {
   constexpr int parts = K * V / 1024;
   const int part = blockIdx.x % parts;
@@ -294,22 +305,23 @@ __global__ __launch_bounds__(256) void ssm_combine_kernel(SsmArgs a) {
   const int at = (part * 256 + threadIdx.x) * 4;      // element in the register order
   f32x4 E = zero4();
   if (a.h0) {
-    // register order: [wave][pt][nt][lane][e]
-    constexpr int NT = K / 16, PT = V / 64;
-    const int lane = (at >> 2) & 63, q = at >> 8, nt = q % NT, pt = (q / NT) % PT, w = q / (NT * PT);
-    const int v = w * (V / 4) + 16 * pt + (lane & 15);
+    // register order: [16-column tile][nt][lane][e]
+    constexpr int NT = K / 16;
+    const int lane = (at >> 2) & 63, q = at >> 8, nt = q % NT, ct = q / NT;
+    const int v = 16 * ct + (lane & 15);
     const int k = 32 * (nt >> 1) + 8 * (lane >> 4) + 4 * (nt & 1);
 #pragma unroll
     for (int e = 0; e < 4; ++e) E[e] = a.h0[((int64_t)n * a.H + h) * K * V + (int64_t)(k + e) * V + v];
   }
-  const int64_t step = (int64_t)a.H * K * V;
-  float* p = a.seg_state + ((int64_t)id0 * a.H + h) * K * V + at;
-  const float* dec = a.seg_decay + (int64_t)id0 * a.H + h;
+  const int first = REV ? id0 + m - 1 : id0;
+  const int64_t dir = REV ? -1 : 1, step = dir * a.H * K * V;
+  float* p = a.seg_state + ((int64_t)first * a.H + h) * K * V + at;
+  const float* dec = a.seg_decay + (int64_t)first * a.H + h;
   f32x4 next = *reinterpret_cast<const f32x4*>(p);
   for (int j = 0; j + 1 < m; ++j) {
     const f32x4 add = next;
     if (j + 2 < m) next = *reinterpret_cast<const f32x4*>(p + step);
-    E = E * __expf(dec[(int64_t)j * a.H]) + add;
+    E = E * __expf(dec[dir * j * a.H]) + add;
     *reinterpret_cast<f32x4*>(p) = E;
     p += step;
   }
@@ -381,7 +393,9 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
   }
 }
 
-SsmArgs args_of(const gdr_ssm_problem* p, const SsmPlan& pl) {
+}  // namespace
+
+SsmArgs ssm_args(const gdr_ssm_problem* p, const SsmPlan& pl) {
   SsmArgs a{};
   a.cu = p->cu_seqlens_dev;
   a.xs = p->x_stride;
@@ -399,13 +413,11 @@ SsmArgs args_of(const gdr_ssm_problem* p, const SsmPlan& pl) {
   return a;
 }
 
-}  // namespace
-
-// How sequences are cut.  Uncut, a launch takes the longest sequence's chunks;
-// cut, every chunk's x and B are read twice and two launches are added, worth
-// about four chunks.  `slots` workgroups run at once.
-SsmPlan ssm_plan(const gdr_ssm_problem* p) {
-  const int64_t slots = p->V == 64 ? 768 : 512;
+// How sequences are cut for a launch with `per_seg` workgroups for each
+// segment, of which `slots` run at once.  Uncut, it takes the longest
+// sequence's chunks; cut, every chunk's x and B are read once more and two
+// launches are added, worth about four chunks.
+SsmPlan ssm_plan(const gdr_ssm_problem* p, int64_t per_seg, int64_t slots) {
   int64_t chunks = 0, longest = 0, tokens = 0;
   for (int n = 0; n < (p->cu_seqlens_host ? p->N : 1); ++n) {
     const int64_t len = p->cu_seqlens_host
@@ -416,7 +428,7 @@ SsmPlan ssm_plan(const gdr_ssm_problem* p) {
     tokens += len;
   }
   if (!p->cu_seqlens_host) chunks *= p->B;
-  const int64_t ideal = std::max<int64_t>(4, (chunks * p->H + slots - 1) / slots);
+  const int64_t ideal = std::max<int64_t>(4, (chunks * per_seg + slots - 1) / slots);
   SsmPlan pl;
   pl.split = 2 * longest > 3 * ideal + 8;
   int64_t sc = pl.split ? ideal : std::max<int64_t>(1, longest);
@@ -426,32 +438,39 @@ SsmPlan ssm_plan(const gdr_ssm_problem* p) {
   return pl;
 }
 
+SsmPlan ssm_fwd_plan(const gdr_ssm_problem* p) {
+  return ssm_plan(p, p->H, p->V == 64 ? 768 : 512);
+}
+
 size_t ssm_fwd_workspace(const gdr_ssm_problem* p, const SsmPlan& pl) {
   if (!pl.split) return 0;
   return align256((size_t)pl.nids * p->H * p->K * p->V * sizeof(float)) +
          align256((size_t)pl.nids * p->H * sizeof(float));
 }
 
-template <typename F>
-static void by_shape(const gdr_ssm_problem* p, F f) {
-  auto type = [&](auto t) {
+// Every segment's end states (grad: the gradients at its start) in
+// a.seg_state; for the gradient a holds dy, C and dht for x, B and h0.
+void launch_ssm_states(const gdr_ssm_problem* p, const SsmArgs& a, bool grad, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.nids * p->H));
+  ssm_by_shape(p, [&](auto t, auto k, auto v) {
     using T = decltype(t);
-    auto c64 = std::integral_constant<int, 64>();
-    auto c128 = std::integral_constant<int, 128>();
-    if (p->K == 64 && p->V == 64) f(T(), c64, c64);
-    else if (p->K == 64) f(T(), c64, c128);
-    else if (p->V == 64) f(T(), c128, c64);
-    else f(T(), c128, c128);
-  };
-  if (p->in_dtype == GDR_BF16) type(__bf16());
-  else type(_Float16());
+    constexpr int K = k.value, V = v.value;
+    const dim3 cgrid((unsigned)((int64_t)p->N * p->H * (K * V / 1024)));
+    if (grad) {
+      GDR_LAUNCH("ssm_state_grad", (ssm_walk_kernel<T, K, V, kGrad>), grid, dim3(kNT), st, a);
+      GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, true>), cgrid, dim3(256), st, a);
+    } else {
+      GDR_LAUNCH("ssm_state", (ssm_walk_kernel<T, K, V, kState>), grid, dim3(kNT), st, a);
+      GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, false>), cgrid, dim3(256), st, a);
+    }
+  });
 }
 
 gdr_status launch_ssm_fwd(const gdr_ssm_problem* p, const SsmPlan& pl, const void* x,
                           const void* dt, const void* A_log, const void* B, const void* C,
                           const void* D, const void* dt_bias, const float* h0, void* y, float* ht,
                           void* ws, hipStream_t st) {
-  SsmArgs a = args_of(p, pl);
+  SsmArgs a = ssm_args(p, pl);
   a.x = x; a.dt = dt; a.A_log = A_log; a.B = B; a.C = C; a.D = D; a.dt_bias = dt_bias;
   a.h0 = h0; a.y = y; a.ht = ht;
   if (pl.split) {
@@ -459,16 +478,11 @@ gdr_status launch_ssm_fwd(const gdr_ssm_problem* p, const SsmPlan& pl, const voi
     a.seg_decay = reinterpret_cast<float*>(
         reinterpret_cast<char*>(ws) + align256((size_t)pl.nids * p->H * p->K * p->V * sizeof(float)));
   }
+  if (pl.split) launch_ssm_states(p, a, false, st);
   const dim3 grid((unsigned)((int64_t)pl.nids * p->H));
-  by_shape(p, [&](auto t, auto k, auto v) {
-    using T = decltype(t);
-    constexpr int K = k.value, V = v.value;
-    if (pl.split) {
-      GDR_LAUNCH("ssm_state", (ssm_walk_kernel<T, K, V, false>), grid, dim3(kNT), st, a);
-      GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V>),
-                 dim3((unsigned)((int64_t)p->N * p->H * (K * V / 1024))), dim3(256), st, a);
-    }
-    GDR_LAUNCH("ssm_out", (ssm_walk_kernel<T, K, V, true>), grid, dim3(kNT), st, a);
+  ssm_by_shape(p, [&](auto t, auto k, auto v) {
+    GDR_LAUNCH("ssm_out", (ssm_walk_kernel<decltype(t), k.value, v.value, kOut>), grid, dim3(kNT),
+               st, a);
   });
   return launch_status("ssm_fwd");
 }
@@ -477,10 +491,10 @@ gdr_status launch_ssm_step(const gdr_ssm_problem* p, const void* x, const void* 
                            const void* A_log, const void* B, const void* C, const void* D,
                            const void* dt_bias, const float* h0, void* y, float* ht,
                            hipStream_t st) {
-  SsmArgs a = args_of(p, SsmPlan{64, 0, false});
+  SsmArgs a = ssm_args(p, SsmPlan{64, 0, false});
   a.x = x; a.dt = dt; a.A_log = A_log; a.B = B; a.C = C; a.D = D; a.dt_bias = dt_bias;
   a.h0 = h0; a.y = y; a.ht = ht;
-  by_shape(p, [&](auto t, auto k, auto v) {
+  ssm_by_shape(p, [&](auto t, auto k, auto v) {
     constexpr int K = k.value, V = v.value;
     GDR_LAUNCH("ssm_step", (ssm_step_kernel<decltype(t), K, V>),
                dim3((unsigned)((int64_t)p->N * p->H * (V / 32))), dim3(256), st, a);

@@ -494,6 +494,20 @@ gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
                        const float* initial_state, void* y, float* final_state, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* The gradient of the forward (everything it needs of it is recomputed).
+ *   in : the forward's inputs; dy; dfinal_state (nullable = zero)
+ *   out: dx, ddt (with respect to the raw step sizes), dA_log, dB, dC; dD,
+ *        ddt_bias, dinitial_state (each nullable = not written, and only with
+ *        its input).  Parameters' gradients are in p_dtype, sums over all
+ *        tokens in a fixed order. */
+size_t gdr_ssm_bwd_workspace_size(const gdr_ssm_problem* p);
+gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
+                       const void* B, const void* C, const void* D, const void* dt_bias,
+                       const void* dy, const float* dfinal_state, const float* initial_state,
+                       void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
+                       void* ddt_bias, float* dinitial_state, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Token by token for decode steps: the same y and final_state, the state read
  * once and written once; final_state may be initial_state (updated in
  * place). */

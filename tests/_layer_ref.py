@@ -125,7 +125,7 @@ def scan(x, raw, A_log, B, C, D=None, bias=None, softplus=True, state=None, cu=N
         dstep, dstepm = torch.zeros_like(step), torch.zeros_like(step)
         dB, dBm, dC, dCm = (torch.zeros_like(B) for _ in range(4))
         ds, dsm = torch.zeros_like(last), torch.zeros_like(last)
-        dA, dAm = torch.zeros_like(rate), torch.zeros_like(rate)
+        dA, sfxm = torch.zeros_like(rate), torch.zeros_like(step)
         group = lambda v: v.reshape(G, R, K).sum(1)  # noqa: E731
     for row, a, b, i in spans(x, cu):
         S = x.new_zeros(H, K, V) if state is None else state[i]
@@ -148,6 +148,7 @@ def scan(x, raw, A_log, B, C, D=None, bias=None, softplus=True, state=None, cu=N
             continue
         P = x.new_zeros(H, K, V) if dlast is None else dlast[i]
         Pm = P.abs()
+        later = torch.zeros_like(rate)     # what the suffix sum behind dg has added up
         for t in reversed(range(a, b)):
             st, xt, g = step[row, t], x[row, t], dy[row, t]
             bt, c = B[row, t].repeat_interleave(R, 0), C[row, t].repeat_interleave(R, 0)
@@ -165,16 +166,17 @@ def scan(x, raw, A_log, B, C, D=None, bias=None, softplus=True, state=None, cu=N
                 dxm[row, t] += (D[:, None] * g).abs()
             e = torch.exp(rate * st)
             da, dam = (P * S0).sum((1, 2)) * e, (Pm * Sm0).sum((1, 2)) * e
+            later = later + (Sm * cg.abs()).sum((1, 2)) + st.abs() * (xt.abs() * um).sum(-1)
+            sfxm[row, t] = dam + later
             dstep[row, t] = (xt * u).sum(-1) + rate * da
-            dstepm[row, t] = (xt.abs() * um).sum(-1) + rate.abs() * dam
+            dstepm[row, t] = (xt.abs() * um).sum(-1) + rate.abs() * sfxm[row, t]
             dA += rate * st * da
-            dAm += (rate * st).abs() * dam
             P, Pm = e[:, None, None] * P, e[:, None, None] * Pm
         ds[i], dsm[i] = P, Pm
     out.update(y=y, ym=ym, last=last, lastm=lastm)
     if dy is not None:
         draw, drawm = dstep * dz, dstepm * dz
         out.update(dx=dx, dxm=dxm, ddt=draw, ddtm=drawm, dB=dB, dBm=dBm, dC=dC, dCm=dCm, ds=ds,
-                   dsm=dsm, dA=dA, dAm=dAm, dbias=draw.sum((0, 1)), dbiasm=drawm.sum((0, 1)),
+                   dsm=dsm, dA=dA, dAm=(rate.abs() * step.abs() * sfxm).sum((0, 1)), dbias=draw.sum((0, 1)), dbiasm=drawm.sum((0, 1)),
                    dD=(dy * x).sum((0, 1, 3)), dDm=(dy * x).abs().sum((0, 1, 3)))
     return out

@@ -10,7 +10,12 @@ of earlier chunks carries: the reference returns those magnitudes.  Outputs
 (16 bits): one rounding of the output; the decayed scores and the chunk's
 start state are rounded to the type as operands, half a step each, relative to
 the magnitudes of the products: so half a step of the value and a little over
-one half step of the sum of magnitudes."""
+one half step of the sum of magnitudes.  The gradients of x, B and C round one
+operand in the same way.  The step sizes' gradient is a suffix sum of fp32
+values, each within 2^-16 of its terms' magnitudes (pairs to 2^-18, exponentials
+and sums as above), so its bar is 2^-16 of the magnitudes of everything that is
+summed behind a token; dA_log and ddt_bias add those bars up.  dD sums exact
+products in fp32: 2^-17."""
 import pytest
 import torch
 
@@ -100,6 +105,113 @@ def test_token_by_token(name):
         y2, last2 = gdr.fused_recurrent_selective_scan(*args(g), sp, st, inplace_final_state=True, **kw)
         assert last2.data_ptr() == st.data_ptr()
         assert torch.equal(y, y2) and torch.equal(last, last2)
+
+
+GRADS = ("dx", "ddt", "dA", "dB", "dC", "dD", "dbias", "ds")
+
+
+def grad_slack(name, dtype):
+    if name in ("dx", "dB", "dC"):
+        return 1.25 * ref.half_step(dtype)
+    return {"ds": STATE_SLACK, "dD": 2.0 ** -17}.get(name, 2.0 ** -16)
+
+
+MORE = {
+    "shared_by_3": ((1, 130, 6, 2, 64, 64, BF), {}),
+    "shared_by_8": ((2, 77, 8, 1, 128, 64, HF), dict(p_dtype=HF)),
+    "cut_shared": ((1, 1500, 4, 1, 64, 64, BF), dict(lens=[700, 1, 0, 799])),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES) + list(MORE))
+def test_gradients(name):
+    shape, kw = {**CASES, **MORE}[name]
+    t = make(*shape, **kw)
+    sp = kw.get("softplus", True)
+    g = dev(t)
+    names = [n for n, k in zip(GRADS, ("x", "dt", "A_log", "B", "C", "D", "dt_bias", "state"))
+             if g[k] is not None]
+    leaves = [g[k].requires_grad_(True) for k in ("x", "dt", "A_log", "B", "C", "D", "dt_bias", "state")
+              if g[k] is not None]
+    y, last = gdr.chunk_selective_scan(*args(g), sp, g["state"], True, g["cu"], t["cu"])
+    got = torch.autograd.grad([y, last], leaves, [g["dy"], g["dlast"]])
+    torch.cuda.synchronize()
+    r = ref.scan(t["x"], t["dt"], t["A_log"], t["B"], t["C"], t["D"], t["dt_bias"], sp, t["state"],
+                 t["cu"], t["dy"], t["dlast"])
+    check_forward(t, y.detach(), last.detach(), r)
+    for n, v in zip(names, got):
+        err = (ref.d(v) - r[n]).norm() / r[n].norm()
+        print(name, n, "%.2e" % float(err), flush=True)
+        ref.held(n, v, r[n], r[n + "m"], v.dtype, grad_slack(n, t["x"].dtype))
+    # without the final state's gradient, and the same bits twice
+    a1 = gdr.chunk_selective_scan_bwd(*args(g)[:5], g["dy"], g["D"], g["dt_bias"], sp, None, g["state"],
+                                      g["cu"], t["cu"])
+    a2 = gdr.chunk_selective_scan_bwd(*args(g)[:5], g["dy"], g["D"], g["dt_bias"], sp,
+                                      torch.zeros_like(g["dlast"]), g["state"], g["cu"], t["cu"])
+    for u, v in zip(a1, a2):
+        assert (u is None) == (v is None) and (u is None or torch.equal(u, v))
+
+
+def test_gradient_against_differences():
+    """Random directions, dt, its bias, A_log, D and the state in fp32; x, B and
+    C move on their 16-bit grid, so their differences are taken against the
+    exact step.  The outputs round to 2^-9 of themselves, which a step of 2^-4
+    turns into 2^-5 per output, random over 8,000 outputs; the curvature adds
+    h^2 / 6: 5 % of the directional derivative's own root of squares."""
+    t = dev(make(2, 70, 2, 1, 64, 64, HF, dt_dtype=F32, seed=3))
+    keys = ("x", "dt", "A_log", "B", "C", "D", "dt_bias", "state")
+    got = gdr.chunk_selective_scan_bwd(*args(t)[:5], t["dy"], t["D"], t["dt_bias"], True, t["dlast"],
+                                       t["state"])
+    gen = torch.Generator().manual_seed(2)
+    h = 2.0 ** -4
+    for k, g in zip(keys, got):
+        v = torch.randn(t[k].shape, generator=gen).cuda()
+
+        def value(s):
+            q = dict(t)
+            q[k] = (t[k].float() + s * v).to(t[k].dtype)
+            y, last = gdr.chunk_selective_scan_fwd(*args(q), True, q["state"])
+            return (y.double() * t["dy"]).sum() + (last.double() * t["dlast"]).sum(), q[k].double()
+
+        (up, a), (down, b) = value(h), value(-h)
+        want = (g.double() * (a - b)).sum()
+        scale = (g.double() * (a - b)).square().sum().sqrt()
+        assert abs(up - down - want) <= 0.05 * scale + 2e-3 * abs(want), (k, float(up - down), float(want))
+
+
+def test_captured_and_replayed():
+    """A training step in a graph, replayed with eager work in between; two
+    graphs with workspaces of their own."""
+    t = dev(make(1, 1500, 4, 2, 64, 64, BF, lens=[900, 0, 600]))
+    cu = t["cu"].cpu()
+
+    def step():
+        y, last = gdr.chunk_selective_scan_fwd(*args(t), True, t["state"], True, t["cu"], cu)
+        g = gdr.chunk_selective_scan_bwd(*args(t)[:5], t["dy"], t["D"], t["dt_bias"], True, t["dlast"],
+                                         t["state"], t["cu"], cu)
+        return (y, last) + g
+
+    want = step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out))
+    for _ in range(3):
+        for graph, out in graphs:
+            for o in out:
+                o.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, out in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+        step()
 
 
 def test_steps_continue_a_prompt():
