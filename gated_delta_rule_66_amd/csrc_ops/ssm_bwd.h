@@ -65,48 +65,32 @@ namespace {
 
 template <typename T, int K, int V>
 struct GradSmem {
-  static constexpr int LK = K + 8, LV = V + 8, LM = 64 + 8;
-  static constexpr int kR = V * LK > 2 * 64 * LM ? V * LK : 2 * 64 * LM;
-  T C[64 * LK];
-  T B[64 * LK];
-  T X[64 * LV];
-  T Y[64 * LV];
-  T R[kR];  // a head's state columns [V][LK], then W and C B^T o L [64][LM]
-  float gam[64], eg[64], es[64], wt[64], dts[64];
+  T C[64 * K];
+  T B[64 * K];
+  T X[64 * V];
+  T Y[64 * V];
+  T R[V * K > 2 * 64 * 64 ? V * K : 2 * 64 * 64];  // state columns [V][K], then W and the scores
+  float gam[2][64];  // in powers of two
+  float eg[2][64], es[2][64], wt[2][64], dts[2][64], decay[2];
   float pe[4][64], pa[V / 16][64];
   int ex[kGradHeads][V / 16];
-  float fin[2][V / 16];
+  float fin[kGradHeads][V / 16];
 };
 
-// The ten tiles on or below the diagonal over NW waves, tile s of wave w
-// (row block * 4 + column block), -1 past its share.
-template <int NW>
-__device__ __forceinline__ int grad_tile(int w, int s) {
-  if (NW == 4) {
-    constexpr uint64_t t = 0xC | (0xDull << 4) | (0x0ull << 8) | (0xEull << 12) | (0xFull << 16) |
-                           (0x5ull << 20) | (0x8ull << 24) | (0x9ull << 28) | (0xAull << 36) |
-                           (0x4ull << 40);
-    return s < (w < 2 ? 3 : 2) ? (int)(t >> (12 * w + 4 * s)) & 15 : -1;
-  }
-  // eight waves: the first two take a second tile
-  constexpr uint64_t t = 0xFEDCA984ull;             // waves 0 .. 7
-  if (s == 0) return (int)(t >> (4 * w)) & 15;
-  return s == 1 && w < 2 ? (w == 0 ? 0x0 : 0x5) : -1;
-}
-
+// The two walks are mirror images: with (P, Q, p, q) = (C, B, dY, X) forward
+// and (B, C, X, dY) backward, a the token a result belongs to and b the one
+// it sums over (b <= a forward, b >= a backward), both form the scores P_a .
+// Q_b and p_a . q_b, the state's product with P and its dot with p, the
+// gradient of P from the state and W, and update the state with Q^T q.
 template <typename T, int K, int V, int HPW, bool REV>
-__global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGradArgs ga) {
+__global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void ssm_grad_kernel(
+    SsmGradArgs ga) {
   typedef typename VT<T>::x8 x8;
   typedef typename VT<T>::x4 x4;
-  typedef GradSmem<T, K, V> Smem;
-  constexpr int LK = Smem::LK, LV = Smem::LV, LM = Smem::LM;
   constexpr int NW = V / 16, NTH = 64 * NW, NT = K / 16, TPW = 4 * NT / NW;
-  constexpr int MT = NW == 4 ? 3 : 2;  // most tiles of a wave
+  constexpr int MT = kMostTiles<NW>;
   constexpr bool kScaled = !__is_same(T, __bf16);
-  struct __attribute__((packed, aligned(sizeof(T)))) Raw8 {
-    uint32_t u[2];
-  };
-  __shared__ Smem s;
+  __shared__ __align__(16) GradSmem<T, K, V> s;
   const SsmArgs& a = ga.f;
   const int R = a.H / a.G;
   const int L = xcd_order(blockIdx.x, gridDim.x);
@@ -117,8 +101,8 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
     if (REV && threadIdx.x < (unsigned)nh) ga.part_dD[(int64_t)id * a.H + head0 + threadIdx.x] = 0.f;
     return;
   }
-  const int w = threadIdx.x >> 6, l = lane_id(), g4 = l >> 4, col = l & 15;
-  const int v0 = 16 * w;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane_id();
 
   // start states: the forward walk's from the segment before (or h0), the
   // backward walk's from the segment after (or dht)
@@ -135,23 +119,11 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        dst[nt][e] = src ? src[(int64_t)state_k<V>(nt, e) * V + v0 + col] : 0.f;
+      for (int e = 0; e < 4; ++e) dst[nt][e] = src ? src[state_at(w, nt, e, V)] : 0.f;
   };
   auto end_grad = [&](int h, f32x4* dst) {  // the state's gradient at the segment's end
     if (sg.j + 1 < sg.count) load_slot(ga.seg_grad, id + 1, h, dst);
     else load_user(ga.dht, h, dst);
-  };
-  auto exponent = [&](const f32x4* p) {  // wave-wide: largest |S| 2^e in [2^13, 2^14)
-    float m = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(p[nt][e]));
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    const int e = 14 - __builtin_amdgcn_frexp_expf(m);
-    return m > 0.f && m < __builtin_inff() ? min(max(e, -100), 100) : 100;
   };
 #pragma unroll
   for (int hh = 0; hh < HPW; ++hh) {
@@ -161,7 +133,7 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
       else if (sg.j > 0) load_slot(a.seg_state, id - 1, h, S[hh]);
       else load_user(a.h0, h, S[hh]);
       if (kScaled) {
-        const int e = exponent(S[hh]);
+        const int e = state_exponent<NT>(S[hh]);
         if (l == 0) s.ex[hh][w] = e;
       }
     } else {
@@ -169,7 +141,6 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
       for (int nt = 0; nt < NT; ++nt) S[hh][nt] = zero4();
     }
   }
-  if (kScaled) __syncthreads();
 
   float rate[HPW], bias[HPW], skip[HPW], dsum[HPW];
 #pragma unroll
@@ -191,27 +162,58 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
   float raw = 0.f;
   const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
   auto token = [&](int c) { return sg.t0 + 64ll * (REV ? nch - 1 - c : c); };
+  auto rows_of = [&](int64_t t) { return (int)min((int64_t)64, sg.t1 - t); };
   auto request_bc = [&](int c) {
     const int64_t t = token(c);
-    const int rows = (int)min((int64_t)64, sg.t1 - t);
-    rb.load(bg + t * a.bs, a.bs, rows);
-    rc.load(cg + t * a.cs, a.cs, rows);
+    rb.load(bg + t * a.bs, a.bs, rows_of(t));
+    rc.load(cg + t * a.cs, a.cs, rows_of(t));
   };
   auto request_xy = [&](int c, int hh) {
     const int64_t t = token(c);
-    const int rows = (int)min((int64_t)64, sg.t1 - t);
-    rx.load(xg + t * a.xs + hh * V, a.xs, rows);
-    ry.load(yg + t * ys + hh * V, ys, rows);
-    raw = l < rows ? load_scalar(a.dt, (t + l) * a.H + head0 + hh, a.dt_dtype) : 0.f;
+    rx.load(xg + t * a.xs + hh * V, a.xs, rows_of(t));
+    ry.load(yg + t * ys + hh * V, ys, rows_of(t));
+  };
+  auto request_dt = [&](int c, int hh) {
+    const int64_t t = token(c);
+    raw = l < rows_of(t) ? load_scalar(a.dt, (t + l) * a.H + head0 + hh, a.dt_dtype) : 0.f;
+  };
+  auto gate = [&](int c, int hh, int b) {  // one token per lane
+    const float step =
+        l < rows_of(token(c)) ? ssm_step_size(raw, bias[hh], a.softplus) : 0.f;
+    const float g = rate[hh] * step;
+    const float gam = wave_prefix(g), es = __expf(wave_suffix_excl(g));
+    s.gam[b][l] = gam * kLog2e;
+    s.eg[b][l] = __expf(gam);
+    s.es[b][l] = es;
+    s.wt[b][l] = step * es;
+    s.dts[b][l] = step;
+    if (l == 0) s.decay[b] = __expf(lane_value(gam, 63));
   };
   if (nch > 0) {
     request_bc(0);
     request_xy(0, 0);
+    if (w == NW - 1) {
+      request_dt(0, 0);
+      gate(0, 0, 0);
+      if (nh > 1) request_dt(0, 1);
+      else if (nch > 1) request_dt(1, 0);
+    }
   }
+  if (kScaled) __syncthreads();
 
+  const T* P = REV ? s.B : s.C;
+  const T* Q = REV ? s.C : s.B;
+  const T* p = REV ? s.X : s.Y;
+  const T* q = REV ? s.Y : s.X;
+  T* const W = s.R;
+  T* const GL = s.R + 64 * 64;
+  Sw<K> ok;
+  Sw<V> ov;
+  Sw<64> om;
+  int b = 0;  // the gate's buffer
   for (int c = 0; c < nch; ++c) {
     const int64_t t = token(c);
-    const int rows = (int)min((int64_t)64, sg.t1 - t);
+    const int rows = rows_of(t);
     f32x4 gt[MT], wsum[MT], acc[TPW];
 #pragma unroll
     for (int k = 0; k < MT; ++k) gt[k] = wsum[k] = zero4();
@@ -221,25 +223,16 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
     for (int hh = 0; hh < HPW; ++hh) {
       if (hh >= nh) continue;
       const bool last = hh + 1 == nh;
-      // gate, one token per lane
-      const float step = l < rows ? ssm_step_size(raw, bias[hh], a.softplus) : 0.f;
-      const float g = rate[hh] * step;
-      const float gam = wave_inclusive_scan(g), suf = wave_suffix_excl(g);
-      const float decay = __expf(__shfl(gam, 63, 64));
-      if (w == 0) {
-        const float es = __expf(suf);
-        s.gam[l] = gam;
-        s.eg[l] = __expf(gam);
-        s.es[l] = es;
-        s.wt[l] = step * es;
-        s.dts[l] = step;
-      }
+      const int lf = fresh_v(l), wf = fresh_s(w), g4 = lf >> 4, col = lf & 15, v0 = 16 * wf;
+      ok.hide();
+      ov.hide();
+      om.hide();
       if (hh == 0) {
-        rb.store(s.B, LK);
-        rc.store(s.C, LK);
+        rb.store(s.B);
+        rc.store(s.C);
       }
-      rx.store(s.X, LV);
-      ry.store(s.Y, LV);
+      rx.store(s.X);
+      ry.store(s.Y);
       // the state's columns, rounded, for the other waves
       float up = 1.f, down = 1.f;
       if (kScaled) {
@@ -250,242 +243,226 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
         down = ldexpf(1.f, -e);
       }
 #pragma unroll
-      for (int kb = 0; kb < NT / 2; ++kb)
-        *reinterpret_cast<x8*>(s.R + (v0 + col) * LK + 32 * kb + 8 * g4) =
-            pack8<T>(S[hh][2 * kb] * up, S[hh][2 * kb + 1] * up);
+      for (int nt = 0; nt < NT; ++nt) {
+        x4 z;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = from_f<T>(kScaled ? S[hh][nt][e] * up : S[hh][nt][e]);
+        *row4(s.R, ok, v0, 16 * nt) = z;
+      }
       __syncthreads();  // A: tiles, gate and state columns are in LDS
 
-      if (!last) request_xy(c, hh + 1);
-      else if (c + 1 < nch) request_xy(c + 1, 0);
-      if (hh == 0 && c + 1 < nch) request_bc(c + 1);
-
-      // scores, their row or column sums, and W summed over the heads
+      // scores (transposed: rows b, columns a), their sums over b, and W
+      // summed over the heads
       f32x4 gl[MT];
 #pragma unroll
       for (int k = 0; k < MT; ++k) {
-        const int ti = grad_tile<NW>(w, k);
+        const int ti = tri_tile<NW>(wf, k);
         gl[k] = zero4();
         if (ti >= 0) {
-          const int rbk = ti >> 2, cbk = ti & 3;
+          const int ab = REV ? ti & 3 : ti >> 2, bb = REV ? ti >> 2 : ti & 3;
           if (hh == 0) {
 #pragma unroll
             for (int kb = 0; kb < K / 32; ++kb)
-              gt[k] = mfma16(frag_row(s.C + 16 * rbk * LK + 32 * kb, LK),
-                             frag_row(s.B + 16 * cbk * LK + 32 * kb, LK), gt[k]);
+              gt[k] = mfma16(row_frag(Q, ok, 16 * bb, 32 * kb), row_frag(P, ok, 16 * ab, 32 * kb),
+                             gt[k]);
           }
           f32x4 vt = zero4();
 #pragma unroll
           for (int kv = 0; kv < V / 32; ++kv)
-            vt = mfma16(frag_row(s.Y + 16 * rbk * LV + 32 * kv, LV),
-                        frag_row(s.X + 16 * cbk * LV + 32 * kv, LV), vt);
-          const int i = 16 * cbk + col;
-          const float gi = s.gam[i], di = s.dts[i];
-          float cs = 0.f;
+            vt = mfma16(row_frag(q, ov, 16 * bb, 32 * kv), row_frag(p, ov, 16 * ab, 32 * kv), vt);
+          const int ia = 16 * ab + col, ib = 16 * bb + 4 * g4;
+          const float gam_a = s.gam[b][ia], dt_a = s.dts[b][ia];
+          const f32x4 gam_b = *reinterpret_cast<const f32x4*>(&s.gam[b][ib]);
+          const f32x4 dt_b = *reinterpret_cast<const f32x4*>(&s.dts[b][ib]);
+          float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 16 * rbk + 4 * g4 + e;
-            const float lm = r >= i ? __expf(s.gam[r] - gi) : 0.f;
+            const bool in = REV ? ib + e >= ia : ib + e <= ia;
+            const float lx = exp2_fast(fminf(REV ? gam_b[e] - gam_a : gam_a - gam_b[e], 0.f));
+            const float lm = in ? lx : 0.f;
             const float f = vt[e] * lm;
-            wsum[k][e] += f * di;
+            const float fd = f * (REV ? dt_a : dt_b[e]);
+            wsum[k][e] += fd;
             if (REV) {
               gl[k][e] = gt[k][e] * lm;
-              cs += gt[k][e] * f;
-              if (r == i) dsum[hh] += vt[e];
+              sum += gt[k][e] * f;
+              if (ib + e == ia) dsum[hh] += vt[e];
             } else {
-              const float rs = sum16(gt[k][e] * f * di);
-              if (col == 0) s.pe[cbk][r] = rs;
+              sum += gt[k][e] * fd;
             }
           }
-          if (REV) {
-            cs = sum4g(cs);
-            if (g4 == 0) s.pe[rbk][i] = cs;
-          }
+          sum = sum4g(sum);
+          if (g4 == 0) s.pe[bb][ia] = sum;
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 
-      // dC^T (dB^T): the state's part, rows k, columns t
+      // P's gradient, transposed: the state's part, rows k, columns a
       {
-        const T* rows_lds = REV ? s.X : s.Y;
-        const float* sc = REV ? s.wt : s.eg;
-        constexpr int PER = TPW < 4 ? TPW : 4;   // tiles that share a column of the state
+        const float* sc = REV ? s.wt[b] : s.eg[b];
+        constexpr int PER = TPW < 4 ? TPW : 4;   // tiles that share the state's operand
 #pragma unroll
-        for (int q = 0; q < TPW / PER; ++q) {
-          const int idx = w * TPW + q * PER, nt = idx >> 2, rb0 = idx & 3;
+        for (int j = 0; j < TPW / PER; ++j) {
+          const int idx = wf * TPW + j * PER, nt = idx >> 2, a0 = idx & 3;
           f32x4 tmp[PER];
 #pragma unroll
           for (int i = 0; i < PER; ++i) tmp[i] = zero4();
 #pragma unroll
           for (int kv = 0; kv < V / 32; ++kv) {
-            const x8 af = frag_tr(s.R + 32 * kv * LK + 16 * nt, LK);
+            const x8 af = tr_frag(s.R, ok, 32 * kv, 16 * nt);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-              tmp[i] = mfma16(af, frag_row(rows_lds + 16 * (rb0 + i) * LV + 32 * kv, LV), tmp[i]);
+              tmp[i] = mfma16(af, split_frag(p, ov, 16 * (a0 + i), 32 * kv), tmp[i]);
           }
 #pragma unroll
           for (int i = 0; i < PER; ++i)
-            acc[q * PER + i] += tmp[i] * (sc[16 * (rb0 + i) + col] * down);
+            acc[j * PER + i] += tmp[i] * (sc[16 * (a0 + i) + col] * down);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
 
-      // S^T C^T (P^T B^T) with the state's pair, rows v, columns t; its dot
-      // with dy (x) goes into the row (column) sums
+      // the state's product with P, its pair of operands, rows v, columns a;
+      // its dot with p goes into a's sum
       f32x4 u[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) u[r] = zero4();
 #pragma unroll
-      for (int kb = 0; kb < NT / 2; ++kb) {
+      for (int kb = 0; kb < K / 32; ++kb) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[e] = S[hh][2 * kb][e] * up;
-          v[4 + e] = S[hh][2 * kb + 1][e] * up;
+          v[e] = kScaled ? S[hh][2 * kb][e] * up : S[hh][2 * kb][e];
+          v[4 + e] = kScaled ? S[hh][2 * kb + 1][e] * up : S[hh][2 * kb + 1][e];
         }
         x8 hi, lo;
         split8<T>(v, hi, lo);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const x8 f = frag_row((REV ? s.B : s.C) + 16 * r * LK + 32 * kb, LK);
+          const x8 f = split_frag(P, ok, 16 * r, 32 * kb);
           u[r] = mfma16(hi, f, u[r]);
           u[r] = mfma16(lo, f, u[r]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * r + col;
-        u[r] *= (REV ? s.es : s.eg)[row] * down;
-        const x4 o = *reinterpret_cast<const x4*>((REV ? s.X : s.Y) + row * LV + v0 + 4 * g4);
+        u[r] *= (REV ? s.es[b] : s.eg[b])[16 * r + col] * down;
+        const x4 o = *row4(p, ov, 16 * r, v0);
         float dot = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) dot += u[r][e] * to_f(o[e]);
         dot = sum4g(dot);
-        if (g4 == 0) s.pa[w][row] = dot;
+        if (g4 == 0) s.pa[w][16 * r + col] = dot;
       }
 
       // the state's update
       x8 xf[2];
-      {
-        const T* src = REV ? s.Y : s.X;
-        const T* mat = REV ? s.C : s.B;
-        float wt[2][8];
-        float m = 0.f;
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-          xf[tb] = frag_tr(src + 32 * tb * LV + v0, LV);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            wt[tb][e] = (REV ? s.eg : s.wt)[32 * tb + 8 * g4 + e];
-            if (kScaled) m = fmaxf(m, fabsf(to_f(xf[tb][e]) * wt[tb][e]));
-          }
-        }
-        const float scale = kScaled ? ldexpf(1.f, column_exponent(m)) : 1.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S[hh][nt] *= decay * scale;
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = to_f(xf[tb][e]) * wt[tb][e] * scale;
-          x8 hi, lo;
-          split8<T>(v, hi, lo);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const x8 bf = frag_tr_pair(mat + 32 * tb * LK + 32 * (nt >> 1) + 4 * (nt & 1), LK);
-            S[hh][nt] = mfma16(bf, hi, S[hh][nt]);
-            S[hh][nt] = mfma16(bf, lo, S[hh][nt]);
-          }
-        }
-        if (kScaled) {
-          const float back = 1.f / scale;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) S[hh][nt] *= back;
-        }
-      }
+      for (int tb = 0; tb < 2; ++tb) xf[tb] = tr_frag(q, ov, 32 * tb, v0);
+      update_state<T, K>(S[hh], Q, ok, xf, REV ? s.eg[b] : s.wt[b], g4, s.decay[b]);
       __syncthreads();  // B: the state columns are read, the partial sums written
 
+      if (!last) request_xy(c, hh + 1);
+      else if (c + 1 < nch) request_xy(c + 1, 0);
+      if (last && c + 1 < nch) request_bc(c + 1);
       if (kScaled) {
-        const int e = exponent(S[hh]);
+        const int e = state_exponent<NT>(S[hh]);
         if (l == 0) s.ex[hh][w] = e;
       }
-      if (threadIdx.x < 64 && l < rows) {
+      if (w == 0 && l < rows) {
         const int blk = l >> 4;
         float v = 0.f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (REV ? b >= blk : b <= blk) v += s.pe[b][l];
+        for (int i = 0; i < 4; ++i)
+          if (REV ? i >= blk : i <= blk) v += s.pe[i][l];
 #pragma unroll
-        for (int b = 0; b < NW; ++b) v += s.pa[b][l];
+        for (int i = 0; i < NW; ++i) v += s.pa[i][l];
         (REV ? ga.q : ga.row)[(int64_t)(head0 + hh) * ga.tokens + t + l] = v;
       }
       if (last || REV) {
-        T* W = s.R;
-        T* GL = s.R + 64 * LM;
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
-          const int ti = grad_tile<NW>(w, k);
+          const int ti = tri_tile<NW>(wf, k);
           if (ti >= 0) {
-            const int o = (16 * (ti >> 2) + 4 * g4) * LM + 16 * (ti & 3) + col;
+            const int ab = REV ? ti & 3 : ti >> 2, bb = REV ? ti >> 2 : ti & 3;
+            x4 z;
+            if (last) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (last) W[o + e * LM] = from_f<T>(wsum[k][e]);
-              if (REV) GL[o + e * LM] = from_f<T>(gl[k][e]);
+              for (int e = 0; e < 4; ++e) z[e] = from_f<T>(wsum[k][e]);
+              *row4(W, om, 16 * ab, 16 * bb) = z;
+            }
+            if (REV) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) z[e] = from_f<T>(gl[k][e]);
+              *row4(GL, om, 16 * ab, 16 * bb) = z;
             }
           }
         }
-        // the tiles above the diagonal that the products read: (0, 1), (2, 3)
-        for (int i = threadIdx.x; i < 512; i += NTH) {
-          const int o = ((i >> 8) * 32 + ((i >> 4) & 15)) * LM + (i >> 8) * 32 + 16 + (i & 15);
-          W[o] = (T)0.f;
-          GL[o] = (T)0.f;
+        // the tiles beyond the diagonal that the products read: (a, b) = (0, 1)
+        // and (2, 3) forward, (1, 0) and (3, 2) backward
+        for (int i = threadIdx.x; i < 128; i += NTH) {
+          const int r0 = (i >> 6) * 32, ar = r0 + (REV ? 16 : 0) + ((i >> 2) & 15),
+                    bc = r0 + (REV ? 0 : 16) + 4 * (i & 3);
+          const x4 z{};
+          *reinterpret_cast<x4*>(W + sw_off<64>(ar, bc)) = z;
+          *reinterpret_cast<x4*>(GL + sw_off<64>(ar, bc)) = z;
         }
-        __syncthreads();  // C: W and C B^T o L are in LDS
+        __syncthreads();  // C: W and the decayed scores are in LDS
 
         if (last) {
+          const int row_bytes = a.G * K * (ga.slots == 1 ? (int)sizeof(T) : 4);
+          const int64_t o = (t * a.G + grp) * K;
+          char* base = ga.slots == 1
+                           ? reinterpret_cast<char*>(reinterpret_cast<T*>(REV ? ga.dB : ga.dC) + o)
+                           : reinterpret_cast<char*>((REV ? ga.part_dB : ga.part_dC) +
+                                                     (int64_t)slot * ga.tokens * a.G * K + o);
+          const auto rs = buf_rsrc(base, (int64_t)(rows - 1) * row_bytes + K * (ga.slots == 1 ? 2 : 4));
 #pragma unroll
           for (int i = 0; i < TPW; ++i) {
-            const int idx = w * TPW + i, nt = idx >> 2, blk = idx & 3;
-            if (!REV) {
-              for (int ib = 0; ib <= (blk >> 1); ++ib)
-                acc[i] = mfma16(frag_tr(s.B + 32 * ib * LK + 16 * nt, LK),
-                                frag_row(W + 16 * blk * LM + 32 * ib, LM), acc[i]);
+            const int idx = wf * TPW + i, nt = idx >> 2, ab = idx & 3;
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb)
+              if (REV ? sb >= (ab >> 1) : sb <= (ab >> 1))
+                acc[i] = mfma16(tr_frag(Q, ok, 32 * sb, 16 * nt), split_frag(W, om, 16 * ab, 32 * sb),
+                                acc[i]);
+            const int off = (16 * ab + col) * row_bytes, k0 = 16 * nt + 4 * g4;
+            if (ga.slots == 1) {
+              const x4 z{from_f<T>(acc[i][0]), from_f<T>(acc[i][1]), from_f<T>(acc[i][2]),
+                         from_f<T>(acc[i][3])};
+              buf_store8(rs, off + 2 * k0, __builtin_bit_cast(u32x2, z));
             } else {
-              for (int rk = blk >> 1; rk < 2; ++rk)
-                acc[i] = mfma16(frag_tr(s.C + 32 * rk * LK + 16 * nt, LK),
-                                frag_tr(W + 32 * rk * LM + 16 * blk, LM), acc[i]);
-            }
-            const int row = 16 * blk + col;
-            if (row < rows) {
-              const int64_t o = ((t + row) * a.G + grp) * K + 16 * nt + 4 * g4;
-              if (ga.slots == 1) {
-                x4 z{from_f<T>(acc[i][0]), from_f<T>(acc[i][1]), from_f<T>(acc[i][2]),
-                     from_f<T>(acc[i][3])};
-                *reinterpret_cast<Raw8*>(reinterpret_cast<T*>(REV ? ga.dB : ga.dC) + o) =
-                    __builtin_bit_cast(Raw8, z);
-              } else {
-                float* p = (REV ? ga.part_dB : ga.part_dC) + (int64_t)slot * ga.tokens * a.G * K + o;
-                *reinterpret_cast<f32x4*>(p) = acc[i];
-              }
+              buf_store16(rs, off + 4 * k0, __builtin_bit_cast(uint4, acc[i]));
             }
           }
         }
         if (REV) {
           T* dx = reinterpret_cast<T*>(ga.dx) + t * ys + (int64_t)(head0 + hh) * V;
+          const int yb = (int)ys * (int)sizeof(T);
+          const auto rs = buf_rsrc(dx, (int64_t)(rows - 1) * yb + V * (int)sizeof(T));
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
 #pragma unroll
-            for (int rk = r >> 1; rk < 2; ++rk)
-              u[r] = mfma16(xf[rk], frag_tr(GL + 32 * rk * LM + 16 * r, LM), u[r]);
+            for (int sb = r >> 1; sb < 2; ++sb)
+              u[r] = mfma16(xf[sb], split_frag(GL, om, 16 * r, 32 * sb), u[r]);
             const int row = 16 * r + col;
-            if (row < rows) {
-              const float di = s.dts[row];
-              const x4 yv = *reinterpret_cast<const x4*>(s.Y + row * LV + v0 + 4 * g4);
-              x4 z;
+            const float di = s.dts[b][row];
+            const x4 yv = *row4(s.Y, ov, 16 * r, v0);
+            x4 z;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) z[e] = from_f<T>(di * u[r][e] + skip[hh] * to_f(yv[e]));
-              *reinterpret_cast<Raw8*>(dx + row * ys + v0 + 4 * g4) = __builtin_bit_cast(Raw8, z);
-            }
+            for (int e = 0; e < 4; ++e) z[e] = from_f<T>(di * u[r][e] + skip[hh] * to_f(yv[e]));
+            buf_store8(rs, row * yb + (v0 + 4 * g4) * (int)sizeof(T), __builtin_bit_cast(u32x2, z));
           }
         }
       }
+      if (w == NW - 1) {  // the gate of the next head or chunk, whose dt is here already
+        const int hn = last ? 0 : hh + 1, cn = last ? c + 1 : c;
+        if (cn < nch) {
+          gate(cn, last ? 0 : (hh + 1 < HPW ? hh + 1 : 0), b ^ 1);
+          const int h2 = hn + 1 < nh ? hn + 1 : 0, c2 = hn + 1 < nh ? cn : cn + 1;
+          if (c2 < nch) request_dt(c2, h2);
+        }
+      }
+      b ^= 1;
       __syncthreads();  // D: the tiles may be overwritten
     }
   }
@@ -501,19 +478,18 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 2 : 1) void ssm_grad_kernel(SsmGra
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            ga.dh0[((int64_t)sg.n * a.H + h) * KV + (int64_t)state_k<V>(nt, e) * V + v0 + col] =
-                S[hh][nt][e];
+            ga.dh0[((int64_t)sg.n * a.H + h) * KV + state_at(w, nt, e, V)] = S[hh][nt][e];
       }
       const float d = wave_sum(dsum[hh]);
       if (l == 0) s.fin[hh][w] = d;
     } else {
-      f32x4 P[NT];
-      end_grad(h, P);
+      f32x4 E[NT];
+      end_grad(h, E);
       float d = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d += S[hh][nt][e] * P[nt][e];
+        for (int e = 0; e < 4; ++e) d += S[hh][nt][e] * E[nt][e];
       d = wave_sum(d);
       if (l == 0) s.fin[hh][w] = d;
     }

@@ -90,45 +90,75 @@ __device__ __forceinline__ int xcd_order(int b, int nb) {
   return x * q + min(x, r) + (b >> 3);
 }
 
+// A value that the compiler takes to be new at this point: what depends on it
+// is formed here again and not kept in registers across the chunk loop.
+__device__ __forceinline__ int fresh_v(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+__device__ __forceinline__ int fresh_s(int x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// softplus(z) = max(z, 0) + log(1 + u), u = e^{-|z|}, to a few units of fp32's
+// last place: a step size's relative error is multiplied by the exponent that
+// the decay has summed up.  e^t is 2^h (1 + ln 2 r) with t log2(e) = h + r, the
+// product's rounding being r; log(1 + u) = 2 atanh(s), s = u / (2 + u) <= 1/3, by
+// its series (the first term left out is below 2^-25 of the sum).
 __device__ __forceinline__ float ssm_step_size(float raw, float bias, int softplus) {
-  const float z = raw + bias;
-  return softplus ? fmaxf(z, 0.f) + log1pf(__expf(-fabsf(z))) : z;
+  const float z = raw + bias, t = fmaxf(-fabsf(z), -120.f);
+  const float h = t * kLog2e, r = __builtin_fmaf(t, kLog2e, -h);
+  const float e = exp2_fast(h);
+  const float u = __builtin_fmaf(e, r * 0.69314718f, e);
+  const float s = u * fast_rcp(2.f + u), q = s * s;
+  float p = 1.f / 15.f;
+  p = __builtin_fmaf(p, q, 1.f / 13.f);
+  p = __builtin_fmaf(p, q, 1.f / 11.f);
+  p = __builtin_fmaf(p, q, 1.f / 9.f);
+  p = __builtin_fmaf(p, q, 1.f / 7.f);
+  p = __builtin_fmaf(p, q, 1.f / 5.f);
+  p = __builtin_fmaf(p, q, 1.f / 3.f);
+  p = __builtin_fmaf(p, q, 1.f);
+  return softplus && z == z ? __builtin_fmaf(2.f * s, p, fmaxf(z, 0.f)) : z;
 }
 
 __device__ __forceinline__ float param(const void* p, int i, int dtype) {
   return p ? load_scalar(p, i, dtype) : 0.f;
 }
 
-// Exclusive suffix sum over the wave's lanes: sum of x over the lanes above.
-__device__ __forceinline__ float wave_suffix_excl(float x) {
-  const int l = lane_id();
-  float s = __shfl_down(x, 1, 64);
-  if (l == 63) s = 0.f;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const float y = __shfl_down(s, off, 64);
-    if (l + off < 64) s += y;
-  }
-  return s;
+// Prefix (inclusive) and suffix (exclusive) sums over the wave's lanes: DPP
+// shifts within the rows of 16, then the rows' totals through scalars.
+template <int CTRL>
+__device__ __forceinline__ float dpp_zero(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
+                                                               0xF, 0xF, true));
 }
-
-// Transposed operand fragment with its rows in pair order: lane (grp, col)
-// receives X[k0 + 8 grp + e][m0 + 8 (col / 4) + col % 4] of a row-major LDS
-// matrix (base = &X[k0][m0]).  The D tiles of two such operands, m0 and m0 + 4,
-// then hold rows 8 grp + e and 8 grp + 4 + e of a 32-row block: packed side by
-// side they are an operand in contiguous k order with no data movement, and
-// the other operand is one 16-byte read (frag_row).
-template <typename T>
-__device__ __forceinline__ typename VT<T>::x8 frag_tr_pair(const T* base, int ld) {
-  const int l = lane_id();
-  const int grp = l >> 4, j = l & 15;
-  const T* p0 = base + (8 * grp + (j >> 2)) * ld + 8 * (j & 3);
-  const T* p1 = p0 + 4 * ld;
-  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p0));
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p1));
-  const i16x8 r = i16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  return __builtin_bit_cast(typename VT<T>::x8, r);
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ float wave_prefix(float x) {
+  x += dpp_zero<0x111>(x);
+  x += dpp_zero<0x112>(x);
+  x += dpp_zero<0x114>(x);
+  x += dpp_zero<0x118>(x);
+  const float a = lane_value(x, 15), b = lane_value(x, 31), c = lane_value(x, 47);
+  const int row = lane_id() >> 4;
+  return x + (row == 0 ? 0.f : row == 1 ? a : row == 2 ? a + b : (a + b) + c);
+}
+__device__ __forceinline__ float wave_suffix_excl(float x) {
+  x = __shfl_down(x, 1, 64);
+  if (lane_id() == 63) x = 0.f;
+  x += dpp_zero<0x101>(x);
+  x += dpp_zero<0x102>(x);
+  x += dpp_zero<0x104>(x);
+  x += dpp_zero<0x108>(x);
+  const float a = lane_value(x, 48), b = lane_value(x, 32), c = lane_value(x, 16);
+  const int row = lane_id() >> 4;
+  return x + (row == 3 ? 0.f : row == 2 ? a : row == 1 ? a + b : (a + b) + c);
 }
 
 // Exponent e such that the largest |v| of the lane's column (the four lanes
@@ -151,56 +181,194 @@ __device__ __forceinline__ void split8(const float* v, typename VT<T>::x8& hi,
                                        typename VT<T>::x8& lo) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    hi[e] = from_f<T>(v[e]);
-    lo[e] = from_f<T>(v[e] - to_f(hi[e]));
+    // v as one fp32 number: from the product it came from the compiler forms
+    // hi twice, once rounded straight to fp16 (v_fma_mixlo_f16) and once by
+    // way of fp32, which now and then are not the same
+    float t = v[e];
+    asm("" : "+v"(t));
+    hi[e] = from_f<T>(t);
+    lo[e] = from_f<T>(t - to_f(hi[e]));
   }
 }
 
-template <typename T>
-__device__ __forceinline__ typename VT<T>::x8 pack8(f32x4 a, f32x4 b) {
-  return typename VT<T>::x8{from_f<T>(a[0]), from_f<T>(a[1]), from_f<T>(a[2]), from_f<T>(a[3]),
-                            from_f<T>(b[0]), from_f<T>(b[1]), from_f<T>(b[2]), from_f<T>(b[3])};
+// Operand reads from swizzled tiles (sw_off).  The lane's byte offsets for the
+// three patterns are formed once; a tile's column offset is a multiple of 16
+// elements and enters by an exclusive or, its rows by an addition, so an
+// address costs at most one instruction.  hide() keeps the compiler from
+// forming all of them ahead of the chunk loop, which spills registers.
+template <int COLS>
+struct Sw {
+  int row, split, tr;
+  __device__ __forceinline__ Sw() {
+    const int l = lane_id(), g = l >> 4, j = l & 15;
+    row = 2 * sw_off<COLS>(j, 8 * g % COLS);
+    split = 2 * sw_off<COLS>(j, 4 * g);
+    tr = 2 * sw_off<COLS>(4 * g + (j >> 2), 4 * (j & 3));
+  }
+  __device__ __forceinline__ void hide() { asm volatile("" : "+v"(row), "+v"(split), "+v"(tr)); }
+};
+// rows r0 + lane % 16, columns k0 + 8 (lane / 16) .. + 7
+template <typename T, int COLS>
+__device__ __forceinline__ typename VT<T>::x8 row_frag(const T* X, const Sw<COLS>& o, int r0, int k0) {
+  return *reinterpret_cast<const typename VT<T>::x8*>(reinterpret_cast<const char*>(X) +
+                                                       2 * COLS * r0 + (o.row ^ (2 * k0)));
+}
+// four elements of row r0 + lane % 16 from column c0 + 4 (lane / 16)
+template <typename T, int COLS>
+__device__ __forceinline__ const typename VT<T>::x4* row4(const T* X, const Sw<COLS>& o, int r0,
+                                                          int c0) {
+  return reinterpret_cast<const typename VT<T>::x4*>(reinterpret_cast<const char*>(X) +
+                                                     2 * COLS * r0 + (o.split ^ (2 * c0)));
+}
+template <typename T, int COLS>
+__device__ __forceinline__ typename VT<T>::x4* row4(T* X, const Sw<COLS>& o, int r0, int c0) {
+  return reinterpret_cast<typename VT<T>::x4*>(reinterpret_cast<char*>(X) + 2 * COLS * r0 +
+                                               (o.split ^ (2 * c0)));
+}
+// the same rows in split k order
+template <typename T, int COLS>
+__device__ __forceinline__ typename VT<T>::x8 split_frag(const T* X, const Sw<COLS>& o, int r0,
+                                                         int k0) {
+  typedef typename VT<T>::x4 x4;
+  const char* p = reinterpret_cast<const char*>(X) + 2 * COLS * r0;
+  const x4 lo = *reinterpret_cast<const x4*>(p + (o.split ^ (2 * k0)));
+  const x4 hi = *reinterpret_cast<const x4*>(p + (o.split ^ (2 * k0 + 32)));
+  return typename VT<T>::x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+// columns m0 + lane % 16, the 32 rows from k0 in split k order
+template <typename T, int COLS>
+__device__ __forceinline__ typename VT<T>::x8 tr_frag(const T* X, const Sw<COLS>& o, int k0, int m0) {
+  const char* p = reinterpret_cast<const char*>(X) + 2 * COLS * k0 + (o.tr ^ (2 * m0));
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p));
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p + 32 * COLS));
+  return __builtin_bit_cast(typename VT<T>::x8,
+                            i16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 }
 
-// 64 rows of COLS elements from global memory into registers and from there
-// to LDS (rows past `rows` are zero); NT threads, 16-byte pieces at any
-// alignment.
+// Exponent e, the same in the wave, such that the largest |S| times 2^e lies in
+// [2^13, 2^14); for fp16 operands.
+template <int NT>
+__device__ __forceinline__ int state_exponent(const f32x4* S) {
+  float m = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(S[nt][e]));
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  const int e = 14 - __builtin_amdgcn_frexp_expf(m);
+  return m > 0.f && m < __builtin_inff() ? min(max(e, -100), 100) : 100;
+}
+
+// The weighted values of block tb of a chunk: column operand xf (split k order)
+// times its tokens' weights.
+template <typename T>
+__device__ __forceinline__ void weighted(const typename VT<T>::x8& xf, const float* wt, int tb,
+                                         int g4, float scale, float* v) {
+  const f32x4 w0 = *reinterpret_cast<const f32x4*>(wt + 32 * tb + 4 * g4) * scale;
+  const f32x4 w1 = *reinterpret_cast<const f32x4*>(wt + 32 * tb + 16 + 4 * g4) * scale;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = to_f(xf[e]) * (e < 4 ? w0[e & 3] : w1[e & 3]);
+}
+
+// S <- decay S + A^T diag(wt) x over a chunk's 64 tokens: A a swizzled 64 x K
+// tile, xf the lane's column of x in two blocks of 32 tokens, wt in LDS.  The
+// weighted values go in as a pair of 16-bit operands; with fp16 the columns
+// are scaled to fit.
+template <typename T, int K>
+__device__ __forceinline__ void update_state(f32x4* S, const T* A, const Sw<K>& o,
+                                             const typename VT<T>::x8* xf, const float* wt, int g4,
+                                             float decay) {
+  constexpr int NT = K / 16;
+  constexpr bool kScaled = !__is_same(T, __bf16);
+  float scale = 1.f;
+  if (kScaled) {
+    float m = 0.f;
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+      float v[8];
+      weighted<T>(xf[tb], wt, tb, g4, 1.f, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+    }
+    scale = ldexpf(1.f, column_exponent(m));
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) S[nt] *= kScaled ? decay * scale : decay;
+#pragma unroll
+  for (int tb = 0; tb < 2; ++tb) {
+    typename VT<T>::x8 hi, lo;
+    float v[8];
+    weighted<T>(xf[tb], wt, tb, g4, scale, v);
+    split8<T>(v, hi, lo);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const auto f = tr_frag(A, o, 32 * tb, 16 * nt);
+      S[nt] = mfma16(f, hi, S[nt]);
+      S[nt] = mfma16(f, lo, S[nt]);
+      // a few operands in flight, not all of them: registers
+      if (nt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (kScaled) {
+    const float back = 1.f / scale;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) S[nt] *= back;
+  }
+}
+
+// 64 rows of COLS elements: NT threads hold them in registers between the
+// global loads and the swizzled LDS tile (sw_off), so that the next chunk's
+// loads are in flight while this one computes.  The range check of the
+// buffer loads makes rows past the chunk's end zero.
 template <typename T, int COLS, int NT>
 struct Rows64 {
-  static constexpr int kPer = 64 * COLS / 8 / NT;
-  Vec<T> r[kPer];
+  static constexpr int kPer = 64 * COLS / 8 / NT, kRow = COLS / 8, kStep = NT / kRow;
+  static_assert(kStep % 16 == 0, "a thread's rows share their swizzle");
+  uint4 r[kPer];
   __device__ __forceinline__ void load(const T* g, int64_t stride, int rows) {
+    const auto rs = buf_rsrc(g, ((rows - 1) * stride + COLS) * (int64_t)sizeof(T));
+    const int sb = (int)stride * (int)sizeof(T);
+    int off = (int)threadIdx.x / kRow * sb + (int)threadIdx.x % kRow * 16;
+    asm volatile("" : "+v"(off));
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int p = i * NT + threadIdx.x, row = p / (COLS / 8), c = p % (COLS / 8) * 8;
-      if (row < rows) {
-        r[i].load(g + row * stride + c);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[i].v[e] = (T)0.f;
-      }
-    }
+    for (int i = 0; i < kPer; ++i) r[i] = buf_load16(rs, off + i * (kStep * sb));
   }
-  __device__ __forceinline__ void store(T* lds, int ld) const {
+  __device__ __forceinline__ void store(T* lds) const {
+    T* p = lds + sw_off<COLS>((int)threadIdx.x / kRow, (int)threadIdx.x % kRow * 8);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int p = i * NT + threadIdx.x, row = p / (COLS / 8), c = p % (COLS / 8) * 8;
-      *reinterpret_cast<uint4*>(lds + row * ld + c) = __builtin_bit_cast(uint4, r[i]);
-    }
+    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(p + i * kStep * COLS) = r[i];
   }
 };
 
-// State element (k, v) of register e of tile nt, column tile pt, for wave w of
-// 4 whose columns start at w V / 4: pair order along k (frag_tr_pair).
-template <int V>
-__device__ __forceinline__ int state_k(int nt, int e) {
+// The ten 16 x 16 tiles on or below the diagonal of a chunk's 64 x 64 matrix
+// over NW waves: tile s of wave w as row block * 4 + column block, -1 past
+// the wave's share (3, 3, 2, 2 of four waves; 2, 2 and six times 1 of eight).
+template <int NW>
+__device__ __forceinline__ int tri_tile(int w, int s) {
+  if (NW == 4) {
+    constexpr uint64_t t = 0xC | (0xDull << 4) | (0x0ull << 8) | (0xEull << 12) | (0xFull << 16) |
+                           (0x5ull << 20) | (0x8ull << 24) | (0x9ull << 28) | (0xAull << 36) |
+                           (0x4ull << 40);
+    return s < (w < 2 ? 3 : 2) ? (int)(t >> (12 * w + 4 * s)) & 15 : -1;
+  }
+  constexpr uint64_t t = 0xFEDCA984ull;
+  if (s == 0) return (int)(t >> (4 * w)) & 15;
+  return s == 1 && w < 2 ? (w == 0 ? 0x0 : 0x5) : -1;
+}
+template <int NW>
+constexpr int kMostTiles = NW == 4 ? 3 : 2;
+
+// State element (k, v) of register e of tile nt in wave w: k = 16 nt + 4 (lane
+// / 16) + e, v = 16 w + lane % 16 (the accumulator layout; two stacked tiles
+// are an operand in split k order).
+__device__ __forceinline__ int state_at(int w, int nt, int e, int V) {
   const int l = lane_id();
-  return 32 * (nt >> 1) + 8 * (l >> 4) + 4 * (nt & 1) + e;
+  return (16 * nt + 4 * (l >> 4) + e) * V + 16 * w + (l & 15);
 }
-template <int V>
-__device__ __forceinline__ int state_v(int w, int pt) {
-  return w * (V / 4) + 16 * pt + (lane_id() & 15);
-}
+
+// token of element e of lane group g4's operand in split k order
+__device__ __forceinline__ int split_at(int g4, int e) { return (e < 4 ? 0 : 12) + 4 * g4 + e; }
 
 // Host side: the problem's arguments, its element type and sizes as types.
 SsmArgs ssm_args(const gdr_ssm_problem* p, const SsmPlan& pl);

@@ -16,49 +16,43 @@ namespace gdr {
 
 namespace {
 
-constexpr int kNT = 256;
-
-// The ten tiles on or below the diagonal of a 64 x 64 matrix over four waves
-// (3, 3, 2, 2): 4 bits each, row block * 4 + column block.
-constexpr uint64_t kTiles = 0xC | (0xDull << 4) | (0x0ull << 8) |        // wave 0
-                            (0xEull << 12) | (0xFull << 16) | (0x5ull << 20) |  // wave 1
-                            (0x8ull << 24) | (0x9ull << 28) |            // wave 2
-                            (0xAull << 36) | (0x4ull << 40);             // wave 3
-__device__ __forceinline__ int tile_of(int w, int s) { return (int)(kTiles >> (12 * w + 4 * s)) & 15; }
-__device__ __forceinline__ int tiles_of(int w) { return w < 2 ? 3 : 2; }
-
 template <typename T, int K, int V>
-struct OutSmem {
-  static constexpr int LK = K + 8, LV = V + 8, LM = 64 + 8;
-  T C[64 * LK];
-  T B[64 * LK];
-  T X[64 * LV];
-  T M[64 * LM];
-  float gam[64], eg[64], wt[64], dts[64];
+struct WalkSmem {
+  T C[64 * K];
+  T B[64 * K];
+  T X[64 * V];
+  T M[64 * 64];
+  float gam[2][64];  // in powers of two
+  float eg[2][64], wt[2][64], dts[2][64], decay[2];
 };
 
 // kOut: the segment's outputs from its start state.  kState: what it adds to
 // the state.  kGrad: what it adds to the state's gradient at its start, the
 // same with dy and C for x and B (the caller passes them so), e^gamma for the
-// weights, and the chunks from the last to the first.  Four waves, each with
-// V / 4 state columns in MFMA accumulators.
+// weights, and the chunks from the last to the first.
+//
+// V / 16 waves, each with 16 state columns in accumulators.  Per chunk, the
+// tiles of the next one are in registers (in flight), those of this one in
+// LDS, swizzled so that row operands and transposing reads are free of bank
+// conflicts; the last wave, which has the fewest score tiles, forms the next
+// chunk's gate.  Three (V = 64) or two (V = 128) workgroups share a CU's LDS
+// and registers and hide each other's barriers.
 enum { kOut, kState, kGrad };
 template <typename T, int K, int V, int MODE>
-__global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
+__global__ __launch_bounds__(4 * V, 3) void ssm_walk_kernel(SsmArgs a) {
   typedef typename VT<T>::x8 x8;
-  typedef OutSmem<T, K, V> Smem;
-  constexpr int LK = Smem::LK, LV = Smem::LV, LM = Smem::LM;
-  constexpr int NT = K / 16, PT = V / 64;
+  typedef typename VT<T>::x4 x4;
+  constexpr int NW = V / 16, NTH = 64 * NW, NT = K / 16;
   constexpr bool OUT = MODE == kOut;
   constexpr bool kScaled = !__is_same(T, __bf16);
-  __shared__ Smem s;
+  __shared__ __align__(16) WalkSmem<T, K, V> s;
   const int L = xcd_order(blockIdx.x, gridDim.x);
   const int id = L / a.H, h = L % a.H, grp_h = h / (a.H / a.G);
   const Segment sg = segment_of(a, id);
   if (sg.count == 0) return;
   if (MODE == kState && sg.j + 1 >= sg.count) return;
   if (MODE == kGrad && sg.j == 0) return;
-  const int w = threadIdx.x >> 6, l = lane_id(), g4 = l >> 4, col = l & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
 
   const T* xg = reinterpret_cast<const T*>(a.x) + (int64_t)h * V;
   const T* bg = reinterpret_cast<const T*>(a.B) + (int64_t)grp_h * K;
@@ -66,198 +60,160 @@ __global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
   const float rate = -expf(load_scalar(a.A_log, h, a.p_dtype));
   const float bias = param(a.dt_bias, h, a.p_dtype), skip = param(a.D, h, a.p_dtype);
 
-  // the state in accumulators
-  f32x4 S[PT][NT];
+  f32x4 S[NT];
   const int64_t unit = ((int64_t)sg.n * a.H + h) * K * V;
   const int64_t slot = ((int64_t)id * a.H + h) * K * V;
   if (OUT && sg.j > 0) {
     const float* src = a.seg_state + slot - (int64_t)a.H * K * V;
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        S[pt][nt] = *reinterpret_cast<const f32x4*>(src + (((w * PT + pt) * NT + nt) * 64 + l) * 4);
+    for (int nt = 0; nt < NT; ++nt)
+      S[nt] = *reinterpret_cast<const f32x4*>(src + ((w * NT + nt) * 64 + l) * 4);
   } else {
     const bool from = OUT && a.h0;
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          S[pt][nt][e] = from ? a.h0[unit + (int64_t)state_k<V>(nt, e) * V + state_v<V>(w, pt)] : 0.f;
+      for (int e = 0; e < 4; ++e) S[nt][e] = from ? a.h0[unit + state_at(w, nt, e, V)] : 0.f;
   }
   if (OUT) {  // tiles above the diagonal that the product with M reads: (0, 1) and (2, 3)
-    for (int i = threadIdx.x; i < 512; i += kNT) {
-      const int r = (i >> 8) * 32 + ((i >> 4) & 15), c = (i >> 8) * 32 + 16 + (i & 15);
-      s.M[r * LM + c] = (T)0.f;
-    }
+    for (int i = threadIdx.x; i < 512; i += NTH)
+      s.M[sw_off<64>((i >> 8) * 32 + ((i >> 4) & 15), (i >> 8) * 32 + 16 + (i & 15))] = (T)0.f;
   }
 
-  Rows64<T, K, kNT> rb, rc;
-  Rows64<T, V, kNT> rx;
+  const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
+  auto token = [&](int c) { return sg.t0 + 64ll * (MODE == kGrad ? nch - 1 - c : c); };
+  auto rows_of = [&](int64_t t) { return (int)min((int64_t)64, sg.t1 - t); };
+  Rows64<T, K, NTH> rb, rc;
+  Rows64<T, V, NTH> rx;
   float raw = 0.f, total = 0.f;
   auto request = [&](int64_t t) {
-    const int rows = (int)min((int64_t)64, sg.t1 - t);
+    const int rows = rows_of(t);
     rx.load(xg + t * a.xs, a.xs, rows);
     rb.load(bg + t * a.bs, a.bs, rows);
     if (OUT) rc.load(cg + t * a.cs, a.cs, rows);
-    raw = l < rows ? load_scalar(a.dt, (t + l) * a.H + h, a.dt_dtype) : 0.f;
   };
-  const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
-  auto token = [&](int c) { return sg.t0 + 64ll * (MODE == kGrad ? nch - 1 - c : c); };
-  if (nch > 0) request(token(0));
+  auto request_dt = [&](int64_t t) {
+    raw = l < rows_of(t) ? load_scalar(a.dt, (t + l) * a.H + h, a.dt_dtype) : 0.f;
+  };
+  // a chunk's gate, one token per lane; tokens past the end have step size 0
+  auto gate = [&](int64_t t, int b) {
+    const float step = l < rows_of(t) ? ssm_step_size(raw, bias, a.softplus) : 0.f;
+    const float g = rate * step;
+    const float gam = wave_prefix(g);
+    const float all = lane_value(gam, 63);
+    total += all;
+    s.gam[b][l] = gam * kLog2e;
+    s.eg[b][l] = __expf(gam);
+    s.wt[b][l] = MODE == kGrad ? __expf(gam) : step * __expf(wave_suffix_excl(g));
+    s.dts[b][l] = step;
+    if (l == 0) s.decay[b] = __expf(all);
+  };
+  if (nch > 0) {
+    request(token(0));
+    if (w == NW - 1) {
+      request_dt(token(0));
+      gate(token(0), 0);
+      if (nch > 1) request_dt(token(1));
+    }
+  }
 
+  Sw<K> ok;
+  Sw<V> ov;
+  Sw<64> om;
   for (int c = 0; c < nch; ++c) {
     const int64_t t = token(c);
-    const int rows = (int)min((int64_t)64, sg.t1 - t);
-    // the chunk's gate, one token per lane (every wave forms it; the first
-    // one stores it); tokens past the end have step size 0
-    const float step = l < rows ? ssm_step_size(raw, bias, a.softplus) : 0.f;
-    const float g = rate * step;
-    const float gam = wave_inclusive_scan(g), suf = wave_suffix_excl(g);
-    const float all = __shfl(gam, 63, 64);
-    total += all;
-    if (w == 0) {
-      s.gam[l] = gam;
-      s.eg[l] = __expf(gam);
-      s.wt[l] = MODE == kGrad ? __expf(gam) : step * __expf(suf);
-      s.dts[l] = step;
-    }
-    rx.store(s.X, LV);
-    rb.store(s.B, LK);
-    if (OUT) rc.store(s.C, LK);
+    const int b = c & 1;
+    const int lf = fresh_v(l), wf = fresh_s(w), g4 = lf >> 4, col = lf & 15, v0 = 16 * wf;
+    ok.hide();
+    ov.hide();
+    om.hide();
+    rx.store(s.X);
+    rb.store(s.B);
+    if (OUT) rc.store(s.C);
     __syncthreads();
-    if (c + 1 < nch) request(token(c + 1));
 
-    f32x4 acc[PT][4];
+    f32x4 acc[4];
     if (OUT) {
-      // M = (C B^T) o L diag(dt), rounded to T as an operand
-      const int nt = tiles_of(w);
-      for (int k = 0; k < nt; ++k) {
-        const int ti = tile_of(w, k), rbk = ti >> 2, cbk = ti & 3;
-        f32x4 m = zero4();
+      // M = (C B^T) o L diag(dt), rounded to T as an operand; its tiles are
+      // formed transposed, so that a lane holds four neighbours of a row
 #pragma unroll
-        for (int kb = 0; kb < K / 32; ++kb)
-          m = mfma16(frag_row(s.C + 16 * rbk * LK + 32 * kb, LK),
-                     frag_row(s.B + 16 * cbk * LK + 32 * kb, LK), m);
-        const int i = 16 * cbk + col;
-        const float gi = s.gam[i], di = s.dts[i];
+      for (int k = 0; k < kMostTiles<NW>; ++k) {
+        const int ti = tri_tile<NW>(wf, k);
+        if (ti >= 0) {
+          const int rbk = ti >> 2, cbk = ti & 3;
+          f32x4 m = zero4();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 16 * rbk + 4 * g4 + e;
-          const float v = r >= i ? m[e] * __expf(s.gam[r] - gi) * di : 0.f;
-          s.M[r * LM + i] = from_f<T>(v);
+          for (int kb = 0; kb < K / 32; ++kb)
+            m = mfma16(row_frag(s.B, ok, 16 * cbk, 32 * kb), row_frag(s.C, ok, 16 * rbk, 32 * kb), m);
+          const int i = 16 * cbk + 4 * g4, r = 16 * rbk + col;
+          const f32x4 gi = *reinterpret_cast<const f32x4*>(&s.gam[b][i]);
+          const f32x4 di = *reinterpret_cast<const f32x4*>(&s.dts[b][i]);
+          const float gr = s.gam[b][r];
+          x4 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+          {
+            const float v = m[e] * exp2_fast(fminf(gr - gi[e], 0.f)) * di[e];
+            o[e] = from_f<T>(r >= i + e ? v : 0.f);
+          }
+          *row4(s.M, om, 16 * rbk, 16 * cbk) = o;
         }
       }
       // the state's part of the output, transposed: rows v, columns t
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[pt][r] = zero4();
+      for (int r = 0; r < 4; ++r) acc[r] = zero4();
+      float up = 1.f, down = 1.f;
+      if (kScaled) {
+        const int e = state_exponent<NT>(S);
+        up = ldexpf(1.f, e);
+        down = ldexpf(1.f, -e);
+      }
 #pragma unroll
       for (int kb = 0; kb < K / 32; ++kb) {
-        x8 sf[PT];
+        const x8 sf = kScaled ? pack_split<T>(S[2 * kb] * up, S[2 * kb + 1] * up)
+                              : pack_split<T>(S[2 * kb], S[2 * kb + 1]);
 #pragma unroll
-        for (int pt = 0; pt < PT; ++pt) sf[pt] = pack8<T>(S[pt][2 * kb], S[pt][2 * kb + 1]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const x8 cf = frag_row(s.C + 16 * r * LK + 32 * kb, LK);
-#pragma unroll
-          for (int pt = 0; pt < PT; ++pt) acc[pt][r] = mfma16(sf[pt], cf, acc[pt][r]);
-        }
+        for (int r = 0; r < 4; ++r)
+          acc[r] = mfma16(sf, split_frag(s.C, ok, 16 * r, 32 * kb), acc[r]);
+        if (kb % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float eg = s.eg[16 * r + col];
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt) acc[pt][r] *= eg;
-      }
+      for (int r = 0; r < 4; ++r) acc[r] *= s.eg[b][16 * r + col] * down;
       __syncthreads();
     }
+    if (c + 1 < nch) request(token(c + 1));
 
     // x^T fragments serve the product with M and, weighted, the state's
     // update; with fp16 the state's columns are scaled while it is added
-    const float decay = __expf(all);
-    x8 xf[2][PT];
-    float wt[2][8], scale[PT];
+    x8 xf[2];
 #pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
+    for (int tb = 0; tb < 2; ++tb) xf[tb] = tr_frag(s.X, ov, 32 * tb, v0);
+    if (OUT) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wt[tb][e] = s.wt[32 * tb + 8 * g4 + e];
+      for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-        xf[tb][pt] = frag_tr(s.X + 32 * tb * LV + w * (V / 4) + 16 * pt, LV);
+        for (int r = 2 * tb; r < 4; ++r)
+          acc[r] = mfma16(xf[tb], split_frag(s.M, om, 16 * r, 32 * tb), acc[r]);
     }
-#pragma unroll
-    for (int pt = 0; pt < PT; ++pt) {
-      scale[pt] = 1.f;
-      if (kScaled) {
-        float m = 0.f;
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(to_f(xf[tb][pt][e]) * wt[tb][e]));
-        scale[pt] = ldexpf(1.f, column_exponent(m));
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= decay * scale[pt];
-    }
-#pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
-      x8 hi[PT], lo[PT];
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-        if (OUT) {
-#pragma unroll
-          for (int r = 2 * tb; r < 4; ++r)
-            acc[pt][r] = mfma16(xf[tb][pt], frag_row(s.M + 16 * r * LM + 32 * tb, LM), acc[pt][r]);
-        }
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = to_f(xf[tb][pt][e]) * wt[tb][e] * scale[pt];
-        split8<T>(v, hi[pt], lo[pt]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const x8 bf = frag_tr_pair(s.B + 32 * tb * LK + 32 * (nt >> 1) + 4 * (nt & 1), LK);
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt) {
-          S[pt][nt] = mfma16(bf, hi[pt], S[pt][nt]);
-          S[pt][nt] = mfma16(bf, lo[pt], S[pt][nt]);
-        }
-      }
-    }
-    if (kScaled) {
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-        const float back = 1.f / scale[pt];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= back;
-      }
-    }
+    update_state<T, K>(S, s.B, ok, xf, s.wt[b], g4, s.decay[b]);
 
     if (OUT) {
-      typedef typename VT<T>::x4 x4;
-      struct __attribute__((packed, aligned(sizeof(T)))) Raw {
-        uint32_t u[2];
-      };
-      T* y = reinterpret_cast<T*>(a.y) + ((t * a.H) + h) * V;
+      T* y = reinterpret_cast<T*>(a.y) + (t * a.H + h) * V;
+      const int ys = a.H * V * (int)sizeof(T);
+      const auto rs = buf_rsrc(y, (int64_t)(rows_of(t) - 1) * ys + V * (int)sizeof(T));
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * r + col;
-        if (row < rows) {
+        const x4 xv = *row4(s.X, ov, 16 * r, v0);
+        x4 o;
 #pragma unroll
-          for (int pt = 0; pt < PT; ++pt) {
-            const int v0 = w * (V / 4) + 16 * pt + 4 * g4;
-            const x4 xv = *reinterpret_cast<const x4*>(s.X + row * LV + v0);
-            x4 o;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = from_f<T>(acc[pt][r][e] + skip * to_f(xv[e]));
-            *reinterpret_cast<Raw*>(y + (int64_t)row * a.H * V + v0) = __builtin_bit_cast(Raw, o);
-          }
-        }
+        for (int e = 0; e < 4; ++e) o[e] = from_f<T>(acc[r][e] + skip * to_f(xv[e]));
+        buf_store8(rs, row * ys + (v0 + 4 * g4) * (int)sizeof(T), __builtin_bit_cast(u32x2, o));
       }
+    }
+    if (w == NW - 1 && c + 1 < nch) {
+      gate(token(c + 1), b ^ 1);
+      if (c + 2 < nch) request_dt(token(c + 2));
     }
     __syncthreads();
   }
@@ -265,19 +221,14 @@ __global__ __launch_bounds__(kNT, 2) void ssm_walk_kernel(SsmArgs a) {
   if (!OUT) {
     float* dst = a.seg_state + slot;
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<f32x4*>(dst + (((w * PT + pt) * NT + nt) * 64 + l) * 4) = S[pt][nt];
-    if (threadIdx.x == 0) a.seg_decay[(int64_t)id * a.H + h] = total;
+    for (int nt = 0; nt < NT; ++nt)
+      *reinterpret_cast<f32x4*>(dst + ((w * NT + nt) * 64 + l) * 4) = S[nt];
+    if (w == NW - 1 && l == 0) a.seg_decay[(int64_t)id * a.H + h] = total;
   } else if (a.ht && sg.j + 1 == sg.count) {
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          a.ht[unit + (int64_t)state_k<V>(nt, e) * V + state_v<V>(w, pt)] = S[pt][nt][e];
+      for (int e = 0; e < 4; ++e) a.ht[unit + state_at(w, nt, e, V)] = S[nt][e];
   }
 }
 
@@ -309,7 +260,7 @@ __global__ __launch_bounds__(256) void ssm_combine_kernel(SsmArgs a) {
     constexpr int NT = K / 16;
     const int lane = (at >> 2) & 63, q = at >> 8, nt = q % NT, ct = q / NT;
     const int v = 16 * ct + (lane & 15);
-    const int k = 32 * (nt >> 1) + 8 * (lane >> 4) + 4 * (nt & 1);
+    const int k = 16 * nt + 4 * (lane >> 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) E[e] = a.h0[((int64_t)n * a.H + h) * K * V + (int64_t)(k + e) * V + v];
   }
@@ -457,10 +408,10 @@ void launch_ssm_states(const gdr_ssm_problem* p, const SsmArgs& a, bool grad, hi
     constexpr int K = k.value, V = v.value;
     const dim3 cgrid((unsigned)((int64_t)p->N * p->H * (K * V / 1024)));
     if (grad) {
-      GDR_LAUNCH("ssm_state_grad", (ssm_walk_kernel<T, K, V, kGrad>), grid, dim3(kNT), st, a);
+      GDR_LAUNCH("ssm_state_grad", (ssm_walk_kernel<T, K, V, kGrad>), grid, dim3(4 * V), st, a);
       GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, true>), cgrid, dim3(256), st, a);
     } else {
-      GDR_LAUNCH("ssm_state", (ssm_walk_kernel<T, K, V, kState>), grid, dim3(kNT), st, a);
+      GDR_LAUNCH("ssm_state", (ssm_walk_kernel<T, K, V, kState>), grid, dim3(4 * V), st, a);
       GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, false>), cgrid, dim3(256), st, a);
     }
   });
@@ -481,8 +432,8 @@ gdr_status launch_ssm_fwd(const gdr_ssm_problem* p, const SsmPlan& pl, const voi
   if (pl.split) launch_ssm_states(p, a, false, st);
   const dim3 grid((unsigned)((int64_t)pl.nids * p->H));
   ssm_by_shape(p, [&](auto t, auto k, auto v) {
-    GDR_LAUNCH("ssm_out", (ssm_walk_kernel<decltype(t), k.value, v.value, kOut>), grid, dim3(kNT),
-               st, a);
+    GDR_LAUNCH("ssm_out", (ssm_walk_kernel<decltype(t), k.value, v.value, kOut>), grid,
+               dim3(4 * v.value), st, a);
   });
   return launch_status("ssm_fwd");
 }
