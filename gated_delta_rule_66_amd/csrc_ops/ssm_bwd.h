@@ -263,13 +263,13 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
           if (hh == 0) {
 #pragma unroll
             for (int kb = 0; kb < K / 32; ++kb)
-              gt[k] = mfma16(row_frag(Q, ok, 16 * bb, 32 * kb), row_frag(P, ok, 16 * ab, 32 * kb),
+              gt[k] = mfma16(split_frag(Q, ok, 16 * bb, 32 * kb), split_frag(P, ok, 16 * ab, 32 * kb),
                              gt[k]);
           }
           f32x4 vt = zero4();
 #pragma unroll
           for (int kv = 0; kv < V / 32; ++kv)
-            vt = mfma16(row_frag(q, ov, 16 * bb, 32 * kv), row_frag(p, ov, 16 * ab, 32 * kv), vt);
+            vt = mfma16(split_frag(q, ov, 16 * bb, 32 * kv), split_frag(p, ov, 16 * ab, 32 * kv), vt);
           const int ia = 16 * ab + col, ib = 16 * bb + 4 * g4;
           const float gam_a = s.gam[b][ia], dt_a = s.dts[b][ia];
           const f32x4 gam_b = *reinterpret_cast<const f32x4*>(&s.gam[b][ib]);
@@ -404,8 +404,8 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
           const int r0 = (i >> 6) * 32, ar = r0 + (REV ? 16 : 0) + ((i >> 2) & 15),
                     bc = r0 + (REV ? 0 : 16) + 4 * (i & 3);
           const x4 z{};
-          *reinterpret_cast<x4*>(W + sw_off<64>(ar, bc)) = z;
-          *reinterpret_cast<x4*>(GL + sw_off<64>(ar, bc)) = z;
+          *reinterpret_cast<x4*>(W + unit_off<64>(ar, bc)) = z;
+          *reinterpret_cast<x4*>(GL + unit_off<64>(ar, bc)) = z;
         }
         __syncthreads();  // C: W and the decayed scores are in LDS
 

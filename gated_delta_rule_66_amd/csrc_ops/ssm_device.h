@@ -191,28 +191,36 @@ __device__ __forceinline__ void split8(const float* v, typename VT<T>::x8& hi,
   }
 }
 
-// Operand reads from swizzled tiles (sw_off).  The lane's byte offsets for the
-// three patterns are formed once; a tile's column offset is a multiple of 16
-// elements and enters by an exclusive or, its rows by an addition, so an
-// address costs at most one instruction.  hide() keeps the compiler from
-// forming all of them ahead of the chunk loop, which spills registers.
+// Tiles in LDS have unpadded rows of COLS (64 or 128) 16-bit elements whose
+// 8-byte units are permuted: unit u of row r sits at u ^ unit_swizzle(r).  An
+// operand read takes one unit of each of 16 rows, a transposing read four
+// neighbouring units of four rows; the LDS serves 16 lanes of 8 bytes (128
+// bytes, 32 banks) at a time, and either way these fall on all 32 banks
+// once: over 16 aligned rows the swizzle takes every value, and over four its
+// upper two bits do.  (Permuting 16-byte pieces, as 16-byte operand reads
+// need, left a third of the reads in two-way conflicts.)
+__device__ __forceinline__ int unit_swizzle(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+// element offset of (r, c), c a multiple of 4
+template <int COLS>
+__device__ __forceinline__ int unit_off(int r, int c) {
+  return COLS * r + 4 * ((c >> 2) ^ unit_swizzle(r));
+}
+
+// Operand reads.  The lane's byte offsets for the patterns are formed once; a
+// tile's column offset is a multiple of 16 elements and enters by an
+// exclusive or, its rows by an addition, so an address costs at most one
+// instruction.  hide() keeps the compiler from forming all of them ahead of
+// the chunk loop, which spills registers.
 template <int COLS>
 struct Sw {
-  int row, split, tr;
+  int split, tr;
   __device__ __forceinline__ Sw() {
     const int l = lane_id(), g = l >> 4, j = l & 15;
-    row = 2 * sw_off<COLS>(j, 8 * g % COLS);
-    split = 2 * sw_off<COLS>(j, 4 * g);
-    tr = 2 * sw_off<COLS>(4 * g + (j >> 2), 4 * (j & 3));
+    split = 2 * unit_off<COLS>(j, 4 * g);
+    tr = 2 * unit_off<COLS>(4 * g + (j >> 2), 4 * (j & 3));
   }
-  __device__ __forceinline__ void hide() { asm volatile("" : "+v"(row), "+v"(split), "+v"(tr)); }
+  __device__ __forceinline__ void hide() { asm volatile("" : "+v"(split), "+v"(tr)); }
 };
-// rows r0 + lane % 16, columns k0 + 8 (lane / 16) .. + 7
-template <typename T, int COLS>
-__device__ __forceinline__ typename VT<T>::x8 row_frag(const T* X, const Sw<COLS>& o, int r0, int k0) {
-  return *reinterpret_cast<const typename VT<T>::x8*>(reinterpret_cast<const char*>(X) +
-                                                       2 * COLS * r0 + (o.row ^ (2 * k0)));
-}
 // four elements of row r0 + lane % 16 from column c0 + 4 (lane / 16)
 template <typename T, int COLS>
 __device__ __forceinline__ const typename VT<T>::x4* row4(const T* X, const Sw<COLS>& o, int r0,
@@ -225,7 +233,7 @@ __device__ __forceinline__ typename VT<T>::x4* row4(T* X, const Sw<COLS>& o, int
   return reinterpret_cast<typename VT<T>::x4*>(reinterpret_cast<char*>(X) + 2 * COLS * r0 +
                                                (o.split ^ (2 * c0)));
 }
-// the same rows in split k order
+// rows r0 + lane % 16 as an operand in split k order
 template <typename T, int COLS>
 __device__ __forceinline__ typename VT<T>::x8 split_frag(const T* X, const Sw<COLS>& o, int r0,
                                                          int k0) {
@@ -335,9 +343,15 @@ struct Rows64 {
     for (int i = 0; i < kPer; ++i) r[i] = buf_load16(rs, off + i * (kStep * sb));
   }
   __device__ __forceinline__ void store(T* lds) const {
-    T* p = lds + sw_off<COLS>((int)threadIdx.x / kRow, (int)threadIdx.x % kRow * 8);
+    char* p = reinterpret_cast<char*>(lds) +
+              2 * unit_off<COLS>((int)threadIdx.x / kRow, (int)threadIdx.x % kRow * 8);
+    char* o = reinterpret_cast<char*>(lds) +
+              2 * unit_off<COLS>((int)threadIdx.x / kRow, (int)threadIdx.x % kRow * 8 + 4);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(p + i * kStep * COLS) = r[i];
+    for (int i = 0; i < kPer; ++i) {
+      *reinterpret_cast<uint2*>(p + 2 * i * kStep * COLS) = make_uint2(r[i].x, r[i].y);
+      *reinterpret_cast<uint2*>(o + 2 * i * kStep * COLS) = make_uint2(r[i].z, r[i].w);
+    }
   }
 };
 

@@ -39,7 +39,7 @@ struct WalkSmem {
 // and registers and hide each other's barriers.
 enum { kOut, kState, kGrad };
 template <typename T, int K, int V, int MODE>
-__global__ __launch_bounds__(4 * V, 3) void ssm_walk_kernel(SsmArgs a) {
+__global__ __launch_bounds__(4 * V, V == 64 ? 3 : 4) void ssm_walk_kernel(SsmArgs a) {
   typedef typename VT<T>::x8 x8;
   typedef typename VT<T>::x4 x4;
   constexpr int NW = V / 16, NTH = 64 * NW, NT = K / 16;
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(4 * V, 3) void ssm_walk_kernel(SsmArgs a) {
   }
   if (OUT) {  // tiles above the diagonal that the product with M reads: (0, 1) and (2, 3)
     for (int i = threadIdx.x; i < 512; i += NTH)
-      s.M[sw_off<64>((i >> 8) * 32 + ((i >> 4) & 15), (i >> 8) * 32 + 16 + (i & 15))] = (T)0.f;
+      s.M[unit_off<64>((i >> 8) * 32 + ((i >> 4) & 15), (i >> 8) * 32 + 16 + (i & 12)) + (i & 3)] = (T)0.f;
   }
 
   const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
@@ -134,48 +134,54 @@ __global__ __launch_bounds__(4 * V, 3) void ssm_walk_kernel(SsmArgs a) {
 
     f32x4 acc[4];
     if (OUT) {
-      // M = (C B^T) o L diag(dt), rounded to T as an operand; its tiles are
-      // formed transposed, so that a lane holds four neighbours of a row
+      // The state's part of the output, transposed (rows v, columns t), and
+      // the scores of the wave's column block of tokens: they share C's
+      // operands.
+      f32x4 sc[4];
 #pragma unroll
-      for (int k = 0; k < kMostTiles<NW>; ++k) {
-        const int ti = tri_tile<NW>(wf, k);
-        if (ti >= 0) {
-          const int rbk = ti >> 2, cbk = ti & 3;
-          f32x4 m = zero4();
-#pragma unroll
-          for (int kb = 0; kb < K / 32; ++kb)
-            m = mfma16(row_frag(s.B, ok, 16 * cbk, 32 * kb), row_frag(s.C, ok, 16 * rbk, 32 * kb), m);
-          const int i = 16 * cbk + 4 * g4, r = 16 * rbk + col;
-          const f32x4 gi = *reinterpret_cast<const f32x4*>(&s.gam[b][i]);
-          const f32x4 di = *reinterpret_cast<const f32x4*>(&s.dts[b][i]);
-          const float gr = s.gam[b][r];
-          x4 o;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-          {
-            const float v = m[e] * exp2_fast(fminf(gr - gi[e], 0.f)) * di[e];
-            o[e] = from_f<T>(r >= i + e ? v : 0.f);
-          }
-          *row4(s.M, om, 16 * rbk, 16 * cbk) = o;
-        }
-      }
-      // the state's part of the output, transposed: rows v, columns t
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = zero4();
+      for (int r = 0; r < 4; ++r) acc[r] = sc[r] = zero4();
       float up = 1.f, down = 1.f;
       if (kScaled) {
         const int e = state_exponent<NT>(S);
         up = ldexpf(1.f, e);
         down = ldexpf(1.f, -e);
       }
+      // score tiles (row blocks) of this wave: the block's column is w % 4; of
+      // eight waves, two share a column's tiles
+      const int cb = wf & 3, mine = (NW == 8 ? (5 - cb) >> 1 : 4);
+      const int r0 = NW == 8 && wf >= 4 ? cb + mine : cb;
+      const int r1 = NW == 8 && wf < 4 ? cb + mine : 4;
 #pragma unroll
       for (int kb = 0; kb < K / 32; ++kb) {
         const x8 sf = kScaled ? pack_split<T>(S[2 * kb] * up, S[2 * kb + 1] * up)
                               : pack_split<T>(S[2 * kb], S[2 * kb + 1]);
+        const x8 bf = split_frag(s.B, ok, 16 * cb, 32 * kb);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[r] = mfma16(sf, split_frag(s.C, ok, 16 * r, 32 * kb), acc[r]);
+        for (int r = 0; r < 4; ++r) {
+          const x8 cf = split_frag(s.C, ok, 16 * r, 32 * kb);
+          acc[r] = mfma16(sf, cf, acc[r]);
+          if (r >= r0 && r < r1) sc[r] = mfma16(bf, cf, sc[r]);
+        }
         if (kb % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+      }
+      // M = (C B^T) o L diag(dt), rounded to T as an operand; its tiles are
+      // transposed, so that a lane holds four neighbours of a row
+      const int i = 16 * cb + 4 * g4;
+      const f32x4 gi = *reinterpret_cast<const f32x4*>(&s.gam[b][i]);
+      const f32x4 di = *reinterpret_cast<const f32x4*>(&s.dts[b][i]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r >= r0 && r < r1) {
+          const int row = 16 * r + col;
+          const float gr = s.gam[b][row];
+          x4 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = sc[r][e] * exp2_fast(fminf(gr - gi[e], 0.f)) * di[e];
+            o[e] = from_f<T>(row >= i + e ? v : 0.f);
+          }
+          *row4(s.M, om, 16 * r, 16 * cb) = o;
+        }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[r] *= s.eg[b][16 * r + col] * down;
