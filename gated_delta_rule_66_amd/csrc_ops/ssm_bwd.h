@@ -404,8 +404,8 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
           const int r0 = (i >> 6) * 32, ar = r0 + (REV ? 16 : 0) + ((i >> 2) & 15),
                     bc = r0 + (REV ? 0 : 16) + 4 * (i & 3);
           const x4 z{};
-          *reinterpret_cast<x4*>(W + unit_off<64>(ar, bc)) = z;
-          *reinterpret_cast<x4*>(GL + unit_off<64>(ar, bc)) = z;
+          *reinterpret_cast<x4*>(W + sw_off<64>(ar, bc)) = z;
+          *reinterpret_cast<x4*>(GL + sw_off<64>(ar, bc)) = z;
         }
         __syncthreads();  // C: W and the decayed scores are in LDS
 

@@ -191,21 +191,11 @@ __device__ __forceinline__ void split8(const float* v, typename VT<T>::x8& hi,
   }
 }
 
-// Tiles in LDS have unpadded rows of COLS (64 or 128) 16-bit elements whose
-// 8-byte units are permuted: unit u of row r sits at u ^ unit_swizzle(r).  An
-// operand read takes one unit of each of 16 rows, a transposing read four
-// neighbouring units of four rows; the LDS serves 16 lanes of 8 bytes (128
-// bytes, 32 banks) at a time, and either way these fall on all 32 banks
-// once: over 16 aligned rows the swizzle takes every value, and over four its
-// upper two bits do.  (Permuting 16-byte pieces, as 16-byte operand reads
-// need, left a third of the reads in two-way conflicts.)
-__device__ __forceinline__ int unit_swizzle(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
-// element offset of (r, c), c a multiple of 4
-template <int COLS>
-__device__ __forceinline__ int unit_off(int r, int c) {
-  return COLS * r + 4 * ((c >> 2) ^ unit_swizzle(r));
-}
-
+// Tiles in LDS have unpadded rows with their 16-byte pieces permuted (sw_off).
+// All operands are read 8 bytes a lane, rows in split k order or transposed:
+// measured, both then run at the rate of linear reads (a wave's 512 bytes in
+// 1.7 counter ticks), while 16-byte row operands (4.5 against 2.7 linear) and
+// tiles permuted by 8-byte units (2.8 against 1.7) do not.
 // Operand reads.  The lane's byte offsets for the patterns are formed once; a
 // tile's column offset is a multiple of 16 elements and enters by an
 // exclusive or, its rows by an addition, so an address costs at most one
@@ -216,8 +206,8 @@ struct Sw {
   int split, tr;
   __device__ __forceinline__ Sw() {
     const int l = lane_id(), g = l >> 4, j = l & 15;
-    split = 2 * unit_off<COLS>(j, 4 * g);
-    tr = 2 * unit_off<COLS>(4 * g + (j >> 2), 4 * (j & 3));
+    split = 2 * sw_off<COLS>(j, 4 * g);
+    tr = 2 * sw_off<COLS>(4 * g + (j >> 2), 4 * (j & 3));
   }
   __device__ __forceinline__ void hide() { asm volatile("" : "+v"(split), "+v"(tr)); }
 };
@@ -343,15 +333,9 @@ struct Rows64 {
     for (int i = 0; i < kPer; ++i) r[i] = buf_load16(rs, off + i * (kStep * sb));
   }
   __device__ __forceinline__ void store(T* lds) const {
-    char* p = reinterpret_cast<char*>(lds) +
-              2 * unit_off<COLS>((int)threadIdx.x / kRow, (int)threadIdx.x % kRow * 8);
-    char* o = reinterpret_cast<char*>(lds) +
-              2 * unit_off<COLS>((int)threadIdx.x / kRow, (int)threadIdx.x % kRow * 8 + 4);
+    T* p = lds + sw_off<COLS>((int)threadIdx.x / kRow, (int)threadIdx.x % kRow * 8);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      *reinterpret_cast<uint2*>(p + 2 * i * kStep * COLS) = make_uint2(r[i].x, r[i].y);
-      *reinterpret_cast<uint2*>(o + 2 * i * kStep * COLS) = make_uint2(r[i].z, r[i].w);
-    }
+    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(p + i * kStep * COLS) = r[i];
   }
 };
 

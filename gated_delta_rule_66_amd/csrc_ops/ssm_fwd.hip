@@ -9,6 +9,7 @@
 // ssm_combine_kernel adds them up along each sequence, and ssm_out_kernel
 // walks each segment from its start state.
 #include <algorithm>
+#include <cmath>
 
 #include "ssm_device.h"
 
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 3 : 4) void ssm_walk_kernel(SsmArg
   }
   if (OUT) {  // tiles above the diagonal that the product with M reads: (0, 1) and (2, 3)
     for (int i = threadIdx.x; i < 512; i += NTH)
-      s.M[unit_off<64>((i >> 8) * 32 + ((i >> 4) & 15), (i >> 8) * 32 + 16 + (i & 12)) + (i & 3)] = (T)0.f;
+      s.M[sw_off<64>((i >> 8) * 32 + ((i >> 4) & 15), (i >> 8) * 32 + 16 + (i & 15))] = (T)0.f;
   }
 
   const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
@@ -371,25 +372,57 @@ SsmArgs ssm_args(const gdr_ssm_problem* p, const SsmPlan& pl) {
 }
 
 // How sequences are cut for a launch with `per_seg` workgroups for each
-// segment, of which `slots` run at once.  Uncut, it takes the longest
-// sequence's chunks; cut, every chunk's x and B are read once more and two
+// segment, of which `slots` run at once: the segment length, in chunks, of
+// least cost.  Workgroups run in rounds of `slots`; a round takes its
+// segments' chunks and about 1.5 chunks for the states at both ends, a last
+// round that fills a share f of the slots (0.45 + 0.55 f) of that (a CU's
+// workgroups share its units: one alone takes 3 us a chunk, three 7).  Cut,
+// every chunk's x and B are read once more for 0.4 of a chunk, and two
 // launches are added, worth about four chunks.
 SsmPlan ssm_plan(const gdr_ssm_problem* p, int64_t per_seg, int64_t slots) {
-  int64_t chunks = 0, longest = 0, tokens = 0;
-  for (int n = 0; n < (p->cu_seqlens_host ? p->N : 1); ++n) {
+  int64_t longest = 0, tokens = 0;
+  const int seqs = p->cu_seqlens_host ? p->N : 1;
+  auto chunks_of = [&](int n) {
     const int64_t len = p->cu_seqlens_host
                             ? (int64_t)p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n]
                             : p->T;
-    chunks += (len + 63) / 64;
-    longest = std::max(longest, (len + 63) / 64);
-    tokens += len;
+    return (len + 63) / 64;
+  };
+  for (int n = 0; n < seqs; ++n) longest = std::max(longest, chunks_of(n));
+  if (p->cu_seqlens_host) tokens = p->T;
+  longest = std::max<int64_t>(1, longest);
+  const int64_t copies = p->cu_seqlens_host ? 1 : p->B;
+  auto rounds = [&](double wgs) {
+    const double full = std::floor(wgs / slots), f = wgs / slots - full;
+    return full + (f > 0.0 ? 0.45 + 0.55 * f : 0.0);
+  };
+  // every length up to 32 chunks, then steps of about an eighth, and no cut
+  int64_t best_sc = longest;
+  double best = 1e300;
+  for (int64_t sc = std::min<int64_t>(4, longest);;) {
+    int64_t segs = 0, work = 0;
+    for (int n = 0; n < seqs; ++n) {
+      const int64_t c = chunks_of(n);
+      segs += std::max<int64_t>(1, (c + sc - 1) / sc);
+      work += c;
+    }
+    const double wgs = (double)(segs * copies * per_seg);
+    const bool cut = sc < longest;
+    // unequal segments: no shorter than the longest, no less than the work
+    const double mean = (double)work / (double)segs;
+    const double r = rounds(wgs);
+    const double one = std::max((double)sc, r * mean) + 1.5 * std::max(1.0, r);
+    const double cost = (r <= 1.0 ? r * (sc + 1.5) : one) * (cut ? 1.4 : 1.0) + (cut ? 4.0 : 0.0);
+    if (cost < best) {
+      best = cost;
+      best_sc = sc;
+    }
+    if (sc == longest) break;
+    sc = std::min(longest, sc < 32 ? sc + 1 : sc + sc / 8);
   }
-  if (!p->cu_seqlens_host) chunks *= p->B;
-  const int64_t ideal = std::max<int64_t>(4, (chunks * per_seg + slots - 1) / slots);
   SsmPlan pl;
-  pl.split = 2 * longest > 3 * ideal + 8;
-  int64_t sc = pl.split ? ideal : std::max<int64_t>(1, longest);
-  pl.seg = (int)(sc * 64);
+  pl.split = best_sc < longest;
+  pl.seg = (int)(best_sc * 64);
   pl.nids = p->cu_seqlens_host ? (int)(p->N + tokens / pl.seg)
                                : (int)(p->B * ((p->T + (int64_t)pl.seg - 1) / pl.seg));
   return pl;
