@@ -2,18 +2,19 @@
 #pragma once
 
 #include "../csrc/gdr_device.h"
+#include "../csrc/gdr_internal.h"
 
 namespace gdr {
 
-// Eight (16-bit) or four (fp32) consecutive elements, 16 bytes.  Rows of odd
-// width start at any element, so the access promises only the element's own
+// N consecutive elements, 8 or 16 bytes (by default 16).  Rows of odd width
+// start at any element, so the access promises only the element's own
 // alignment: global memory takes 16-byte loads and stores at any address (the
 // compiler emits one global_load_dwordx4 either way).
-template <typename T>
+template <typename T, int N = 16 / (int)sizeof(T)>
 struct Vec {
-  static constexpr int n = 16 / sizeof(T);
+  static constexpr int n = N;
   struct __attribute__((packed, aligned(sizeof(T)))) Raw {
-    uint32_t u[4];
+    uint32_t u[N * sizeof(T) / 4];
   };
   T v[n];
 
@@ -23,6 +24,10 @@ struct Vec {
   }
   __device__ __forceinline__ void store(T* p) const {
     *reinterpret_cast<Raw*>(p) = __builtin_bit_cast(Raw, *this);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < n; ++e) v[e] = (T)0.f;
   }
   // the first m elements (the row's end); the others are zero
   __device__ __forceinline__ void load_part(const T* p, int m) {
@@ -43,6 +48,25 @@ struct Vec {
       if (e < m) p[e] = v[e];
   }
 };
+
+// COUNT (a multiple of 4) consecutive values of a parameter held in 16 bits
+// or fp32
+template <typename T, int COUNT>
+__device__ __forceinline__ void load_values(const T* p, float* f) {
+#pragma unroll
+  for (int k = 0; k < COUNT; k += 4) {
+    Vec<T, 4> v;
+    v.load(p + k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[k + e] = to_f(v.v[e]);
+  }
+}
+template <int COUNT>
+__device__ __forceinline__ void load_params(const void* p, int64_t i, int dtype, float* f) {
+  if (dtype == GDR_BF16) load_values<__bf16, COUNT>(reinterpret_cast<const __bf16*>(p) + i, f);
+  else if (dtype == GDR_FP16) load_values<_Float16, COUNT>(reinterpret_cast<const _Float16*>(p) + i, f);
+  else load_values<float, COUNT>(reinterpret_cast<const float*>(p) + i, f);
+}
 
 // n consecutive values of a parameter held in 16 bits or fp32
 __device__ __forceinline__ float load_param(const void* p, int64_t i, int dtype) {
