@@ -106,7 +106,7 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
 
   // start states: the forward walk's from the segment before (or h0), the
   // backward walk's from the segment after (or dht)
-  f32x4 S[HPW][NT];
+  f32x4 S[HPW][1][NT];
   const int64_t KV = (int64_t)K * V;
   auto load_slot = [&](const float* p, int id_, int h, f32x4* dst) {
     const float* src = p + ((int64_t)id_ * a.H + h) * KV;
@@ -129,16 +129,16 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
   for (int hh = 0; hh < HPW; ++hh) {
     if (hh < nh) {
       const int h = head0 + hh;
-      if (REV) end_grad(h, S[hh]);
-      else if (sg.j > 0) load_slot(a.seg_state, id - 1, h, S[hh]);
-      else load_user(a.h0, h, S[hh]);
+      if (REV) end_grad(h, S[hh][0]);
+      else if (sg.j > 0) load_slot(a.seg_state, id - 1, h, S[hh][0]);
+      else load_user(a.h0, h, S[hh][0]);
       if (kScaled) {
-        const int e = state_exponent<NT>(S[hh]);
+        const int e = state_exponent<NT>(S[hh][0]);
         if (l == 0) s.ex[hh][w] = e;
       }
     } else {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) S[hh][nt] = zero4();
+      for (int nt = 0; nt < NT; ++nt) S[hh][0][nt] = zero4();
     }
   }
 
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
       for (int nt = 0; nt < NT; ++nt) {
         x4 z;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = from_f<T>(kScaled ? S[hh][nt][e] * up : S[hh][nt][e]);
+        for (int e = 0; e < 4; ++e) z[e] = from_f<T>(kScaled ? S[hh][0][nt][e] * up : S[hh][0][nt][e]);
         *row4(s.R, ok, v0, 16 * nt) = z;
       }
       __syncthreads();  // A: tiles, gate and state columns are in LDS
@@ -331,8 +331,8 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
         float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[e] = kScaled ? S[hh][2 * kb][e] * up : S[hh][2 * kb][e];
-          v[4 + e] = kScaled ? S[hh][2 * kb + 1][e] * up : S[hh][2 * kb + 1][e];
+          v[e] = kScaled ? S[hh][0][2 * kb][e] * up : S[hh][0][2 * kb][e];
+          v[4 + e] = kScaled ? S[hh][0][2 * kb + 1][e] * up : S[hh][0][2 * kb + 1][e];
         }
         x8 hi, lo;
         split8<T>(v, hi, lo);
@@ -356,17 +356,17 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
       }
 
       // the state's update
-      x8 xf[2];
+      x8 xf[2][1];
 #pragma unroll
-      for (int tb = 0; tb < 2; ++tb) xf[tb] = tr_frag(q, ov, 32 * tb, v0);
-      update_state<T, K>(S[hh], Q, ok, xf, REV ? s.eg[b] : s.wt[b], g4, s.decay[b]);
+      for (int tb = 0; tb < 2; ++tb) xf[tb][0] = tr_frag(q, ov, 32 * tb, v0);
+      update_state<T, K, 1>(S[hh], Q, ok, xf, REV ? s.eg[b] : s.wt[b], g4, s.decay[b]);
       __syncthreads();  // B: the state columns are read, the partial sums written
 
       if (!last) request_xy(c, hh + 1);
       else if (c + 1 < nch) request_xy(c + 1, 0);
       if (last && c + 1 < nch) request_bc(c + 1);
       if (kScaled) {
-        const int e = state_exponent<NT>(S[hh]);
+        const int e = state_exponent<NT>(S[hh][0]);
         if (l == 0) s.ex[hh][w] = e;
       }
       if (w == 0 && l < rows) {
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
           for (int r = 0; r < 4; ++r) {
 #pragma unroll
             for (int sb = r >> 1; sb < 2; ++sb)
-              u[r] = mfma16(xf[sb], split_frag(GL, om, 16 * r, 32 * sb), u[r]);
+              u[r] = mfma16(xf[sb][0], split_frag(GL, om, 16 * r, 32 * sb), u[r]);
             const int row = 16 * r + col;
             const float di = s.dts[b][row];
             const x4 yv = *row4(s.Y, ov, 16 * r, v0);
@@ -478,7 +478,7 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            ga.dh0[((int64_t)sg.n * a.H + h) * KV + state_at(w, nt, e, V)] = S[hh][nt][e];
+            ga.dh0[((int64_t)sg.n * a.H + h) * KV + state_at(w, nt, e, V)] = S[hh][0][nt][e];
       }
       const float d = wave_sum(dsum[hh]);
       if (l == 0) s.fin[hh][w] = d;
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(4 * V, K * V >= 8192 ? 2 : (V == 64 ? 3 : 4)) void 
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d += S[hh][nt][e] * E[nt][e];
+        for (int e = 0; e < 4; ++e) d += S[hh][0][nt][e] * E[nt][e];
       d = wave_sum(d);
       if (l == 0) s.fin[hh][w] = d;
     }

@@ -269,49 +269,62 @@ __device__ __forceinline__ void weighted(const typename VT<T>::x8& xf, const flo
   for (int e = 0; e < 8; ++e) v[e] = to_f(xf[e]) * (e < 4 ? w0[e & 3] : w1[e & 3]);
 }
 
-// S <- decay S + A^T diag(wt) x over a chunk's 64 tokens: A a swizzled 64 x K
-// tile, xf the lane's column of x in two blocks of 32 tokens, wt in LDS.  The
-// weighted values go in as a pair of 16-bit operands; with fp16 the columns
-// are scaled to fit.
-template <typename T, int K>
-__device__ __forceinline__ void update_state(f32x4* S, const T* A, const Sw<K>& o,
-                                             const typename VT<T>::x8* xf, const float* wt, int g4,
-                                             float decay) {
+// S <- decay S + A^T diag(wt) x over a chunk's 64 tokens, for PT blocks of 16
+// columns: A a swizzled 64 x K tile, xf[tb][pt] the lane's column of x in two
+// blocks of 32 tokens, wt in LDS.  The weighted values go in as a pair of
+// 16-bit operands; with fp16 the columns are scaled to fit.
+template <typename T, int K, int PT>
+__device__ __forceinline__ void update_state(f32x4 (&S)[PT][K / 16], const T* A, const Sw<K>& o,
+                                             const typename VT<T>::x8 (&xf)[2][PT], const float* wt,
+                                             int g4, float decay) {
   constexpr int NT = K / 16;
   constexpr bool kScaled = !__is_same(T, __bf16);
-  float scale = 1.f;
-  if (kScaled) {
-    float m = 0.f;
+  float scale[PT];
 #pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
-      float v[8];
-      weighted<T>(xf[tb], wt, tb, g4, 1.f, v);
+  for (int pt = 0; pt < PT; ++pt) {
+    scale[pt] = 1.f;
+    if (kScaled) {
+      float m = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+      for (int tb = 0; tb < 2; ++tb) {
+        float v[8];
+        weighted<T>(xf[tb][pt], wt, tb, g4, 1.f, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+      }
+      scale[pt] = ldexpf(1.f, column_exponent(m));
     }
-    scale = ldexpf(1.f, column_exponent(m));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= kScaled ? decay * scale[pt] : decay;
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) S[nt] *= kScaled ? decay * scale : decay;
-#pragma unroll
   for (int tb = 0; tb < 2; ++tb) {
-    typename VT<T>::x8 hi, lo;
-    float v[8];
-    weighted<T>(xf[tb], wt, tb, g4, scale, v);
-    split8<T>(v, hi, lo);
+    typename VT<T>::x8 hi[PT], lo[PT];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) {
+      float v[8];
+      weighted<T>(xf[tb][pt], wt, tb, g4, scale[pt], v);
+      split8<T>(v, hi[pt], lo[pt]);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const auto f = tr_frag(A, o, 32 * tb, 16 * nt);
-      S[nt] = mfma16(f, hi, S[nt]);
-      S[nt] = mfma16(f, lo, S[nt]);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        S[pt][nt] = mfma16(f, hi[pt], S[pt][nt]);
+        S[pt][nt] = mfma16(f, lo[pt], S[pt][nt]);
+      }
       // a few operands in flight, not all of them: registers
-      if (nt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      if (nt % (4 / PT) == 4 / PT - 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (kScaled) {
-    const float back = 1.f / scale;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) S[nt] *= back;
+    for (int pt = 0; pt < PT; ++pt) {
+      const float back = 1.f / scale[pt];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= back;
+    }
   }
 }
 
@@ -324,8 +337,10 @@ struct Rows64 {
   static constexpr int kPer = 64 * COLS / 8 / NT, kRow = COLS / 8, kStep = NT / kRow;
   static_assert(kStep % 16 == 0, "a thread's rows share their swizzle");
   uint4 r[kPer];
-  __device__ __forceinline__ void load(const T* g, int64_t stride, int rows) {
-    const auto rs = buf_rsrc(g, ((rows - 1) * stride + COLS) * (int64_t)sizeof(T));
+  // `cols` of a row's COLS elements exist (the others of the last row read as
+  // zero, of the rows before it as whatever follows)
+  __device__ __forceinline__ void load(const T* g, int64_t stride, int rows, int cols = COLS) {
+    const auto rs = buf_rsrc(g, ((rows - 1) * stride + cols) * (int64_t)sizeof(T));
     const int sb = (int)stride * (int)sizeof(T);
     int off = (int)threadIdx.x / kRow * sb + (int)threadIdx.x % kRow * 16;
     asm volatile("" : "+v"(off));
@@ -357,12 +372,12 @@ __device__ __forceinline__ int tri_tile(int w, int s) {
 template <int NW>
 constexpr int kMostTiles = NW == 4 ? 3 : 2;
 
-// State element (k, v) of register e of tile nt in wave w: k = 16 nt + 4 (lane
-// / 16) + e, v = 16 w + lane % 16 (the accumulator layout; two stacked tiles
-// are an operand in split k order).
-__device__ __forceinline__ int state_at(int w, int nt, int e, int V) {
+// State element (k, v) of register e of tile nt in column block ct: k = 16 nt +
+// 4 (lane / 16) + e, v = 16 ct + lane % 16 (the accumulator layout; two stacked
+// tiles are an operand in split k order).
+__device__ __forceinline__ int state_at(int ct, int nt, int e, int V) {
   const int l = lane_id();
-  return (16 * nt + 4 * (l >> 4) + e) * V + 16 * w + (l & 15);
+  return (16 * nt + 4 * (l >> 4) + e) * V + 16 * ct + (l & 15);
 }
 
 // token of element e of lane group g4's operand in split k order

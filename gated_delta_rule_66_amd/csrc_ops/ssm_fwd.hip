@@ -17,14 +17,14 @@ namespace gdr {
 
 namespace {
 
-template <typename T, int K, int V>
+template <typename T, int K, int V, int HPW>
 struct WalkSmem {
   T C[64 * K];
   T B[64 * K];
-  T X[64 * V];
-  T M[64 * 64];
-  float gam[2][64];  // in powers of two
-  float eg[2][64], wt[2][64], dts[2][64], decay[2];
+  T X[64 * HPW * V];
+  T M[HPW][64 * 64];
+  float gam[HPW][2][64];  // in powers of two
+  float eg[HPW][2][64], wt[HPW][2][64], dts[HPW][2][64], decay[HPW][2];
 };
 
 // kOut: the segment's outputs from its start state.  kState: what it adds to
@@ -32,69 +32,86 @@ struct WalkSmem {
 // same with dy and C for x and B (the caller passes them so), e^gamma for the
 // weights, and the chunks from the last to the first.
 //
-// V / 16 waves, each with 16 state columns in accumulators.  Per chunk, the
-// tiles of the next one are in registers (in flight), those of this one in
-// LDS, swizzled so that row operands and transposing reads are free of bank
-// conflicts; the last wave, which has the fewest score tiles, forms the next
-// chunk's gate.  Three (V = 64) or two (V = 128) workgroups share a CU's LDS
-// and registers and hide each other's barriers.
+// A workgroup walks HPW heads of one group, which share the B and C tiles and
+// the scores C B^T; each wave holds 16 PT columns of one head's state in
+// accumulators and reads every operand of B and C once for them.  Per chunk,
+// the tiles of the next one are in registers (in flight), those of this one
+// in LDS, swizzled so that no operand read has bank conflicts; the last waves,
+// which have the fewest score tiles, form the next chunk's gates.
 enum { kOut, kState, kGrad };
-template <typename T, int K, int V, int MODE>
-__global__ __launch_bounds__(4 * V, V == 64 ? 3 : 4) void ssm_walk_kernel(SsmArgs a) {
+template <typename T, int K, int V, int HPW, int PT, int MODE>
+__global__ __launch_bounds__(4 * HPW * V / PT, HPW * PT == 1 ? 3 : 2) void ssm_walk_kernel(SsmArgs a) {
   typedef typename VT<T>::x8 x8;
   typedef typename VT<T>::x4 x4;
-  constexpr int NW = V / 16, NTH = 64 * NW, NT = K / 16;
+  constexpr int NW = HPW * V / (16 * PT), WPH = NW / HPW, NTH = 64 * NW, NT = K / 16;
+  constexpr int XC = HPW * V;  // columns of the x tile
   constexpr bool OUT = MODE == kOut;
   constexpr bool kScaled = !__is_same(T, __bf16);
-  __shared__ __align__(16) WalkSmem<T, K, V> s;
+  static_assert(NW == 4 || NW == 8, "score tiles are dealt to four or eight waves");
+  __shared__ __align__(16) WalkSmem<T, K, V, HPW> s;
+  const int R = a.H / a.G, slots = (R + HPW - 1) / HPW;
   const int L = xcd_order(blockIdx.x, gridDim.x);
-  const int id = L / a.H, h = L % a.H, grp_h = h / (a.H / a.G);
+  const int part = L % slots, grp_h = L / slots % a.G, id = L / (slots * a.G);
+  const int head0 = grp_h * R + part * HPW, nh = min(HPW, R - part * HPW);
   const Segment sg = segment_of(a, id);
   if (sg.count == 0) return;
   if (MODE == kState && sg.j + 1 >= sg.count) return;
   if (MODE == kGrad && sg.j == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
+  const int hw = w / WPH, ct0 = w % WPH * PT, h = head0 + min(hw, nh - 1);
+  const bool active = hw < nh;
 
-  const T* xg = reinterpret_cast<const T*>(a.x) + (int64_t)h * V;
+  const T* xg = reinterpret_cast<const T*>(a.x) + (int64_t)head0 * V;
   const T* bg = reinterpret_cast<const T*>(a.B) + (int64_t)grp_h * K;
   const T* cg = reinterpret_cast<const T*>(a.C) + (int64_t)grp_h * K;
-  const float rate = -expf(load_scalar(a.A_log, h, a.p_dtype));
-  const float bias = param(a.dt_bias, h, a.p_dtype), skip = param(a.D, h, a.p_dtype);
+  const float skip = param(a.D, h, a.p_dtype);
+  // the head whose gate this wave forms, if it is one of the last waves
+  const int gh = NW - 1 - w, ghead = head0 + min(gh, nh - 1);
+  const bool gates = gh < nh;
+  const float rate = -expf(load_scalar(a.A_log, ghead, a.p_dtype));
+  const float bias = param(a.dt_bias, ghead, a.p_dtype);
 
-  f32x4 S[NT];
+  f32x4 S[PT][NT];
   const int64_t unit = ((int64_t)sg.n * a.H + h) * K * V;
   const int64_t slot = ((int64_t)id * a.H + h) * K * V;
-  if (OUT && sg.j > 0) {
-    const float* src = a.seg_state + slot - (int64_t)a.H * K * V;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      S[nt] = *reinterpret_cast<const f32x4*>(src + ((w * NT + nt) * 64 + l) * 4);
-  } else {
-    const bool from = OUT && a.h0;
+  for (int pt = 0; pt < PT; ++pt) {
+    if (OUT && sg.j > 0) {
+      const float* src = a.seg_state + slot - (int64_t)a.H * K * V;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
+        S[pt][nt] = *reinterpret_cast<const f32x4*>(src + (((ct0 + pt) * NT + nt) * 64 + l) * 4);
+    } else {
+      const bool from = OUT && a.h0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] = from ? a.h0[unit + state_at(w, nt, e, V)] : 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          S[pt][nt][e] = from ? a.h0[unit + state_at(ct0 + pt, nt, e, V)] : 0.f;
+    }
   }
   if (OUT) {  // tiles above the diagonal that the product with M reads: (0, 1) and (2, 3)
-    for (int i = threadIdx.x; i < 512; i += NTH)
-      s.M[sw_off<64>((i >> 8) * 32 + ((i >> 4) & 15), (i >> 8) * 32 + 16 + (i & 15))] = (T)0.f;
+    for (int i = threadIdx.x; i < 512 * HPW; i += NTH) {
+      const int k = i & 511;
+      s.M[i >> 9][sw_off<64>((k >> 8) * 32 + ((k >> 4) & 15), (k >> 8) * 32 + 16 + (k & 15))] =
+          (T)0.f;
+    }
   }
 
   const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
   auto token = [&](int c) { return sg.t0 + 64ll * (MODE == kGrad ? nch - 1 - c : c); };
   auto rows_of = [&](int64_t t) { return (int)min((int64_t)64, sg.t1 - t); };
   Rows64<T, K, NTH> rb, rc;
-  Rows64<T, V, NTH> rx;
+  Rows64<T, XC, NTH> rx;
   float raw = 0.f, total = 0.f;
   auto request = [&](int64_t t) {
     const int rows = rows_of(t);
-    rx.load(xg + t * a.xs, a.xs, rows);
+    rx.load(xg + t * a.xs, a.xs, rows, nh * V);
     rb.load(bg + t * a.bs, a.bs, rows);
     if (OUT) rc.load(cg + t * a.cs, a.cs, rows);
   };
   auto request_dt = [&](int64_t t) {
-    raw = l < rows_of(t) ? load_scalar(a.dt, (t + l) * a.H + h, a.dt_dtype) : 0.f;
+    raw = l < rows_of(t) ? load_scalar(a.dt, (t + l) * a.H + ghead, a.dt_dtype) : 0.f;
   };
   // a chunk's gate, one token per lane; tokens past the end have step size 0
   auto gate = [&](int64_t t, int b) {
@@ -103,15 +120,15 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 3 : 4) void ssm_walk_kernel(SsmArg
     const float gam = wave_prefix(g);
     const float all = lane_value(gam, 63);
     total += all;
-    s.gam[b][l] = gam * kLog2e;
-    s.eg[b][l] = __expf(gam);
-    s.wt[b][l] = MODE == kGrad ? __expf(gam) : step * __expf(wave_suffix_excl(g));
-    s.dts[b][l] = step;
-    if (l == 0) s.decay[b] = __expf(all);
+    s.gam[gh][b][l] = gam * kLog2e;
+    s.eg[gh][b][l] = __expf(gam);
+    s.wt[gh][b][l] = MODE == kGrad ? __expf(gam) : step * __expf(wave_suffix_excl(g));
+    s.dts[gh][b][l] = step;
+    if (l == 0) s.decay[gh][b] = __expf(all);
   };
   if (nch > 0) {
     request(token(0));
-    if (w == NW - 1) {
+    if (gates) {
       request_dt(token(0));
       gate(token(0), 0);
       if (nch > 1) request_dt(token(1));
@@ -119,12 +136,13 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 3 : 4) void ssm_walk_kernel(SsmArg
   }
 
   Sw<K> ok;
-  Sw<V> ov;
+  Sw<XC> ov;
   Sw<64> om;
   for (int c = 0; c < nch; ++c) {
     const int64_t t = token(c);
     const int b = c & 1;
-    const int lf = fresh_v(l), wf = fresh_s(w), g4 = lf >> 4, col = lf & 15, v0 = 16 * wf;
+    const int lf = fresh_v(l), wf = fresh_s(w), g4 = lf >> 4, col = lf & 15;
+    const int hf = wf / WPH, v0 = hf * V + wf % WPH * (16 * PT);  // column in the x tile
     ok.hide();
     ov.hide();
     om.hide();
@@ -133,110 +151,168 @@ __global__ __launch_bounds__(4 * V, V == 64 ? 3 : 4) void ssm_walk_kernel(SsmArg
     if (OUT) rc.store(s.C);
     __syncthreads();
 
-    f32x4 acc[4];
+    f32x4 acc[PT][4];
     if (OUT) {
       // The state's part of the output, transposed (rows v, columns t), and
       // the scores of the wave's column block of tokens: they share C's
       // operands.
       f32x4 sc[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = sc[r] = zero4();
+      for (int r = 0; r < 4; ++r) {
+        sc[r] = zero4();
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) acc[pt][r] = zero4();
+      }
       float up = 1.f, down = 1.f;
       if (kScaled) {
-        const int e = state_exponent<NT>(S);
+        int e = state_exponent<NT>(S[0]);
+#pragma unroll
+        for (int pt = 1; pt < PT; ++pt) e = min(e, state_exponent<NT>(S[pt]));
         up = ldexpf(1.f, e);
         down = ldexpf(1.f, -e);
       }
-      // score tiles (row blocks) of this wave: the block's column is w % 4; of
-      // eight waves, two share a column's tiles
+      // score tiles (row blocks r0 .. r1 - 1) of this wave: the block's column
+      // is w % 4; of eight waves, two share a column's tiles
       const int cb = wf & 3, mine = (NW == 8 ? (5 - cb) >> 1 : 4);
       const int r0 = NW == 8 && wf >= 4 ? cb + mine : cb;
       const int r1 = NW == 8 && wf < 4 ? cb + mine : 4;
 #pragma unroll
       for (int kb = 0; kb < K / 32; ++kb) {
-        const x8 sf = kScaled ? pack_split<T>(S[2 * kb] * up, S[2 * kb + 1] * up)
-                              : pack_split<T>(S[2 * kb], S[2 * kb + 1]);
+        x8 sf[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt)
+          sf[pt] = kScaled ? pack_split<T>(S[pt][2 * kb] * up, S[pt][2 * kb + 1] * up)
+                           : pack_split<T>(S[pt][2 * kb], S[pt][2 * kb + 1]);
         const x8 bf = split_frag(s.B, ok, 16 * cb, 32 * kb);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const x8 cf = split_frag(s.C, ok, 16 * r, 32 * kb);
-          acc[r] = mfma16(sf, cf, acc[r]);
-          if (r >= r0 && r < r1) sc[r] = mfma16(bf, cf, sc[r]);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[pt][r] = mfma16(sf[pt], cf, acc[pt][r]);
+          sc[r] = mfma16(bf, cf, sc[r]);  // needed or not: branches would cut the schedule up
         }
-        if (kb % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        if (PT > 1 || kb % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       }
       // M = (C B^T) o L diag(dt), rounded to T as an operand; its tiles are
       // transposed, so that a lane holds four neighbours of a row
       const int i = 16 * cb + 4 * g4;
-      const f32x4 gi = *reinterpret_cast<const f32x4*>(&s.gam[b][i]);
-      const f32x4 di = *reinterpret_cast<const f32x4*>(&s.dts[b][i]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (r >= r0 && r < r1) {
-          const int row = 16 * r + col;
-          const float gr = s.gam[b][row];
-          x4 o;
+      for (int hh = 0; hh < HPW; ++hh) {
+        if (hh >= nh) continue;
+        const f32x4 gi = *reinterpret_cast<const f32x4*>(&s.gam[hh][b][i]);
+        const f32x4 di = *reinterpret_cast<const f32x4*>(&s.dts[hh][b][i]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v = sc[r][e] * exp2_fast(fminf(gr - gi[e], 0.f)) * di[e];
-            o[e] = from_f<T>(row >= i + e ? v : 0.f);
+        for (int r = 0; r < 4; ++r) {
+          if (r >= r0 && r < r1) {
+            const int row = 16 * r + col;
+            const float gr = s.gam[hh][b][row];
+            x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float v = sc[r][e] * exp2_fast(fminf(gr - gi[e], 0.f)) * di[e];
+              o[e] = from_f<T>(row >= i + e ? v : 0.f);
+            }
+            *row4(s.M[hh], om, 16 * r, 16 * cb) = o;
           }
-          *row4(s.M, om, 16 * r, 16 * cb) = o;
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] *= s.eg[b][16 * r + col] * down;
+      for (int r = 0; r < 4; ++r) {
+        const float eg = s.eg[hf][b][16 * r + col] * down;
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) acc[pt][r] *= eg;
+      }
       __syncthreads();
     }
     if (c + 1 < nch) request(token(c + 1));
 
-    // x^T fragments serve the product with M and, weighted, the state's
-    // update; with fp16 the state's columns are scaled while it is added
-    x8 xf[2];
-#pragma unroll
-    for (int tb = 0; tb < 2; ++tb) xf[tb] = tr_frag(s.X, ov, 32 * tb, v0);
-    if (OUT) {
+    if (active) {
+      // x^T fragments serve the product with M and, weighted, the state's
+      // update; with fp16 the state's columns are scaled while it is added
+      x8 xf[2][PT];
 #pragma unroll
       for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-        for (int r = 2 * tb; r < 4; ++r)
-          acc[r] = mfma16(xf[tb], split_frag(s.M, om, 16 * r, 32 * tb), acc[r]);
-    }
-    update_state<T, K>(S, s.B, ok, xf, s.wt[b], g4, s.decay[b]);
-
-    if (OUT) {
-      T* y = reinterpret_cast<T*>(a.y) + (t * a.H + h) * V;
-      const int ys = a.H * V * (int)sizeof(T);
-      const auto rs = buf_rsrc(y, (int64_t)(rows_of(t) - 1) * ys + V * (int)sizeof(T));
+        for (int pt = 0; pt < PT; ++pt) xf[tb][pt] = tr_frag(s.X, ov, 32 * tb, v0 + 16 * pt);
+      if (OUT) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * r + col;
-        const x4 xv = *row4(s.X, ov, 16 * r, v0);
-        x4 o;
+        for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = from_f<T>(acc[r][e] + skip * to_f(xv[e]));
-        buf_store8(rs, row * ys + (v0 + 4 * g4) * (int)sizeof(T), __builtin_bit_cast(u32x2, o));
+          for (int r = 2 * tb; r < 4; ++r) {
+            const x8 mf = split_frag(s.M[hf], om, 16 * r, 32 * tb);
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[pt][r] = mfma16(xf[tb][pt], mf, acc[pt][r]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (OUT) {
+        T* y = reinterpret_cast<T*>(a.y) + (t * a.H + head0) * V;
+        const int ys = a.H * V * (int)sizeof(T);
+        const auto rs = buf_rsrc(y, (int64_t)(rows_of(t) - 1) * ys + nh * V * (int)sizeof(T));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * r + col;
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) {
+            const x4 xv = *row4(s.X, ov, 16 * r, v0 + 16 * pt);
+            x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = from_f<T>(acc[pt][r][e] + skip * to_f(xv[e]));
+            buf_store8(rs, row * ys + (v0 + 16 * pt + 4 * g4) * (int)sizeof(T),
+                       __builtin_bit_cast(u32x2, o));
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      update_state<T, K, PT>(S, s.B, ok, xf, s.wt[hf][b], g4, s.decay[hf][b]);
     }
-    if (w == NW - 1 && c + 1 < nch) {
+    if (gates && c + 1 < nch) {
       gate(token(c + 1), b ^ 1);
       if (c + 2 < nch) request_dt(token(c + 2));
     }
     __syncthreads();
   }
 
+  if (!active && !(gates && !OUT)) return;
   if (!OUT) {
+    if (gates && l == 0) a.seg_decay[(int64_t)id * a.H + ghead] = total;
+    if (!active) return;
     float* dst = a.seg_state + slot;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      *reinterpret_cast<f32x4*>(dst + ((w * NT + nt) * 64 + l) * 4) = S[nt];
-    if (w == NW - 1 && l == 0) a.seg_decay[(int64_t)id * a.H + h] = total;
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<f32x4*>(dst + (((ct0 + pt) * NT + nt) * 64 + l) * 4) = S[pt][nt];
   } else if (a.ht && sg.j + 1 == sg.count) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a.ht[unit + state_at(w, nt, e, V)] = S[nt][e];
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          a.ht[unit + state_at(ct0 + pt, nt, e, V)] = S[pt][nt][e];
   }
+}
+
+// The walk's shape: V = 64 takes two heads of a group at once (32 columns a
+// wave) where a group has two; V = 128 one head on four waves of 32 columns.
+int walk_heads(const gdr_ssm_problem* p) { return p->V == 64 && p->H / p->G >= 2 ? 2 : 1; }
+template <int MODE>
+void launch_walk(const gdr_ssm_problem* p, const SsmArgs& a, const char* name, hipStream_t st) {
+  const int R = p->H / p->G, heads = walk_heads(p);
+  const dim3 grid((unsigned)((int64_t)a.nids * p->G * ((R + heads - 1) / heads)));
+  ssm_by_shape(p, [&](auto t, auto k, auto v) {
+    using T = decltype(t);
+    constexpr int K = k.value, V = v.value;
+    if constexpr (V == 128) {
+      GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 1, 2, MODE>), grid, dim3(256), st, a);
+    } else {
+      if (heads == 2)
+        GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 2, 2, MODE>), grid, dim3(256), st, a);
+      else
+        GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 1, 1, MODE>), grid, dim3(256), st, a);
+    }
+  });
 }
 
 // Segment j's end state over what it added, E_j = e^{decay_j} E_{j-1} +
@@ -275,13 +351,23 @@ __global__ __launch_bounds__(256) void ssm_combine_kernel(SsmArgs a) {
   const int64_t dir = REV ? -1 : 1, step = dir * a.H * K * V;
   float* p = a.seg_state + ((int64_t)first * a.H + h) * K * V + at;
   const float* dec = a.seg_decay + (int64_t)first * a.H + h;
-  f32x4 next = *reinterpret_cast<const f32x4*>(p);
-  for (int j = 0; j + 1 < m; ++j) {
-    const f32x4 add = next;
-    if (j + 2 < m) next = *reinterpret_cast<const f32x4*>(p + step);
-    E = E * __expf(dec[dir * j * a.H]) + add;
-    *reinterpret_cast<f32x4*>(p) = E;
-    p += step;
+  // eight segments' loads at a time: the chain itself is a few operations
+  for (int j = 0; j + 1 < m; j += 8) {
+    f32x4 add[8];
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i + 1 < m) {
+        add[i] = *reinterpret_cast<const f32x4*>(p + i * step);
+        d[i] = dec[dir * (j + i) * a.H];
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i + 1 < m) {
+        E = E * __expf(d[i]) + add[i];
+        *reinterpret_cast<f32x4*>(p + i * step) = E;
+      }
+    p += 8 * step;
   }
 }
 
@@ -429,7 +515,8 @@ SsmPlan ssm_plan(const gdr_ssm_problem* p, int64_t per_seg, int64_t slots) {
 }
 
 SsmPlan ssm_fwd_plan(const gdr_ssm_problem* p) {
-  return ssm_plan(p, p->H, p->V == 64 ? 768 : 512);
+  const int R = p->H / p->G, heads = walk_heads(p);
+  return ssm_plan(p, (int64_t)p->G * ((R + heads - 1) / heads), p->V == 64 && heads == 1 ? 768 : 512);
 }
 
 size_t ssm_fwd_workspace(const gdr_ssm_problem* p, const SsmPlan& pl) {
@@ -441,18 +528,13 @@ size_t ssm_fwd_workspace(const gdr_ssm_problem* p, const SsmPlan& pl) {
 // Every segment's end states (grad: the gradients at its start) in
 // a.seg_state; for the gradient a holds dy, C and dht for x, B and h0.
 void launch_ssm_states(const gdr_ssm_problem* p, const SsmArgs& a, bool grad, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.nids * p->H));
-  ssm_by_shape(p, [&](auto t, auto k, auto v) {
-    using T = decltype(t);
+  if (grad) launch_walk<kGrad>(p, a, "ssm_state_grad", st);
+  else launch_walk<kState>(p, a, "ssm_state", st);
+  ssm_by_shape(p, [&](auto, auto k, auto v) {
     constexpr int K = k.value, V = v.value;
-    const dim3 cgrid((unsigned)((int64_t)p->N * p->H * (K * V / 1024)));
-    if (grad) {
-      GDR_LAUNCH("ssm_state_grad", (ssm_walk_kernel<T, K, V, kGrad>), grid, dim3(4 * V), st, a);
-      GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, true>), cgrid, dim3(256), st, a);
-    } else {
-      GDR_LAUNCH("ssm_state", (ssm_walk_kernel<T, K, V, kState>), grid, dim3(4 * V), st, a);
-      GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, false>), cgrid, dim3(256), st, a);
-    }
+    const dim3 grid((unsigned)((int64_t)p->N * p->H * (K * V / 1024)));
+    if (grad) GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, true>), grid, dim3(256), st, a);
+    else GDR_LAUNCH("ssm_combine", (ssm_combine_kernel<K, V, false>), grid, dim3(256), st, a);
   });
 }
 
@@ -469,11 +551,7 @@ gdr_status launch_ssm_fwd(const gdr_ssm_problem* p, const SsmPlan& pl, const voi
         reinterpret_cast<char*>(ws) + align256((size_t)pl.nids * p->H * p->K * p->V * sizeof(float)));
   }
   if (pl.split) launch_ssm_states(p, a, false, st);
-  const dim3 grid((unsigned)((int64_t)pl.nids * p->H));
-  ssm_by_shape(p, [&](auto t, auto k, auto v) {
-    GDR_LAUNCH("ssm_out", (ssm_walk_kernel<decltype(t), k.value, v.value, kOut>), grid,
-               dim3(4 * v.value), st, a);
-  });
+  launch_walk<kOut>(p, a, "ssm_out", st);
   return launch_status("ssm_fwd");
 }
 
