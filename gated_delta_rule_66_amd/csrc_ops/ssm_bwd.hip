@@ -115,7 +115,10 @@ __global__ __launch_bounds__(256) void ssm_group_kernel(const float* pB, const f
 }
 
 // Heads per workgroup (those of one group share its B, C and C B^T and add
-// their dB, dC in registers), workgroups per group and the cut.
+// their dB, dC in registers), workgroups per group and the cut.  A pair of
+// heads fills a CU (8192 tokens, 32 heads, K = V = 128: 502 us for the whole
+// gradient step with segments for 256 workgroups, 569 for 512); one head at
+// V = 64 leaves room for two (K = 64: 273 us for 512, 350 for 256).
 struct GradPlan {
   int heads, slots;
   SsmPlan cut;
@@ -125,7 +128,7 @@ GradPlan grad_plan(const gdr_ssm_problem* p) {
   const int R = p->H / p->G;
   g.heads = R >= 2 ? 2 : 1;
   g.slots = (R + g.heads - 1) / g.heads;
-  g.cut = ssm_plan(p, (int64_t)p->G * g.slots, p->V == 64 ? 512 : 256);
+  g.cut = ssm_plan(p, (int64_t)p->G * g.slots, g.heads == 1 && p->V == 64 ? 512 : 256);
   return g;
 }
 

@@ -354,24 +354,6 @@ struct Rows64 {
   }
 };
 
-// The ten 16 x 16 tiles on or below the diagonal of a chunk's 64 x 64 matrix
-// over NW waves: tile s of wave w as row block * 4 + column block, -1 past
-// the wave's share (3, 3, 2, 2 of four waves; 2, 2 and six times 1 of eight).
-template <int NW>
-__device__ __forceinline__ int tri_tile(int w, int s) {
-  if (NW == 4) {
-    constexpr uint64_t t = 0xC | (0xDull << 4) | (0x0ull << 8) | (0xEull << 12) | (0xFull << 16) |
-                           (0x5ull << 20) | (0x8ull << 24) | (0x9ull << 28) | (0xAull << 36) |
-                           (0x4ull << 40);
-    return s < (w < 2 ? 3 : 2) ? (int)(t >> (12 * w + 4 * s)) & 15 : -1;
-  }
-  constexpr uint64_t t = 0xFEDCA984ull;
-  if (s == 0) return (int)(t >> (4 * w)) & 15;
-  return s == 1 && w < 2 ? (w == 0 ? 0x0 : 0x5) : -1;
-}
-template <int NW>
-constexpr int kMostTiles = NW == 4 ? 3 : 2;
-
 // State element (k, v) of register e of tile nt in column block ct: k = 16 nt +
 // 4 (lane / 16) + e, v = 16 ct + lane % 16 (the accumulator layout; two stacked
 // tiles are an operand in split k order).
@@ -379,9 +361,6 @@ __device__ __forceinline__ int state_at(int ct, int nt, int e, int V) {
   const int l = lane_id();
   return (16 * nt + 4 * (l >> 4) + e) * V + 16 * ct + (l & 15);
 }
-
-// token of element e of lane group g4's operand in split k order
-__device__ __forceinline__ int split_at(int g4, int e) { return (e < 4 ? 0 : 12) + 4 * g4 + e; }
 
 // Host side: the problem's arguments, its element type and sizes as types.
 SsmArgs ssm_args(const gdr_ssm_problem* p, const SsmPlan& pl);
