@@ -82,9 +82,10 @@ def _like(name, t, shape, dtypes, device):
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _token_rows(x, inner):
-    """(x, stride): x [B, T, ...] as rows one token stride apart, the last
-    `inner` dimensions contiguous; copied only when it is not laid out so."""
+def _token_rows(x, inner, most=1 << 62):
+    """(x, stride): x [B, T, ...] as rows one token stride (at most `most`)
+    apart, the last `inner` dimensions contiguous; copied only when it is not
+    laid out so."""
     B, T = x.shape[0], x.shape[1]
     width = 1
     ok = True
@@ -94,7 +95,7 @@ def _token_rows(x, inner):
         width *= x.shape[-d]
     if ok:
         s = x.stride(1) if T > 1 else (x.stride(0) if B > 1 else width)
-        if s >= width and (B == 1 or T == 1 or x.stride(0) == T * s):
+        if width <= s <= most and (B == 1 or T == 1 or x.stride(0) == T * s):
             return x, s
     return x.contiguous(), width
 
@@ -253,7 +254,7 @@ class _Ssm:
     """The checked arguments of one scan call."""
 
     def __init__(self, x, dt, A_log, B, C, D, dt_bias, dt_softplus, state, cu_seqlens,
-                 cu_seqlens_cpu):
+                 cu_seqlens_cpu, keep_states=False):
         if x.dim() != 4 or B.dim() != 4:
             raise GdrError(2, "x must be [B, T, H, V] and B [B, T, G, K], got %s and %s"
                            % (tuple(x.shape), tuple(B.shape)))
@@ -271,13 +272,14 @@ class _Ssm:
         N, self.cu, self.cu_host = _seqs(x, cu_seqlens, cu_seqlens_cpu)
         self.state_shape = (N, H, K, V)
         self.state = _aligned(_like("initial_state", state, self.state_shape, (torch.float32,), dev))
-        self.x, xs = _token_rows(x, 2)
-        self.B, bs = _token_rows(B, 2)
-        self.C, cs = _token_rows(C, 2)
+        self.x, xs = _token_rows(x, 2, 1 << 23)
+        self.B, bs = _token_rows(B, 2, 1 << 23)
+        self.C, cs = _token_rows(C, 2, 1 << 23)
         self.p = SsmProblem(B=b, T=T, H=H, G=G, K=K, V=V, N=N, cu_seqlens_dev=_ptr(self.cu),
                             cu_seqlens_host=_ptr(self.cu_host), in_dtype=code,
                             dt_dtype=_DT[dt.dtype], p_dtype=_DT[A_log.dtype],
-                            dt_softplus=1 if dt_softplus else 0, x_stride=xs, b_stride=bs,
+                            dt_softplus=1 if dt_softplus else 0,
+                            keep_states=1 if keep_states else 0, x_stride=xs, b_stride=bs,
                             c_stride=cs)
         self.ref = ctypes.byref(self.p)
 
@@ -291,12 +293,10 @@ def _aligned(t):
     return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
 
 
-def chunk_selective_scan_fwd(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
-                             initial_state=None, output_final_state=True, cu_seqlens=None,
-                             cu_seqlens_cpu=None):
-    """:func:`chunk_selective_scan` without autograd: ``(y, final_state)``."""
+def _scan_fwd(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, output_final_state,
+              cu_seqlens, cu_seqlens_cpu, keep_states):
     c = _Ssm(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens,
-             cu_seqlens_cpu)
+             cu_seqlens_cpu, keep_states)
     y = _new(x)
     last = None
     if output_final_state:
@@ -306,16 +306,13 @@ def chunk_selective_scan_fwd(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softpl
     with _guard(x):
         check(lib.gdr_ssm_fwd(c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last), _ptr(ws), n,
                               _stream(x)))
-    return y, last
+    return y, last, ws
 
 
-def chunk_selective_scan_bwd(x, dt, A_log, B, C, dy, D=None, dt_bias=None, dt_softplus=True,
-                             dht=None, initial_state=None, cu_seqlens=None, cu_seqlens_cpu=None):
-    """The gradient of :func:`chunk_selective_scan`: ``(dx, ddt, dA_log, dB, dC,
-    dD, ddt_bias, dh0)``, ``None`` in the place of an input that is ``None``.
-    ``dht`` (optional) is the gradient of the final state."""
+def _scan_bwd(x, dt, A_log, B, C, dy, D, dt_bias, dt_softplus, dht, initial_state, cu_seqlens,
+              cu_seqlens_cpu, keep_states, kept):
     c = _Ssm(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens,
-             cu_seqlens_cpu)
+             cu_seqlens_cpu, keep_states)
     dev = x.device
     dy = _like("dy", dy, x.shape, (x.dtype,), dev)
     dht = _aligned(_like("dht", dht, c.state_shape, (torch.float32,), dev))
@@ -325,36 +322,54 @@ def chunk_selective_scan_bwd(x, dt, A_log, B, C, dy, D=None, dt_bias=None, dt_so
     n = lib.gdr_ssm_bwd_workspace_size(c.ref)
     ws = _bytes(n, dev)
     with _guard(x):
-        check(lib.gdr_ssm_bwd(c.ref, *c.inputs(), _ptr(dy), _ptr(dht), _ptr(c.state), _ptr(dx),
-                              _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(db), _ptr(dh0),
-                              _ptr(ws), n, _stream(x)))
+        check(lib.gdr_ssm_bwd(c.ref, *c.inputs(), _ptr(dy), _ptr(dht), _ptr(c.state), _ptr(kept),
+                              _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(db),
+                              _ptr(dh0), _ptr(ws), n, _stream(x)))
     return dx, ddt, dA, dB, dC, dD, db, dh0
+
+
+def chunk_selective_scan_fwd(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
+                             initial_state=None, output_final_state=True, cu_seqlens=None,
+                             cu_seqlens_cpu=None):
+    """:func:`chunk_selective_scan` without autograd: ``(y, final_state)``."""
+    return _scan_fwd(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state,
+                     output_final_state, cu_seqlens, cu_seqlens_cpu, False)[:2]
+
+
+def chunk_selective_scan_bwd(x, dt, A_log, B, C, dy, D=None, dt_bias=None, dt_softplus=True,
+                             dht=None, initial_state=None, cu_seqlens=None, cu_seqlens_cpu=None):
+    """The gradient of :func:`chunk_selective_scan`: ``(dx, ddt, dA_log, dB, dC,
+    dD, ddt_bias, dh0)``, ``None`` in the place of an input that is ``None``.
+    ``dht`` (optional) is the gradient of the final state."""
+    return _scan_bwd(x, dt, A_log, B, C, dy, D, dt_bias, dt_softplus, dht, initial_state,
+                     cu_seqlens, cu_seqlens_cpu, False, None)
 
 
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state,
-                output_final_state, cu_seqlens, cu_seqlens_cpu):
+                output_final_state, cu_seqlens, cu_seqlens_cpu, grad):
         ctx.set_materialize_grads(False)
         if cu_seqlens is not None and cu_seqlens_cpu is None:
             cu_seqlens_cpu = cu_seqlens.detach().to("cpu")
-        y, last = chunk_selective_scan_fwd(x, dt, A_log, B, C, D, dt_bias, dt_softplus,
-                                           initial_state, output_final_state, cu_seqlens,
-                                           cu_seqlens_cpu)
+        ctx.keep = grad and any(ctx.needs_input_grad)
+        y, last, kept = _scan_fwd(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state,
+                                  output_final_state, cu_seqlens, cu_seqlens_cpu, ctx.keep)
         ctx.save_for_backward(x, dt, A_log, B, C, D, dt_bias, initial_state, cu_seqlens,
-                              cu_seqlens_cpu)
+                              cu_seqlens_cpu, kept if ctx.keep else None)
         ctx.dt_softplus = dt_softplus
         return y, last
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dlast):
-        x, dt, A_log, B, C, D, dt_bias, state, cu, cu_cpu = ctx.saved_tensors
+        x, dt, A_log, B, C, D, dt_bias, state, cu, cu_cpu, kept = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
-        dx, ddt, dA, dB, dC, dD, db, dh0 = chunk_selective_scan_bwd(
-            x, dt, A_log, B, C, dy, D, dt_bias, ctx.dt_softplus, dlast, state, cu, cu_cpu)
-        return dx, ddt, dA, dB, dC, dD, db, None, dh0, None, None, None
+        dx, ddt, dA, dB, dC, dD, db, dh0 = _scan_bwd(
+            x, dt, A_log, B, C, dy, D, dt_bias, ctx.dt_softplus, dlast, state, cu, cu_cpu,
+            ctx.keep, kept)
+        return dx, ddt, dA, dB, dC, dD, db, None, dh0, None, None, None, None
 
 
 def chunk_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
@@ -371,9 +386,12 @@ def chunk_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=T
     place), H a multiple of G, K and V 64 or 128; dt ``[B, T, H]`` in x's dtype or
     fp32; A_log, D, dt_bias ``[H]`` in x's dtype or fp32; states ``[N, H, K, V]``
     fp32.  ``cu_seqlens``: packed sequences (``B == 1``), which may be empty.
-    Gradients flow to every tensor; the forward keeps only its inputs."""
+    Gradients flow to every tensor; for them the forward keeps its inputs and the
+    fp32 states between the segments that it cut the sequences into (some 32 to
+    64 MiB)."""
     return _SelectiveScan.apply(x, dt, A_log, B, C, D, dt_bias, bool(dt_softplus), initial_state,
-                                bool(output_final_state), cu_seqlens, cu_seqlens_cpu)
+                                bool(output_final_state), cu_seqlens, cu_seqlens_cpu,
+                                torch.is_grad_enabled())
 
 
 def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,

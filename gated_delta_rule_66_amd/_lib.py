@@ -58,7 +58,7 @@ class SsmProblem(ctypes.Structure):
         ("cu_seqlens_dev", ctypes.c_void_p),
         ("cu_seqlens_host", ctypes.c_void_p),
         ("in_dtype", ctypes.c_int), ("dt_dtype", ctypes.c_int), ("p_dtype", ctypes.c_int),
-        ("dt_softplus", ctypes.c_int32),
+        ("dt_softplus", ctypes.c_int32), ("keep_states", ctypes.c_int32),
         ("x_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
     ]
 
@@ -179,7 +179,7 @@ def _declare_ops(lib):
     fn("gdr_ssm_fwd", [SP] + [P] * 11 + [S, P])
     fn("gdr_ssm_step", [SP] + [P] * 11)
     fn("gdr_ssm_bwd_workspace_size", [SP], S)
-    fn("gdr_ssm_bwd", [SP] + [P] * 19 + [S, P])
+    fn("gdr_ssm_bwd", [SP] + [P] * 20 + [S, P])
     NP = ctypes.POINTER(NormProblem)
     fn("gdr_rms_norm_check", [NP, ctypes.c_char_p, S])
     fn("gdr_rms_norm_fwd", [NP] + [P] * 8)

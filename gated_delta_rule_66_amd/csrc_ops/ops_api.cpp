@@ -68,8 +68,9 @@ static gdr_status validate(const gdr_conv_problem* p, char* reason, size_t len) 
     return fail(GDR_ERR_SHAPE, reason, len, "the convolution's width must be 2, 3 or 4, got %d",
                 p->W);
   if (p->D > 65536) return fail(GDR_ERR_SHAPE, reason, len, "at most 65536 channels, got %d", p->D);
-  // runs end up to W - 1 + 4 tokens past the last one in 32-bit arithmetic
-  if ((int64_t)p->B * p->T > 0x7fffff00)
+  // the last block's runs begin up to 2^23 tokens past the last one, in 32-bit
+  // arithmetic
+  if ((int64_t)p->B * p->T > 0x7f000000)
     return fail(GDR_ERR_SHAPE, reason, len, "problem too large");
   if (p->x_stride < p->D)
     return fail(GDR_ERR_SHAPE, reason, len, "x_stride=%lld is below D=%d", (long long)p->x_stride,
@@ -133,16 +134,25 @@ static gdr_status validate(const gdr_ssm_problem* p, char* reason, size_t len) {
   if (p->G > p->H || p->H % p->G != 0)
     return fail(GDR_ERR_HEADS, reason, len, "heads must be a multiple of groups (H=%d G=%d)", p->H,
                 p->G);
-  if ((int64_t)p->B * p->T > 0x7fffff00 || p->H > 65536 || (int64_t)p->N * p->H > (1 << 22) ||
-      (int64_t)p->B * p->T * p->H > ((int64_t)1 << 33))
-    return fail(GDR_ERR_SHAPE, reason, len, "problem too large");
+  // launches hold fewer than 2^32 threads: at most 4096 for the states of a
+  // sequence's head, 512 for each of a head's segments, which have 256 tokens
+  // or more unless the sequence is shorter
+  if ((int64_t)p->B * p->T > 0x7f000000 || p->H > 32768 || (int64_t)p->N * p->H > (1 << 19) ||
+      (int64_t)p->B * p->T * p->H > (1 << 30))
+    return fail(GDR_ERR_SHAPE, reason, len,
+                "problem too large (B * T * H up to 2^30, N * H up to 2^19, H up to 32768)");
   if (p->x_stride < (int64_t)p->H * p->V || p->b_stride < (int64_t)p->G * p->K ||
       p->c_stride < (int64_t)p->G * p->K)
     return fail(GDR_ERR_SHAPE, reason, len,
                 "token strides must cover a token's heads (x %lld, B %lld, C %lld)",
                 (long long)p->x_stride, (long long)p->b_stride, (long long)p->c_stride);
-  if (!is_flag(p->dt_softplus))
-    return fail(GDR_ERR_ARG, reason, len, "dt_softplus must be 0 or 1");
+  // 64 rows of a tile lie within 2^31 bytes
+  if (p->x_stride > (1 << 23) || p->b_stride > (1 << 23) || p->c_stride > (1 << 23))
+    return fail(GDR_ERR_SHAPE, reason, len,
+                "token strides must be at most 2^23 (x %lld, B %lld, C %lld)",
+                (long long)p->x_stride, (long long)p->b_stride, (long long)p->c_stride);
+  if (!is_flag(p->dt_softplus) || !is_flag(p->keep_states))
+    return fail(GDR_ERR_ARG, reason, len, "dt_softplus and keep_states must be 0 or 1");
   return check_seqs(p->B, p->T, p->N, p->cu_seqlens_dev, p->cu_seqlens_host, reason, len);
 }
 
@@ -249,7 +259,7 @@ size_t gdr_ssm_bwd_workspace_size(const gdr_ssm_problem* p) {
 gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
                        const void* B, const void* C, const void* D, const void* dt_bias,
                        const void* dy, const float* dfinal_state, const float* initial_state,
-                       void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
+                       const void* kept_states, void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
                        void* ddt_bias, float* dinitial_state, void* workspace,
                        size_t workspace_bytes, void* stream) {
   gdr_status s = validate(p, nullptr, 0);
@@ -261,11 +271,16 @@ gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
   if (misaligned(initial_state) || misaligned(dfinal_state) || misaligned(dinitial_state) ||
       misaligned(workspace))
     return fail(GDR_ERR_ARG, nullptr, 0, "states and workspace must be 16-byte aligned");
+  if (misaligned(kept_states))
+    return fail(GDR_ERR_ARG, nullptr, 0, "kept states must be 16-byte aligned");
+  if (kept_states ? !p->keep_states
+                  : p->keep_states && ssm_fwd_workspace(p, ssm_fwd_plan(p)) > 0)
+    return fail(GDR_ERR_NULL, nullptr, 0, "kept_states come with keep_states, and only then");
   s = need_workspace(ssm_bwd_workspace(p), workspace, workspace_bytes, "scan-gradient");
   if (s != GDR_OK) return s;
   if ((s = gdr_check_device()) != GDR_OK) return s;
-  return launch_ssm_bwd(p, x, dt, A_log, B, C, D, dt_bias, dy, dfinal_state, initial_state, dx, ddt,
-                        dA_log, dB, dC, dD, ddt_bias, dinitial_state, workspace,
+  return launch_ssm_bwd(p, x, dt, A_log, B, C, D, dt_bias, dy, dfinal_state, initial_state,
+                        kept_states, dx, ddt, dA_log, dB, dC, dD, ddt_bias, dinitial_state, workspace,
                         (hipStream_t)stream);
 }
 

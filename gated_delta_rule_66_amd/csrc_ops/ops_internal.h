@@ -37,6 +37,7 @@ struct SsmPlan {
 };
 SsmPlan ssm_plan(const gdr_ssm_problem* p, int64_t per_seg, int64_t slots);
 SsmPlan ssm_fwd_plan(const gdr_ssm_problem* p);
+SsmPlan ssm_grad_cut(const gdr_ssm_problem* p);
 size_t ssm_fwd_workspace(const gdr_ssm_problem* p, const SsmPlan& pl);
 gdr_status launch_ssm_fwd(const gdr_ssm_problem* p, const SsmPlan& pl, const void* x,
                           const void* dt, const void* A_log, const void* B, const void* C,
@@ -51,7 +52,7 @@ size_t ssm_bwd_workspace(const gdr_ssm_problem* p);
 gdr_status launch_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt,
                           const void* A_log, const void* B, const void* C, const void* D,
                           const void* dt_bias, const void* dy, const float* dht, const float* h0,
-                          void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
+                          const void* kept, void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
                           void* ddt_bias, float* dh0, void* ws, hipStream_t st);
 
 }  // namespace gdr

@@ -100,18 +100,19 @@ __global__ __launch_bounds__(256) void ssm_param_kernel(const float* part, int64
 template <typename T>
 __global__ __launch_bounds__(256) void ssm_group_kernel(const float* pB, const float* pC, int slots,
                                                         int64_t n, T* dB, T* dC) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  const bool second = i >= n;
-  const int64_t k = second ? i - n : i;
-  if (k >= n) return;
-  const float* p = (second ? pC : pB) + k;
-  f32x4 v = *reinterpret_cast<const f32x4*>(p);
-  for (int s = 1; s < slots; ++s) v += *reinterpret_cast<const f32x4*>(p + s * n);
   struct __attribute__((packed, aligned(sizeof(T)))) Raw {
     uint32_t u[2];
   };
-  typename VT<T>::x4 o{from_f<T>(v[0]), from_f<T>(v[1]), from_f<T>(v[2]), from_f<T>(v[3])};
-  *reinterpret_cast<Raw*>((second ? dC : dB) + k) = __builtin_bit_cast(Raw, o);
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < 2 * n;
+       i += (int64_t)gridDim.x * 1024) {
+    const bool second = i >= n;
+    const int64_t k = second ? i - n : i;
+    const float* p = (second ? pC : pB) + k;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+    for (int s = 1; s < slots; ++s) v += *reinterpret_cast<const f32x4*>(p + s * n);
+    const typename VT<T>::x4 o{from_f<T>(v[0]), from_f<T>(v[1]), from_f<T>(v[2]), from_f<T>(v[3])};
+    *reinterpret_cast<Raw*>((second ? dC : dB) + k) = __builtin_bit_cast(Raw, o);
+  }
 }
 
 // Heads per workgroup (those of one group share its B, C and C B^T and add
@@ -146,9 +147,11 @@ GradLayout layout(const gdr_ssm_problem* p, const GradPlan& g) {
     return here;
   };
   if (g.cut.split) {
-    o.state = take(ids * p->K * p->V * sizeof(float));
+    if (!p->keep_states) {
+      o.state = take(ids * p->K * p->V * sizeof(float));
+      o.sdec = take(ids * sizeof(float));
+    }
     o.grad = take(ids * p->K * p->V * sizeof(float));
-    o.sdec = take(ids * sizeof(float));
     o.gdec = take(ids * sizeof(float));
   }
   o.row = take(tokens * p->H * sizeof(float));
@@ -165,12 +168,14 @@ GradLayout layout(const gdr_ssm_problem* p, const GradPlan& g) {
 
 }  // namespace
 
+SsmPlan ssm_grad_cut(const gdr_ssm_problem* p) { return grad_plan(p).cut; }
+
 size_t ssm_bwd_workspace(const gdr_ssm_problem* p) { return layout(p, grad_plan(p)).total; }
 
 gdr_status launch_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt,
                           const void* A_log, const void* B, const void* C, const void* D,
                           const void* dt_bias, const void* dy, const float* dht, const float* h0,
-                          void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
+                          const void* kept, void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
                           void* ddt_bias, float* dh0, void* ws, hipStream_t st) {
   const GradPlan g = grad_plan(p);
   const GradLayout o = layout(p, g);
@@ -181,9 +186,13 @@ gdr_status launch_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* d
   a.f.x = x; a.f.dt = dt; a.f.A_log = A_log; a.f.B = B; a.f.C = C; a.f.D = D; a.f.dt_bias = dt_bias;
   a.f.h0 = h0;
   if (g.cut.split) {
-    a.f.seg_state = f32(o.state);
-    a.f.seg_decay = f32(o.sdec);
-    launch_ssm_states(p, a.f, false, st);
+    if (p->keep_states) {
+      a.f.seg_state = reinterpret_cast<float*>(const_cast<void*>(kept));  // only read
+    } else {
+      a.f.seg_state = f32(o.state);
+      a.f.seg_decay = f32(o.sdec);
+      launch_ssm_states(p, a.f, false, st);
+    }
     SsmArgs r = a.f;
     r.x = dy; r.xs = (int64_t)p->H * p->V;
     r.B = C; r.bs = p->c_stride;
@@ -226,7 +235,7 @@ gdr_status launch_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* d
                  params, params + ids);
     if (g.slots > 1) {
       const int64_t n = a.tokens * p->G * K;
-      GDR_LAUNCH("ssm_group", (ssm_group_kernel<T>), dim3((unsigned)((2 * n / 4 + 255) / 256)),
+      GDR_LAUNCH("ssm_group", (ssm_group_kernel<T>), dim3((unsigned)std::min<int64_t>((2 * n / 4 + 255) / 256, 1 << 20)),
                  dim3(256), st, a.part_dB, a.part_dC, g.slots, n, reinterpret_cast<T*>(dB),
                  reinterpret_cast<T*>(dC));
     }

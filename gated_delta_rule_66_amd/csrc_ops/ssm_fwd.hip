@@ -515,6 +515,7 @@ SsmPlan ssm_plan(const gdr_ssm_problem* p, int64_t per_seg, int64_t slots) {
 }
 
 SsmPlan ssm_fwd_plan(const gdr_ssm_problem* p) {
+  if (p->keep_states) return ssm_grad_cut(p);
   const int R = p->H / p->G, heads = walk_heads(p);
   return ssm_plan(p, (int64_t)p->G * ((R + heads - 1) / heads), p->V == 64 && heads == 1 ? 768 : 512);
 }

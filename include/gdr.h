@@ -478,8 +478,9 @@ typedef struct {
   gdr_dtype dt_dtype;             /* in_dtype or GDR_FP32 */
   gdr_dtype p_dtype;              /* in_dtype or GDR_FP32 */
   int32_t dt_softplus;            /* 0 or 1 */
-  int64_t x_stride;               /* elements between tokens, >= H * V */
-  int64_t b_stride, c_stride;     /* the same for B and C, >= G * K */
+  int32_t keep_states;            /* 1: the forward's workspace is kept for the gradient */
+  int64_t x_stride;               /* elements between tokens, H * V to 2^23 */
+  int64_t b_stride, c_stride;     /* the same for B and C, G * K to 2^23 */
 } gdr_ssm_problem;
 
 gdr_status gdr_ssm_check(const gdr_ssm_problem* p, char* reason, size_t reason_len);
@@ -487,15 +488,20 @@ gdr_status gdr_ssm_check(const gdr_ssm_problem* p, char* reason, size_t reason_l
 /* Forward over whole sequences: initial_state (nullable = zeros), y,
  * final_state (nullable = not written; not initial_state).  Long sequences
  * are cut into segments that run in parallel; the cuts depend on the shapes
- * and lengths only. */
+ * and lengths only.  With keep_states the cut is the gradient's, and the
+ * workspace (of the size that the problem with keep_states asks for, possibly
+ * 0) holds the states at the segments' ends afterwards. */
 size_t gdr_ssm_fwd_workspace_size(const gdr_ssm_problem* p);
 gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
                        const void* B, const void* C, const void* D, const void* dt_bias,
                        const float* initial_state, void* y, float* final_state, void* workspace,
                        size_t workspace_bytes, void* stream);
 
-/* The gradient of the forward (everything it needs of it is recomputed).
- *   in : the forward's inputs; dy; dfinal_state (nullable = zero)
+/* The gradient of the forward.
+ *   in : the forward's inputs; dy; dfinal_state (nullable = zero);
+ *        kept_states: with keep_states, the workspace of the forward of the
+ *        same problem and inputs (NULL if its size was 0); without, NULL, and
+ *        everything is recomputed from the inputs
  *   out: dx, ddt (with respect to the raw step sizes), dA_log, dB, dC; dD,
  *        ddt_bias, dinitial_state (each nullable = not written, and only with
  *        its input).  Parameters' gradients are in p_dtype, sums over all
@@ -504,8 +510,8 @@ size_t gdr_ssm_bwd_workspace_size(const gdr_ssm_problem* p);
 gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
                        const void* B, const void* C, const void* D, const void* dt_bias,
                        const void* dy, const float* dfinal_state, const float* initial_state,
-                       void* dx, void* ddt, void* dA_log, void* dB, void* dC, void* dD,
-                       void* ddt_bias, float* dinitial_state, void* workspace,
+                       const void* kept_states, void* dx, void* ddt, void* dA_log, void* dB,
+                       void* dC, void* dD, void* ddt_bias, float* dinitial_state, void* workspace,
                        size_t workspace_bytes, void* stream);
 
 /* Token by token for decode steps: the same y and final_state, the state read
