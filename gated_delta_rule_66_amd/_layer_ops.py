@@ -348,11 +348,11 @@ def chunk_selective_scan_bwd(x, dt, A_log, B, C, dy, D=None, dt_bias=None, dt_so
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state,
-                output_final_state, cu_seqlens, cu_seqlens_cpu, grad):
+                output_final_state, cu_seqlens, cu_seqlens_cpu, keep):
         ctx.set_materialize_grads(False)
         if cu_seqlens is not None and cu_seqlens_cpu is None:
             cu_seqlens_cpu = cu_seqlens.detach().to("cpu")
-        ctx.keep = grad and any(ctx.needs_input_grad)
+        ctx.keep = keep and any(ctx.needs_input_grad)
         y, last, kept = _scan_fwd(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state,
                                   output_final_state, cu_seqlens, cu_seqlens_cpu, ctx.keep)
         ctx.save_for_backward(x, dt, A_log, B, C, D, dt_bias, initial_state, cu_seqlens,
@@ -374,7 +374,7 @@ class _SelectiveScan(torch.autograd.Function):
 
 def chunk_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,
                          initial_state=None, output_final_state=False, cu_seqlens=None,
-                         cu_seqlens_cpu=None):
+                         cu_seqlens_cpu=None, recompute_states=False):
     """Selective state space scan (one decay per head) with autograd: ``(y,
     final_state)``.
 
@@ -387,11 +387,12 @@ def chunk_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=T
     fp32; A_log, D, dt_bias ``[H]`` in x's dtype or fp32; states ``[N, H, K, V]``
     fp32.  ``cu_seqlens``: packed sequences (``B == 1``), which may be empty.
     Gradients flow to every tensor; for them the forward keeps its inputs and the
-    fp32 states between the segments that it cut the sequences into (some 32 to
-    64 MiB)."""
+    fp32 states between the segments that it cut long sequences into (K * V * 4
+    bytes per segment and head); ``recompute_states=True`` keeps only the inputs
+    and recomputes the states in the backward instead."""
     return _SelectiveScan.apply(x, dt, A_log, B, C, D, dt_bias, bool(dt_softplus), initial_state,
                                 bool(output_final_state), cu_seqlens, cu_seqlens_cpu,
-                                torch.is_grad_enabled())
+                                torch.is_grad_enabled() and not recompute_states)
 
 
 def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_softplus=True,

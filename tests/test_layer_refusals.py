@@ -8,7 +8,7 @@ import torch
 import gated_delta_rule_66_amd as gdr
 from gated_delta_rule_66_amd import _lib
 from gated_delta_rule_66_amd._lib import (GDR_BF16, GDR_FP16, GDR_FP32, ConvProblem, NormProblem,
-                                          lib)
+                                          SsmProblem, lib)
 
 FAKE = 0x1000  # never dereferenced: validation happens on the host copy
 
@@ -33,6 +33,14 @@ def norm(**kw):
                 quant=0, group_size=0, eps=1e-6, x_stride=40)
     base.update(kw)
     return NormProblem(**base)
+
+
+def ssm(**kw):
+    base = dict(B=2, T=300, H=4, G=2, K=64, V=128, N=2, in_dtype=GDR_BF16, dt_dtype=GDR_FP32,
+                p_dtype=GDR_FP32, dt_softplus=1, keep_states=0, x_stride=512, b_stride=128,
+                c_stride=128)
+    base.update(kw)
+    return SsmProblem(**base)
 
 
 def verdict(f, p):
@@ -71,8 +79,37 @@ NORM = [
     (norm(eps=float("nan")), "GDR_ERR_ARG", "eps"),
 ]
 
+SSM = [
+    (ssm(K=32), "GDR_ERR_HEAD_DIM", "64 or 128"),
+    (ssm(V=256, x_stride=1024), "GDR_ERR_HEAD_DIM", "64 or 128"),
+    (ssm(in_dtype=GDR_FP32), "GDR_ERR_DTYPE", "bf16 or fp16"),
+    (ssm(dt_dtype=GDR_FP16), "GDR_ERR_DTYPE", "dt must"),
+    (ssm(p_dtype=GDR_FP16), "GDR_ERR_DTYPE", "A_log"),
+    (ssm(T=0), "GDR_ERR_SHAPE", "positive"),
+    (ssm(H=-4), "GDR_ERR_SHAPE", "positive"),
+    (ssm(H=3, x_stride=384), "GDR_ERR_HEADS", "multiple"),
+    (ssm(G=8, b_stride=512, c_stride=512), "GDR_ERR_HEADS", "multiple"),
+    (ssm(x_stride=511), "GDR_ERR_SHAPE", "cover"),
+    (ssm(b_stride=127), "GDR_ERR_SHAPE", "cover"),
+    (ssm(c_stride=127), "GDR_ERR_SHAPE", "cover"),
+    (ssm(x_stride=(1 << 23) + 1), "GDR_ERR_SHAPE", "2^23"),
+    (ssm(b_stride=(1 << 23) + 1), "GDR_ERR_SHAPE", "2^23"),
+    (ssm(c_stride=1 << 40), "GDR_ERR_SHAPE", "2^23"),
+    (ssm(H=32770, x_stride=32770 * 128), "GDR_ERR_SHAPE", "too large"),
+    (ssm(B=1 << 18, N=1 << 18, T=1), "GDR_ERR_SHAPE", "too large"),       # N * H = 2^20
+    (ssm(T=(1 << 27) + 1), "GDR_ERR_SHAPE", "too large"),                 # B * T * H > 2^30
+    (ssm(B=1 << 16, N=1 << 16, T=1 << 15), "GDR_ERR_SHAPE", "too large"),
+    (ssm(N=3), "GDR_ERR_SHAPE", "N == B"),
+    (ssm(dt_softplus=2), "GDR_ERR_ARG", "dt_softplus"),
+    (ssm(keep_states=-1), "GDR_ERR_ARG", "keep_states"),
+    (ssm(cu_seqlens_dev=FAKE), "GDR_ERR_VARLEN", "host copy"),
+]
+
 
 def test_accepted():
+    assert verdict(lib.gdr_ssm_check, ssm()) == ("GDR_OK", "")
+    assert verdict(lib.gdr_ssm_check, ssm(x_stride=1 << 23, T=1 << 27))[0] == "GDR_OK"
+    assert verdict(lib.gdr_ssm_check, ssm(B=1 << 17, N=1 << 17, T=1))[0] == "GDR_OK"
     assert verdict(lib.gdr_conv1d_check, conv()) == ("GDR_OK", "")
     assert verdict(lib.gdr_conv1d_check, conv(dtype=GDR_FP32, W=2))[0] == "GDR_OK"
     assert verdict(lib.gdr_rms_norm_check, norm()) == ("GDR_OK", "")
@@ -130,4 +167,72 @@ def test_tensors_on_the_host_are_refused():
                  lambda: gdr.rms_norm(x, w[:, 0]), lambda: gdr.rms_norm_quant(x, w[:, 0])):
         with pytest.raises(gdr.GdrError) as e:
             call()
+        assert e.value.name == "GDR_ERR_DEVICE"
+
+
+@pytest.mark.parametrize("p,status,msg", SSM)
+def test_scan_rejections(p, status, msg):
+    st, reason = verdict(lib.gdr_ssm_check, p)
+    assert st == status and msg in reason and msg in lib.gdr_last_error().decode()
+    assert lib.gdr_ssm_fwd_workspace_size(ctypes.byref(p)) == 0
+    assert lib.gdr_ssm_bwd_workspace_size(ctypes.byref(p)) == 0
+    code = [k for k, v in _lib.STATUS.items() if v == status][0]
+    assert lib.gdr_ssm_step(ctypes.byref(p), *[FAKE] * 10, None) == code
+
+
+@pytest.mark.parametrize("cu", [(1, 4, 300), (0, 6, 4, 300), (0, 4, 299)])
+def test_bad_scan_offsets(cu):
+    host = offsets(*cu)
+    p = ssm(B=1, N=len(cu) - 1, cu_seqlens_dev=FAKE, cu_seqlens_host=addr(host))
+    assert verdict(lib.gdr_ssm_check, p)[0] == "GDR_ERR_VARLEN"
+    p.B = 2
+    assert verdict(lib.gdr_ssm_check, p)[0] == "GDR_ERR_VARLEN"
+
+
+def test_scan_pointers_and_workspaces():
+    long = dict(T=1 << 16, B=1, N=1)          # cut into segments: needs a workspace
+    p = ssm(**long)
+    ref = ctypes.byref(p)
+    fwd = [FAKE] * 7 + [FAKE, FAKE, 2 * FAKE]   # .., initial_state, y, final_state
+    n = lib.gdr_ssm_fwd_workspace_size(ref)
+    assert n > 0
+    assert lib.gdr_ssm_fwd(ref, None, *fwd[1:], FAKE, n, None) == 1
+    assert lib.gdr_ssm_fwd(ref, *fwd, FAKE, n - 1, None) == 7
+    assert lib.gdr_ssm_fwd(ref, *fwd, None, n, None) == 7
+    assert lib.gdr_ssm_fwd(ref, *fwd, FAKE + 8, n, None) == 10
+    assert lib.gdr_ssm_fwd(ref, *fwd[:-1], FAKE, FAKE, n, None) == 10        # in place
+    assert lib.gdr_ssm_fwd(ref, *fwd[:7], FAKE + 4, *fwd[8:], FAKE, n, None) == 10
+    assert lib.gdr_ssm_step(ref, *fwd[:7], FAKE + 4, FAKE, None, None) == 10
+    assert lib.gdr_ssm_step(ref, *fwd[:7], None, None, None, None) == 1
+    # .., dy, dfinal_state, initial_state, kept, dx, ddt, dA_log, dB, dC, dD, ddt_bias, dh0
+    bwd = [FAKE] * 7 + [FAKE, None, FAKE, None] + [FAKE] * 8
+    n = lib.gdr_ssm_bwd_workspace_size(ref)
+    assert n > 0
+
+    def call(q, at=None, value=None, ws=FAKE, size=None):
+        a = list(bwd)
+        if at is not None:
+            a[at] = value
+        return lib.gdr_ssm_bwd(ctypes.byref(q), *a, ws, n if size is None else size, None)
+
+    assert call(p, size=n - 1) == 7
+    assert call(p, ws=FAKE + 4) == 10
+    assert call(p, 7) == 1 and call(p, 11) == 1
+    assert call(p, 5) == 10 and call(p, 6) == 10 and call(p, 9) == 10      # dD without D, ..
+    assert call(p, 8, FAKE + 4) == 10
+    kept = ssm(keep_states=1, **long)
+    assert lib.gdr_ssm_fwd_workspace_size(ctypes.byref(kept)) > 0
+    assert lib.gdr_ssm_bwd_workspace_size(ctypes.byref(kept)) < n
+    assert call(p, 10, FAKE) == 1          # kept states without the flag
+    assert call(kept, 10, None) == 1       # the flag without the states
+    assert call(kept, 10, FAKE + 4) == 10
+
+
+def test_scan_tensors_on_the_host_are_refused():
+    x, b = torch.zeros(1, 5, 2, 64), torch.zeros(1, 5, 1, 64)
+    h = torch.zeros(2)
+    for f in (gdr.chunk_selective_scan, gdr.chunk_selective_scan_fwd,
+              gdr.fused_recurrent_selective_scan):
+        with pytest.raises(gdr.GdrError) as e:
+            f(x.bfloat16(), torch.zeros(1, 5, 2), h, b.bfloat16(), b.bfloat16())
         assert e.value.name == "GDR_ERR_DEVICE"
