@@ -91,6 +91,32 @@ __device__ __forceinline__ float row_reduce(float v, float* lds) {
   return s;
 }
 
+// The same for a sum in 64 bits.
+template <int CTRL>
+__device__ __forceinline__ double dpp_mov2(double v) {
+  const uint2 u = __builtin_bit_cast(uint2, v);
+  const uint2 r{__builtin_bit_cast(uint32_t, dpp_mov<CTRL>(__builtin_bit_cast(float, u.x))),
+                __builtin_bit_cast(uint32_t, dpp_mov<CTRL>(__builtin_bit_cast(float, u.y)))};
+  return __builtin_bit_cast(double, r);
+}
+template <int NT>
+__device__ __forceinline__ double row_sum(double v, double* lds) {
+  v += dpp_mov2<0xB1>(v);
+  v += dpp_mov2<0x4E>(v);
+  v += dpp_mov2<0x141>(v);
+  v += dpp_mov2<0x140>(v);
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  if (NT == 64) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = lds[0];
+#pragma unroll
+  for (int i = 1; i < NT / 64; ++i) s += lds[i];
+  return s;
+}
+
 struct NormArgs {
   const void* x;
   const void* res;     // nullable
@@ -133,7 +159,7 @@ template <typename T, typename RES, bool QUANT, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
   constexpr bool kRes = !std::is_void<RES>::value;
   typedef typename std::conditional<kRes, RES, T>::type R;
-  __shared__ float lds[16];
+  __shared__ __align__(8) float lds[32];
   const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
   const int64_t row = NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
   if (row >= a.rows) return;  // a whole wave; the barriers below are for NT > 64 only
@@ -147,7 +173,7 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
     load8<T, PART>(x + c, a.D, f[i]);
     if (kRes) load8<R, PART>(res + c, a.D, r[kRes ? i : 0]);
   }
-  float ss = 0.f;
+  double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
@@ -158,11 +184,15 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
       for (int e = 0; e < 8; ++e) f[i][e] = to_f(from_f<R>(f[i][e] + r[kRes ? i : 0][e]));
       if (v0 < a.D) store8<R, PART>(h + c, a.D, f[i]);
     }
+    float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss += c + e >= v0 ? f[i][e] * f[i][e] : 0.f;
+    sum += ss;
   }
-  ss = row_reduce<NT, false>(ss, lds);
-  const float rstd = 1.f / sqrtf(ss / (float)a.D + a.eps);
+  // eight squares in 32 bits, their sums in 64: the mean is its 32-bit
+  // neighbour for any width and any split of the row
+  sum = row_sum<NT>(sum, reinterpret_cast<double*>(lds));
+  const float rstd = rsqrtf((float)sum / (float)a.D + a.eps);
   if (a.rstd && tid == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -210,6 +240,13 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         q[e] = f[i][e] * inv;
+        if (!fp8) {
+          // int8 keeps more bits than e4m3, and a product on the other side of
+          // a tie is a whole step off: the residual makes it the rounded
+          // quotient (where it is finite; infinities keep the product's NaN or 0)
+          const float left = __builtin_fmaf(-q[e], s, f[i][e]);
+          q[e] = fabsf(left) < __builtin_inff() ? __builtin_fmaf(left, inv, q[e]) : q[e];
+        }
         // a NaN passes both comparisons
         q[e] = q[e] > top ? top : q[e] < -top ? -top : q[e];
       }
