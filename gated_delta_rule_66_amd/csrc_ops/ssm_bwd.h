@@ -460,7 +460,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
     if (c + 1 < nch) request(c + 1);
     if (RB < HPW && nh > 1) inter(HPW - 1);
     if (active)
-      update_state<T, K, PT>(S, Q, ok, xf, REV ? s.eg[hw] : s.wt[hw], g4, s.decay[hw]);
+      update_state<T, K, REV>(S, Q, ok, xf, REV ? s.eg[hw] : s.wt[hw], g4, s.decay[hw]);
     if (kScaled) {
       const int e = exponent();
       if (l == 0) s.ex[w] = e;

@@ -271,14 +271,19 @@ __device__ __forceinline__ void weighted(const typename VT<T>::x8& xf, const flo
 
 // S <- decay S + A^T diag(wt) x over a chunk's 64 tokens, for PT blocks of 16
 // columns: A a swizzled 64 x K tile, xf[tb][pt] the lane's column of x in two
-// blocks of 32 tokens, wt in LDS.  The weighted values go in as a pair of
-// 16-bit operands; with fp16 the columns are scaled to fit.
-template <typename T, int K, int PT>
+// blocks of 32 tokens, wt in LDS.  The weighted values go in as 16-bit operands
+// that sum to them: a pair with fp16 (22 bits, the columns scaled to fit) and
+// with bf16 (16 bits and a sign), or, EXACT, three with bf16.  States that are
+// handed on (to a caller, to other segments) take EXACT: a pair's 2^-18 is 50
+// times the error of fp32 sums.  Where a walk's states end in 16-bit outputs
+// and 2^-16 sums (the gradient's forward walk) the pair is enough, and saves
+// 5 % of the walk's time.
+template <typename T, int K, bool EXACT, int PT>
 __device__ __forceinline__ void update_state(f32x4 (&S)[PT][K / 16], const T* A, const Sw<K>& o,
                                              const typename VT<T>::x8 (&xf)[2][PT], const float* wt,
                                              int g4, float decay) {
   constexpr int NT = K / 16;
-  constexpr bool kScaled = !__is_same(T, __bf16);
+  constexpr bool kScaled = !__is_same(T, __bf16), kThree = EXACT && !kScaled;
   float scale[PT];
 #pragma unroll
   for (int pt = 0; pt < PT; ++pt) {
@@ -299,12 +304,17 @@ __device__ __forceinline__ void update_state(f32x4 (&S)[PT][K / 16], const T* A,
   }
 #pragma unroll
   for (int tb = 0; tb < 2; ++tb) {
-    typename VT<T>::x8 hi[PT], lo[PT];
+    typename VT<T>::x8 hi[PT], lo[PT], rest[kThree ? PT : 1];
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) {
       float v[8];
       weighted<T>(xf[tb][pt], wt, tb, g4, scale[pt], v);
       split8<T>(v, hi[pt], lo[pt]);
+      if (kThree) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          rest[pt][e] = from_f<T>(v[e] - to_f(hi[pt][e]) - to_f(lo[pt][e]));
+      }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -313,6 +323,7 @@ __device__ __forceinline__ void update_state(f32x4 (&S)[PT][K / 16], const T* A,
       for (int pt = 0; pt < PT; ++pt) {
         S[pt][nt] = mfma16(f, hi[pt], S[pt][nt]);
         S[pt][nt] = mfma16(f, lo[pt], S[pt][nt]);
+        if (kThree) S[pt][nt] = mfma16(f, rest[pt], S[pt][nt]);
       }
       // a few operands in flight, not all of them: registers
       if (nt % (4 / PT) == 4 / PT - 1) __builtin_amdgcn_sched_barrier(0);

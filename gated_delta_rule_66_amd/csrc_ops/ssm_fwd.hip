@@ -264,7 +264,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, HPW * PT == 1 ? 3 : 2) void ssm_w
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      update_state<T, K, PT>(S, s.B, ok, xf, s.wt[hf][b], g4, s.decay[hf][b]);
+      update_state<T, K, true>(S, s.B, ok, xf, s.wt[hf][b], g4, s.decay[hf][b]);
     }
     if (gates && c + 1 < nch) {
       gate(token(c + 1), b ^ 1);
