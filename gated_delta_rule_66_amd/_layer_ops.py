@@ -9,7 +9,6 @@ package.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -19,7 +18,6 @@ from ._lib import (GDR_BF16, GDR_FP16, GDR_FP32, ConvProblem, GdrError, NormProb
                    lib)
 
 _DT = {torch.bfloat16: GDR_BF16, torch.float16: GDR_FP16, torch.float32: GDR_FP32}
-_NULL_GUARD = contextlib.nullcontext()
 
 
 def _ptr(t):
@@ -33,29 +31,29 @@ def _code(t, name):
         raise GdrError(4, "%s has the unsupported dtype %s" % (name, t.dtype)) from None
 
 
-def _guard(t):
-    """Makes t's device the current one around a launch."""
-    if t.device.index == torch.cuda.current_device():
-        return _NULL_GUARD
-    return torch.cuda.device(t.device)
+# the current device and the current stream's handle without objects around
+# them: a fifth of a small call's time on the host otherwise
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-# the current stream's handle without a Stream object around it: a fifth of a
-# small call's time on the host otherwise
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream(t):
-    if _raw_stream is not None:
-        return _raw_stream(t.device.index)
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _launch(t, f, *args):
+    """f on t's device, which is made the current one, and its current stream."""
+    i = t.get_device()
+    if i == _device():
+        status = f(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = f(*args, _raw_stream(i))
+    check(status)
 
 
 def _new(t, dtype=None):
     """A new contiguous tensor of t's shape and device (t's dtype by default)."""
-    if dtype is None and t.is_contiguous():
-        return torch.empty_like(t)
-    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
+    if t.is_contiguous():
+        return torch.empty_like(t, dtype=dtype)
+    return t.new_empty(t.shape, dtype=dtype)
 
 
 def _need_gpu(name, t):
@@ -65,6 +63,8 @@ def _need_gpu(name, t):
 
 def _expect(name, t, shape, dtypes, device):
     """t must have this shape, one of these dtypes and this device."""
+    if t.shape == shape and t.dtype in dtypes and t.device == device:
+        return
     if tuple(t.shape) != tuple(shape):
         raise GdrError(2, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype not in dtypes:
@@ -78,7 +78,8 @@ def _like(name, t, shape, dtypes, device):
     """:func:`_expect` (None passes), and t contiguous."""
     if t is None:
         return None
-    _expect(name, t, shape, dtypes, device)
+    if t.shape != shape or t.dtype not in dtypes or t.device != device:
+        _expect(name, t, shape, dtypes, device)
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -86,6 +87,9 @@ def _token_rows(x, inner, most=1 << 62):
     """(x, stride): x [B, T, ...] as rows one token stride (at most `most`)
     apart, the last `inner` dimensions contiguous; copied only when it is not
     laid out so."""
+    if x.is_contiguous():
+        shape = x.shape
+        return x, shape[2] if inner == 1 else shape[2] * shape[3]
     B, T = x.shape[0], x.shape[1]
     width = 1
     ok = True
@@ -149,10 +153,8 @@ class _Conv:
         self.state_shape = (N, W - 1, D)
         self.state = _like("initial_state", state, self.state_shape, (x.dtype,), dev)
         self.x, stride = _token_rows(x, 1)
-        self.p = ConvProblem(B=B, T=T, D=D, W=W, N=N, cu_seqlens_dev=_ptr(self.cu),
-                             cu_seqlens_host=_ptr(self.cu_host), dtype=dt,
-                             w_dtype=_code(weight, "weight"), activation=_activation(activation),
-                             x_stride=stride)
+        self.p = ConvProblem(B, T, D, W, N, _ptr(self.cu), _ptr(self.cu_host), dt,
+                             _code(weight, "weight"), _activation(activation), stride)
         self.ref = ctypes.byref(self.p)   # the library checks the problem in every call
 
 
@@ -163,10 +165,9 @@ def causal_conv1d_fwd(x, weight, bias=None, activation="silu", initial_state=Non
     y = _new(x)
     last = None
     if output_final_state:
-        last = torch.empty(c.state_shape, dtype=x.dtype, device=x.device)
-    with _guard(x):
-        check(lib.gdr_conv1d_fwd(c.ref, _ptr(c.x), _ptr(c.weight), _ptr(c.bias), _ptr(c.state),
-                                 _ptr(y), _ptr(last), _stream(x)))
+        last = x.new_empty(c.state_shape)
+    _launch(x, lib.gdr_conv1d_fwd, c.ref, _ptr(c.x), _ptr(c.weight), _ptr(c.bias), _ptr(c.state),
+            _ptr(y), _ptr(last))
     return y, last
 
 
@@ -185,10 +186,8 @@ def causal_conv1d_bwd(x, weight, bias, dy, dfinal_state=None, activation="silu",
     ds = None if c.state is None else torch.empty_like(c.state)
     n = lib.gdr_conv1d_bwd_workspace_size(c.ref)
     ws = _bytes(n, dev)
-    with _guard(x):
-        check(lib.gdr_conv1d_bwd(c.ref, _ptr(c.x), _ptr(c.weight), _ptr(c.bias), _ptr(dy),
-                                 _ptr(dfinal_state), _ptr(c.state), _ptr(dx), _ptr(dw), _ptr(db),
-                                 _ptr(ds), _ptr(ws), n, _stream(x)))
+    _launch(x, lib.gdr_conv1d_bwd, c.ref, _ptr(c.x), _ptr(c.weight), _ptr(c.bias), _ptr(dy),
+            _ptr(dfinal_state), _ptr(c.state), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ds), _ptr(ws), n)
     return dx, dw, db, ds
 
 
@@ -242,9 +241,8 @@ def causal_conv1d_update(x, conv_state, weight, bias=None, activation="silu"):
         raise GdrError(10, "conv_state is updated in place and must be contiguous")
     c = _Conv(x3, weight, bias, activation, conv_state, None, None)
     y = _new(x3)
-    with _guard(x):
-        check(lib.gdr_conv1d_update(c.ref, _ptr(c.x), _ptr(conv_state), _ptr(c.weight),
-                                    _ptr(c.bias), _ptr(y), _stream(x)))
+    _launch(x, lib.gdr_conv1d_update, c.ref, _ptr(c.x), _ptr(conv_state), _ptr(c.weight),
+            _ptr(c.bias), _ptr(y))
     return y.squeeze(1) if squeeze else y
 
 
@@ -275,12 +273,9 @@ class _Ssm:
         self.x, xs = _token_rows(x, 2, 1 << 23)
         self.B, bs = _token_rows(B, 2, 1 << 23)
         self.C, cs = _token_rows(C, 2, 1 << 23)
-        self.p = SsmProblem(B=b, T=T, H=H, G=G, K=K, V=V, N=N, cu_seqlens_dev=_ptr(self.cu),
-                            cu_seqlens_host=_ptr(self.cu_host), in_dtype=code,
-                            dt_dtype=_DT[dt.dtype], p_dtype=_DT[A_log.dtype],
-                            dt_softplus=1 if dt_softplus else 0,
-                            keep_states=1 if keep_states else 0, x_stride=xs, b_stride=bs,
-                            c_stride=cs)
+        self.p = SsmProblem(b, T, H, G, K, V, N, _ptr(self.cu), _ptr(self.cu_host), code,
+                            _DT[dt.dtype], _DT[A_log.dtype], 1 if dt_softplus else 0,
+                            1 if keep_states else 0, xs, bs, cs)
         self.ref = ctypes.byref(self.p)
 
     def inputs(self):
@@ -300,12 +295,10 @@ def _scan_fwd(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, output
     y = _new(x)
     last = None
     if output_final_state:
-        last = torch.empty(c.state_shape, dtype=torch.float32, device=x.device)
+        last = x.new_empty(c.state_shape, dtype=torch.float32)
     n = lib.gdr_ssm_fwd_workspace_size(c.ref)
     ws = _bytes(n, x.device) if n else None
-    with _guard(x):
-        check(lib.gdr_ssm_fwd(c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last), _ptr(ws), n,
-                              _stream(x)))
+    _launch(x, lib.gdr_ssm_fwd, c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last), _ptr(ws), n)
     return y, last, ws
 
 
@@ -321,10 +314,9 @@ def _scan_bwd(x, dt, A_log, B, C, dy, D, dt_bias, dt_softplus, dht, initial_stat
                                                          initial_state))
     n = lib.gdr_ssm_bwd_workspace_size(c.ref)
     ws = _bytes(n, dev)
-    with _guard(x):
-        check(lib.gdr_ssm_bwd(c.ref, *c.inputs(), _ptr(dy), _ptr(dht), _ptr(c.state), _ptr(kept),
-                              _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(db),
-                              _ptr(dh0), _ptr(ws), n, _stream(x)))
+    _launch(x, lib.gdr_ssm_bwd, c.ref, *c.inputs(), _ptr(dy), _ptr(dht), _ptr(c.state), _ptr(kept),
+            _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(db), _ptr(dh0),
+            _ptr(ws), n)
     return dx, ddt, dA, dB, dC, dD, db, dh0
 
 
@@ -412,9 +404,8 @@ def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_
     if inplace_final_state:
         last = initial_state
     elif output_final_state:
-        last = torch.empty(c.state_shape, dtype=torch.float32, device=x.device)
-    with _guard(x):
-        check(lib.gdr_ssm_step(c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last), _stream(x)))
+        last = x.new_empty(c.state_shape, dtype=torch.float32)
+    _launch(x, lib.gdr_ssm_step, c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last))
     return y, last
 
 
@@ -446,11 +437,9 @@ class _Norm:
             flat = x.unsqueeze(0) if x.dim() == 2 else x.flatten(0, -3) if x.dim() > 3 else x
             x, stride = _token_rows(flat, 1)
         self.x = x
-        self.p = NormProblem(rows=rows, D=D, dtype=dt,
-                             res_dtype=dt if res_dtype is None else _DT.get(res_dtype, -1),
-                             w_dtype=_code(weight, "weight"),
-                             has_residual=0 if res_dtype is None else 1, quant=_FORMATS[fmt],
-                             group_size=int(group_size), eps=float(eps), x_stride=stride)
+        self.p = NormProblem(rows, D, dt, dt if res_dtype is None else _DT.get(res_dtype, -1),
+                             _code(weight, "weight"), 0 if res_dtype is None else 1, _FORMATS[fmt],
+                             int(group_size), float(eps), stride)
         self.ref = ctypes.byref(self.p)
 
 
@@ -464,11 +453,10 @@ def _norm_fwd(x, weight, eps, residual, fmt, group_size, need_rstd):
     scale = None
     if fmt is not None:
         groups = 1 if group_size == 0 else -(-D // group_size)
-        scale = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=dev)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_rstd else None
-    with _guard(x):
-        check(lib.gdr_rms_norm_fwd(c.ref, _ptr(c.x), _ptr(residual), _ptr(c.weight), _ptr(y),
-                                   _ptr(scale), _ptr(h), _ptr(rstd), _stream(x)))
+        scale = x.new_empty(x.shape[:-1] + (groups,), dtype=torch.float32)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32) if need_rstd else None
+    _launch(x, lib.gdr_rms_norm_fwd, c.ref, _ptr(c.x), _ptr(residual), _ptr(c.weight), _ptr(y),
+            _ptr(scale), _ptr(h), _ptr(rstd))
     return y, scale, h, rstd
 
 
@@ -507,10 +495,8 @@ def rms_norm_bwd(dy, h, weight, rstd, dh=None, has_residual=False):
     dw = torch.empty_like(c.weight)
     n = lib.gdr_rms_norm_bwd_workspace_size(c.ref)
     ws = _bytes(n, dev)
-    with _guard(dy):
-        check(lib.gdr_rms_norm_bwd(c.ref, _ptr(dy), _ptr(stream), _ptr(c.weight), _ptr(rstd),
-                                   _ptr(dh), _ptr(dx), _ptr(dres), _ptr(dw), _ptr(ws), n,
-                                   _stream(dy)))
+    _launch(dy, lib.gdr_rms_norm_bwd, c.ref, _ptr(dy), _ptr(stream), _ptr(c.weight), _ptr(rstd),
+            _ptr(dh), _ptr(dx), _ptr(dres), _ptr(dw), _ptr(ws), n)
     if not has_residual:
         return dx, None, dw
     return dx, dx if dres is None else dres, dw
