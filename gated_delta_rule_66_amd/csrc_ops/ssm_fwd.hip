@@ -2,12 +2,19 @@
 // chunk on matrix instructions, single tokens on cached states.
 //
 // A prompt moves 4 V bytes of x and y per token and head (16 bits) and needs
-// about 2 K V multiply-adds: on this card memory and the matrix units take
-// about the same time, and few heads leave CUs idle.  So sequences are cut
-// into segments until the launch fills the chip: ssm_state_kernel forms what
-// every segment but the last adds to the state (reads x and B only),
-// ssm_combine_kernel adds them up along each sequence, and ssm_out_kernel
-// walks each segment from its start state.
+// about 2 K V multiply-adds, 5 K V with the pairs and triples that keep the
+// state exact: on this card memory and the matrix units take about the same
+// time, and few heads leave CUs idle.  So sequences are cut into segments until
+// the launch fills the chip: one walk forms what every segment but the last
+// adds to the state (reads x and B only), ssm_combine_kernel adds these up
+// along each sequence, and a second walk goes through each segment from its
+// start state.
+//
+// Measured at 65,536 tokens, 32 heads in 8 groups, K = 128, V = 64, bf16: the
+// state walk 133 us for 402 MB (3.0 TB/s; 104 us with the update left out), the
+// outputs' 280 us for 841 MB (206), the sums in between 17 us.  Both walks are
+// bound by their loads and, little less, by the vector and matrix
+// instructions of the update; two chunks in flight instead of one took as long.
 #include <algorithm>
 #include <cmath>
 
@@ -17,12 +24,12 @@ namespace gdr {
 
 namespace {
 
-template <typename T, int K, int V, int HPW>
+template <typename T, int K, int V, int HPW, bool OUT>
 struct WalkSmem {
-  T C[64 * K];
+  T C[OUT ? 64 * K : 0];
   T B[64 * K];
   T X[64 * HPW * V];
-  T M[HPW][64 * 64];
+  T M[OUT ? HPW : 0][64 * 64];
   float gam[HPW][2][64];  // in powers of two
   float eg[HPW][2][64], wt[HPW][2][64], dts[HPW][2][64], decay[HPW][2];
 };
@@ -34,21 +41,24 @@ struct WalkSmem {
 //
 // A workgroup walks HPW heads of one group, which share the B and C tiles and
 // the scores C B^T; each wave holds 16 PT columns of one head's state in
-// accumulators and reads every operand of B and C once for them.  Per chunk,
+// accumulators and reads every operand of B and C once for them: 32 columns
+// for outputs, whose LDS reads count (65,536 tokens as above: 437 us with 16,
+// 384 with 32), 16 for states, where twice the waves hide more latency
+// (136 us with 32, 133 with 16).  Per chunk,
 // the tiles of the next one are in registers (in flight), those of this one
 // in LDS, swizzled so that no operand read has bank conflicts; the last waves,
 // which have the fewest score tiles, form the next chunk's gates.
 enum { kOut, kState, kGrad };
 template <typename T, int K, int V, int HPW, int PT, int MODE>
-__global__ __launch_bounds__(4 * HPW * V / PT, HPW * PT == 1 ? 3 : 2) void ssm_walk_kernel(SsmArgs a) {
+__global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 ? 3 : 2) void ssm_walk_kernel(SsmArgs a) {
   typedef typename VT<T>::x8 x8;
   typedef typename VT<T>::x4 x4;
   constexpr int NW = HPW * V / (16 * PT), WPH = NW / HPW, NTH = 64 * NW, NT = K / 16;
   constexpr int XC = HPW * V;  // columns of the x tile
   constexpr bool OUT = MODE == kOut;
   constexpr bool kScaled = !__is_same(T, __bf16);
-  static_assert(NW == 4 || NW == 8, "score tiles are dealt to four or eight waves");
-  __shared__ __align__(16) WalkSmem<T, K, V, HPW> s;
+  static_assert(!OUT || NW == 4, "each wave forms one column of score tiles");
+  __shared__ __align__(16) WalkSmem<T, K, V, HPW, OUT> s;
   const int R = a.H / a.G, slots = (R + HPW - 1) / HPW;
   const int L = xcd_order(blockIdx.x, gridDim.x);
   const int part = L % slots, grp_h = L / slots % a.G, id = L / (slots * a.G);
@@ -171,11 +181,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, HPW * PT == 1 ? 3 : 2) void ssm_w
         up = ldexpf(1.f, e);
         down = ldexpf(1.f, -e);
       }
-      // score tiles (row blocks r0 .. r1 - 1) of this wave: the block's column
-      // is w % 4; of eight waves, two share a column's tiles
-      const int cb = wf & 3, mine = (NW == 8 ? (5 - cb) >> 1 : 4);
-      const int r0 = NW == 8 && wf >= 4 ? cb + mine : cb;
-      const int r1 = NW == 8 && wf < 4 ? cb + mine : 4;
+      const int cb = wf;  // wave w: the score tiles of column block w, on and below the diagonal
 #pragma unroll
       for (int kb = 0; kb < K / 32; ++kb) {
         x8 sf[PT];
@@ -203,7 +209,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, HPW * PT == 1 ? 3 : 2) void ssm_w
         const f32x4 di = *reinterpret_cast<const f32x4*>(&s.dts[hh][b][i]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if (r >= r0 && r < r1) {
+          if (r >= cb) {
             const int row = 16 * r + col;
             const float gr = s.gam[hh][b][row];
             x4 o;
@@ -303,12 +309,12 @@ void launch_walk(const gdr_ssm_problem* p, const SsmArgs& a, const char* name, h
   const dim3 grid((unsigned)((int64_t)a.nids * p->G * ((R + heads - 1) / heads)));
   ssm_by_shape(p, [&](auto t, auto k, auto v) {
     using T = decltype(t);
-    constexpr int K = k.value, V = v.value;
+    constexpr int K = k.value, V = v.value, PT = MODE == kOut ? 2 : 1;
     if constexpr (V == 128) {
-      GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 1, 2, MODE>), grid, dim3(256), st, a);
+      GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 1, PT, MODE>), grid, dim3(512 / PT), st, a);
     } else {
       if (heads == 2)
-        GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 2, 2, MODE>), grid, dim3(256), st, a);
+        GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 2, PT, MODE>), grid, dim3(512 / PT), st, a);
       else
         GDR_LAUNCH(name, (ssm_walk_kernel<T, K, V, 1, 1, MODE>), grid, dim3(256), st, a);
     }
