@@ -131,10 +131,10 @@ struct Taps {
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        b[e] = (a.bias && e < m) ? load_param(a.bias, c + e, a.wdt) : 0.f;
+        b[e] = (a.bias && e < m) ? load_scalar(a.bias, c + e, a.wdt) : 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j)
-          w[j][e] = e < m ? load_param(a.w, (int64_t)(c + e) * W + j, a.wdt) : 0.f;
+          w[j][e] = e < m ? load_scalar(a.w, (int64_t)(c + e) * W + j, a.wdt) : 0.f;
       }
     }
   }

@@ -68,11 +68,6 @@ __device__ __forceinline__ void load_params(const void* p, int64_t i, int dtype,
   else load_values<float, COUNT>(reinterpret_cast<const float*>(p) + i, f);
 }
 
-// n consecutive values of a parameter held in 16 bits or fp32
-__device__ __forceinline__ float load_param(const void* p, int64_t i, int dtype) {
-  return load_scalar(p, i, dtype);
-}
-
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + __expf(-z)); }
 

@@ -316,7 +316,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool in = REV ? ib + e >= ia : ib + e <= ia;
-            const float lx = exp2_fast(fminf(REV ? gam_b[e] - gam_a : gam_a - gam_b[e], 0.f));
+            const float lx = exp2_fast(REV ? gam_b[e] - gam_a : gam_a - gam_b[e]);
             const float lm = in ? lx : 0.f;
             const float f = vt[e] * lm;
             const float fd = f * (REV ? dt_a : dt_b[e]);

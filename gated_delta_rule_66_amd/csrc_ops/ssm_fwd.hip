@@ -215,7 +215,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
             x4 o;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float v = sc[r][e] * exp2_fast(fminf(gr - gi[e], 0.f)) * di[e];
+              const float v = sc[r][e] * exp2_fast(gr - gi[e]) * di[e];
               o[e] = from_f<T>(row >= i + e ? v : 0.f);
             }
             *row4(s.M[hh], om, 16 * r, 16 * cb) = o;
@@ -510,7 +510,8 @@ SsmPlan ssm_plan(const gdr_ssm_problem* p, int64_t per_seg, int64_t slots) {
       best_sc = sc;
     }
     if (sc == longest) break;
-    sc = std::min(longest, sc < 32 ? sc + 1 : sc + sc / 8);
+    // (of many sequences fewer lengths: each costs the host a look at all of them)
+    sc = std::min(longest, seqs > 64 ? sc + sc / 2 : sc < 32 ? sc + 1 : sc + sc / 8);
   }
   SsmPlan pl;
   pl.split = best_sc < longest;

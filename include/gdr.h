@@ -401,7 +401,7 @@ int gdr_profile_read(char* names, size_t name_stride, double* total_ms, int* lau
  * may run at once on different streams if they share no output or workspace.
  * Where a problem states a token stride, consecutive tokens' rows of that
  * input lie so many elements apart (a slice of a wider tensor); every other
- * tensor is contiguous.  These operators ask only for the alignment of one
+ * tensor is contiguous.  Outputs overlap no input unless a function says so.  These operators ask only for the alignment of one
  * element unless a function says otherwise. */
 
 /* ---- short causal depthwise convolution ----
@@ -468,7 +468,9 @@ gdr_status gdr_conv1d_update(const gdr_conv_problem* p, const void* x, void* sta
  * states and their gradients are as exact as fp32 inputs would make them, the
  * products inside a chunk (64 tokens) round their decayed scores to in_dtype:
  * with fp16 their magnitude |C_t . B_s| dt_s, and the state's, must stay below
- * 65504. */
+ * 65504.  A chunk's decays are formed from prefix sums of the log decays in
+ * fp32: each is within 2^-23 of the largest |sum| of its chunk, relatively.
+ * Step sizes may be negative without softplus (the state then grows). */
 typedef struct {
   int32_t B, T, H, G, K, V;
   int32_t N;                      /* sequences: B, or len(cu_seqlens) - 1 */

@@ -245,6 +245,38 @@ def test_slices_of_one_projection_are_read_in_place():
         assert torch.equal(y, y2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("K,V,dtype", [(64, 64, HF), (128, 128, BF)])
+def test_negative_steps(K, V, dtype):
+    """Without softplus a step may be negative: the state then grows.  Log
+    decays are up to 1 a token here and sum to a few, so the tolerances' bound
+    on the exponents (16) holds."""
+    t = make(1, 300, 2, 1, K, V, dtype, dt_dtype=F32, softplus=False, bias=False, lens=[130, 170])
+    t["dt"] = torch.randn(t["dt"].shape, generator=torch.Generator().manual_seed(5)) / 64
+    g = dev(t)
+    y, last = gdr.chunk_selective_scan_fwd(*args(g), False, g["state"], True, g["cu"], t["cu"])
+    got = gdr.chunk_selective_scan_bwd(*args(g)[:5], g["dy"], g["D"], None, False, g["dlast"], g["state"],
+                                       g["cu"], t["cu"])
+    r = ref.scan(t["x"], t["dt"], t["A_log"], t["B"], t["C"], t["D"], None, False, t["state"], t["cu"],
+                 t["dy"], t["dlast"])
+    check_forward(t, y, last, r)
+    for n, v in zip(GRADS, got):
+        if v is not None:
+            ref.held(n, v, r[n], r[n + "m"], v.dtype, grad_slack(n, dtype))
+    y, last = gdr.fused_recurrent_selective_scan(*args(g), False, g["state"], True, g["cu"], t["cu"])
+    check_forward(t, y, last, r)
+
+
+def test_many_short_sequences():
+    """More sequences than the cut looks at one by one, some of one token."""
+    lens = [1 + (i * 7) % 40 for i in range(150)] + [0, 900]
+    t = make(1, sum(lens), 2, 1, 64, 64, BF, lens=lens)
+    g = dev(t)
+    y, last = gdr.chunk_selective_scan_fwd(*args(g), True, g["state"], True, g["cu"], t["cu"])
+    r = ref.scan(t["x"], t["dt"], t["A_log"], t["B"], t["C"], t["D"], t["dt_bias"], True, t["state"],
+                 t["cu"])
+    check_forward(t, y, last, r)
+
+
 def test_packed_sequences_are_independent():
     """Each packed sequence has the bits of its own dense run when neither is
     cut; NaNs stay in their sequence."""
