@@ -160,6 +160,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
     rb.store(s.B);
     if (OUT) rc.store(s.C);
     __syncthreads();
+    if (c + 1 < nch) request(token(c + 1));
 
     f32x4 acc[PT][4];
     if (OUT) {
@@ -230,7 +231,6 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
       }
       __syncthreads();
     }
-    if (c + 1 < nch) request(token(c + 1));
 
     if (active) {
       // x^T fragments serve the product with M and, weighted, the state's
