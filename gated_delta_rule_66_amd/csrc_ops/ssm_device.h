@@ -252,8 +252,12 @@ __device__ __forceinline__ int state_exponent(const f32x4* S) {
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(S[nt][e]));
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  m = fmaxf(m, dpp_mov<0xB1>(m));
+  m = fmaxf(m, dpp_mov<0x4E>(m));
+  m = fmaxf(m, dpp_mov<0x141>(m));
+  m = fmaxf(m, dpp_mov<0x140>(m));
+  m = fmaxf(m, __shfl_xor(m, 16, 64));
+  m = fmaxf(m, __shfl_xor(m, 32, 64));
   const int e = 14 - __builtin_amdgcn_frexp_expf(m);
   return m > 0.f && m < __builtin_inff() ? min(max(e, -100), 100) : 100;
 }
