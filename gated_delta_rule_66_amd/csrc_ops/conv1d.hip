@@ -5,11 +5,14 @@
 // last inputs of what came before) or zero.
 //
 // Every operand is touched once and there are about 2 W flops per element, so
-// memory bounds all three kernels.  A thread owns 16 bytes of channels (8 in
-// the gradient, whose window of rows, weights and sums would otherwise leave
-// too few waves) and walks a run of tokens with the last W - 1 rows in
+// memory bounds all three kernels.  A thread owns 16 bytes of channels (8 bytes
+// in small gradients) and walks a run of tokens with the last W - 1 rows in
 // registers, so x is read once plus W - 1 rows per run; the rows of the next
-// group are requested before the current group is computed.  Where the width
+// group are requested before the current group is computed.  Runs have 64
+// tokens where the chip is full with them, and fewer, to 8, where it is not (512
+// tokens of 4096 channels: 10 us against 25 with runs of 64); narrow tensors
+// take fewer channels and more runs per block (60,000 tokens of 24 channels:
+// 9 us against 26 with 64 channel vectors per block).  Where the width
 // is no multiple of the vector, the last vector of a row is moved back to end
 // with the row: it repeats some channels, with the same bits, and the loop
 // has no partial accesses.
@@ -140,6 +143,8 @@ struct Taps {
   }
 };
 
+// The forward: 8192 tokens of 12,288 bf16 channels take 75 us, 5.4 TB/s, what
+// a large copy reaches.
 template <typename T, int N, int W, bool SILU, bool PART>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a) {
   const int cvi = threadIdx.x & (a.cv - 1), sub = threadIdx.x / a.cv;
@@ -235,6 +240,9 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a) {
 // and writes dx W - 1 tokens behind; a run reads W - 1 rows past its end.
 // dw and db are summed in fp32 per run, over the block's runs through LDS in
 // a fixed order, and over the blocks by conv_reduce_kernel: no atomics.
+// 8192 tokens of 12,288 bf16 channels take 146 us, 4.1 TB/s: some 30 vector
+// operations per element, an exponential and a reciprocal at a quarter of the
+// rate among them, take about 115 us by themselves.
 template <typename T, int N, int W, bool SILU, bool PART>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a) {
   __shared__ float red[kThreads * N];
@@ -420,7 +428,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a) {
 }
 
 // dw[d][j] and db[d] from the blocks' sums: 64 columns by 16 shares of the
-// blocks (fixed order).
+// blocks (fixed order).  6 to 8 us, mostly latency; at most 512 blocks' sums
+// (2048 of them cost the gradient 190 instead of 157 us).
 __global__ __launch_bounds__(1024) void conv_reduce_kernel(const float* part, int blocks, int D,
                                                            int W, void* dw, void* db, int wdt) {
   __shared__ float red[16][64];
@@ -447,7 +456,8 @@ __global__ __launch_bounds__(1024) void conv_reduce_kernel(const float* part, in
 
 // One or a few tokens per sequence on a cached state, updated in place: the
 // thread that reads a state column writes it, so vectors do not overlap and
-// the last one of a row may be partial (TAIL).
+// the last one of a row may be partial (TAIL).  256 sequences of 12,288 bf16
+// channels: 50 MB in 8.8 us from the caches.
 template <typename T, int N, int W, bool SILU, bool TAIL>
 __global__ __launch_bounds__(kThreads) void conv_update_kernel(ConvArgs a) {
   const int bx = blockIdx.x % a.xblocks, n = blockIdx.x / a.xblocks;
@@ -544,9 +554,16 @@ int empty_rows(const gdr_conv_problem* p, int runs) {
   return 0;
 }
 
-// Channels per thread: 16 bytes of the type, 4 channels in the gradient.
+// Channels per thread: 16 bytes of the type.  In the gradient, whose rows,
+// weights and sums take 142 registers for four channels and 250 for eight, 16
+// bytes where that still leaves a run of 64 tokens to every thread (8192
+// tokens of 12,288 bf16 channels: 146 us against 157), else four channels
+// (512 tokens of 4096: 15 us against 21; 4096 of 64: 11 against 15).
 int fwd_channels(const gdr_conv_problem* p) { return p->dtype == GDR_FP32 ? 4 : 8; }
-constexpr int kBwdChannels = 4;
+int bwd_channels(const gdr_conv_problem* p) {
+  const int wide = fwd_channels(p);
+  return shape_of(p, wide, kBwdBlocks, kMostParts).ts >= 64 ? wide : 4;
+}
 
 // The type, the width, the activation and whether some access is partial.
 template <typename F>
@@ -600,23 +617,29 @@ gdr_status launch_conv_fwd(const gdr_conv_problem* p, const void* x, const void*
 }
 
 size_t conv_bwd_workspace(const gdr_conv_problem* p) {
-  const Shape s = shape_of(p, kBwdChannels, kBwdBlocks, kMostParts);
+  const Shape s = shape_of(p, bwd_channels(p), kBwdBlocks, kMostParts);
   return align256((size_t)s.yblocks * (p->W + 1) * p->D * sizeof(float));
 }
 
 gdr_status launch_conv_bwd(const gdr_conv_problem* p, const void* x, const void* weight,
                            const void* bias, const void* dy, const void* ds1, const void* s0,
                            void* dx, void* dw, void* db, void* ds0, void* ws, hipStream_t st) {
-  const Shape s = shape_of(p, kBwdChannels, kBwdBlocks, kMostParts);
+  const int N = bwd_channels(p);
+  const Shape s = shape_of(p, N, kBwdBlocks, kMostParts);
   ConvArgs a = args_of(p, s);
   a.x = x; a.w = weight; a.bias = bias; a.s0 = s0; a.dy = dy; a.ds1 = ds1;
   a.dx = dx; a.ds0 = ds0; a.part = reinterpret_cast<float*>(ws);
   a.empty_rows = ds0 ? empty_rows(p, kThreads / s.cv) : 0;
   const dim3 grid((unsigned)s.xblocks * (unsigned)(s.yblocks + a.empty_rows));
-  by_type(p, p->D < kBwdChannels, [&](auto t, auto w, auto silu, auto part) {
-    GDR_LAUNCH("conv_bwd",
-               (conv_bwd_kernel<decltype(t), kBwdChannels, w.value, silu.value, part.value>), grid,
-               dim3(kThreads), st, a);
+  by_type(p, p->D < N, [&](auto t, auto w, auto silu, auto part) {
+    using T = decltype(t);
+    constexpr int wide = 16 / (int)sizeof(T);
+    if (N == 4)
+      GDR_LAUNCH("conv_bwd", (conv_bwd_kernel<T, 4, w.value, silu.value, part.value>), grid,
+                 dim3(kThreads), st, a);
+    else
+      GDR_LAUNCH("conv_bwd", (conv_bwd_kernel<T, wide, w.value, silu.value, part.value>), grid,
+                 dim3(kThreads), st, a);
   });
   const int64_t cols = (int64_t)(p->W + 1) * p->D;
   GDR_LAUNCH("conv_reduce", conv_reduce_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), st,

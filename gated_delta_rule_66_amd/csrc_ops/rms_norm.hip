@@ -154,7 +154,10 @@ constexpr int block_of() {
   return NT == 64 ? 256 : NT;
 }
 
-// RES: the residual's type, void without one.
+// The forward.  RES: the residual's type, void without one.  Memory bounds it:
+// 16,384 rows of 4096 bf16 columns with a residual to e4m3 take 87 us for 472
+// MB (5.4 TB/s), 8192 of them to bf16 46 us for 268 MB (5.8); eight rows take 5
+// us, the latency of a load and two reductions.
 template <typename T, typename RES, bool QUANT, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
   constexpr bool kRes = !std::is_void<RES>::value;
@@ -278,6 +281,8 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
 //   dw = sum_rows dy u.
 // A block walks rows blockIdx.x, + blocks, ... with dw in registers and
 // leaves its sum in `part`; norm_reduce_kernel adds the blocks in order.
+// Memory bounds it: 8192 rows of 4096 bf16 columns take 55 us for 285 MB (5.2
+// TB/s).
 template <typename T, typename RES, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void norm_bwd_kernel(NormArgs a) {
   constexpr bool kRes = !std::is_void<RES>::value;
@@ -359,7 +364,8 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_bwd_kernel(NormArgs a) {
   }
 }
 
-// dweight over the blocks: 16 columns by 16 shares of the blocks.
+// dweight over the blocks: 16 columns by 16 shares of the blocks.  6 us for
+// 4096 columns and 1024 blocks, mostly latency.
 __global__ __launch_bounds__(256) void norm_reduce_kernel(const float* part, int blocks, int D,
                                                           void* dw, int wdt) {
   __shared__ float red[16][17];
@@ -383,7 +389,8 @@ __global__ __launch_bounds__(256) void norm_reduce_kernel(const float* part, int
 // 1024 columns, 256 threads up to 16384, 1024 up to 65536.  One wave for wider
 // rows would need no barriers but holds more of a row per thread: 16384 rows
 // of 4096 columns to e4m3 take 125 us with one wave a row and 88 us with 256
-// threads, 8192 rows with a residual 54 and 47 us.
+// threads, 8192 rows with a residual 54 and 47 us.  Beyond 16384 columns 256
+// threads would hold more than 64 elements each, and spill.
 template <typename F>
 void by_width(int D, F f) {
   const int nv = (D + 7) / 8;

@@ -547,7 +547,8 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
 
 }  // namespace
 
-// Columns of a wave, in blocks of 16.
+// Columns of a wave, in blocks of 16: 32 where two heads of V = 128 share a
+// workgroup (16 waves of 16 columns would have 128 registers each).
 template <int V, int HPW>
 constexpr int kGradColumns = V == 128 && HPW == 2 ? 2 : 1;
 

@@ -71,6 +71,25 @@ def test_forward_and_gradients(name):
         ref.held(k, v, *r[k], v.dtype, SUM_SLACK if k in ("dw", "db") else SLACK)
 
 
+@pytest.mark.parametrize("dtype,W,D", [(BF, 4, 12301), (HF, 3, 12296), (F32, 2, 6151)])
+def test_large_gradients(dtype, W, D):
+    """Sizes whose gradient takes the wide form; the reference on some channels
+    (they are independent), the last ones among them."""
+    B, T = 2, 4100 if dtype != F32 else 4200
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s, dt=dtype: torch.randn(*s, generator=g, device="cuda").to(dt)  # noqa: E731
+    t = dict(x=r(B, T, D), w=r(D, W, dt=F32), b=r(D, dt=F32), s=r(B, W - 1, D), dy=r(B, T, D),
+             ds=r(B, W - 1, D))
+    dx, dw, db, ds = gdr.causal_conv1d_bwd(t["x"], t["w"], t["b"], t["dy"], t["ds"], "silu", t["s"])
+    pick = torch.tensor(list(range(5)) + [D // 2, D // 2 + 1] + list(range(D - 9, D)))
+    c = lambda v, dim: v.index_select(dim, pick.cuda())  # noqa: E731
+    want = ref.conv(c(t["x"], 2), c(t["w"], 0), c(t["b"], 0), True, c(t["s"], 2), None, c(t["dy"], 2),
+                    c(t["ds"], 2))
+    for name, got, dt in (("dx", c(dx, 2), dtype), ("dw", c(dw, 0), F32), ("db", c(db, 0), F32),
+                          ("ds", c(ds, 2), dtype)):
+        ref.held(name, got, *want[name], dt, SUM_SLACK if name in ("dw", "db") else SLACK)
+
+
 def test_a_slice_of_a_wider_tensor_is_read_in_place():
     g = torch.Generator().manual_seed(3)
     wide = torch.randn(2, 50, 77, generator=g).to(BF).cuda()
