@@ -30,9 +30,12 @@
 // tiles of dB or dC are dealt over all waves, for which the states are passed
 // through LDS once, rounded.  The order within a chunk keeps few registers
 // live at once (at K = V = 128 a wave's states take 64 of its 256): scores go to
-// LDS as they are formed, and dx is stored before the next chunk is requested.
-// With 8192 tokens, 32 heads in 16 groups, K = V = 128 the walks take 124 and
-// 153 us; bound by LDS reads and by latency at two waves per SIMD.
+// LDS as they are formed.  The next chunk is requested as soon as this one is
+// in LDS, where registers allow (K = 64, V = 128, two heads, backward: 90
+// against 93 us; K = 128, V = 64: 82 against 86), and in the backward walk
+// with K = V = 128 after dx is stored.  With 8192 tokens, 32 heads in 16
+// groups, K = V = 128 the walks take 116 and 160 us; bound by LDS reads and by
+// latency at two waves per SIMD.
 #pragma once
 
 #include "ssm_device.h"
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
   typedef typename VT<T>::x4 x4;
   constexpr int NW = HPW * V / (16 * PT), WPH = NW / HPW, NTH = 64 * NW, NT = K / 16;
   constexpr int TPW = 4 * NT / NW, MT = kMostTiles<NW>, RB = kPublished<K, V, HPW>;
-  constexpr bool kScaled = !__is_same(T, __bf16);
+  constexpr bool kScaled = !__is_same(T, __bf16), kEarly = !REV || K * V < 128 * 128;
   static_assert(TPW >= 1 && (NW == 4 || NW == 8), "tiles are dealt to all waves");
   __shared__ __align__(16) GradSmem<T, K, V, HPW, NW, REV> s;
   const SsmArgs& a = ga.f;
@@ -286,6 +289,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
       if (c + 1 < nch) request_dt(c + 1);
     }
     __syncthreads();  // A: tiles, gates and the first state columns are in LDS
+    if (kEarly && c + 1 < nch) request(c + 1);
 
     // scores (transposed: rows b, columns a), their sums over b, and W summed
     // over the heads
@@ -457,7 +461,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (c + 1 < nch) request(c + 1);
+    if (!kEarly && c + 1 < nch) request(c + 1);
     if (RB < HPW && nh > 1) inter(HPW - 1);
     if (active)
       update_state<T, K, REV>(S, Q, ok, xf, REV ? s.eg[hw] : s.wt[hw], g4, s.decay[hw]);
