@@ -56,6 +56,14 @@ def _new(t, dtype=None):
     return t.new_empty(t.shape, dtype=dtype)
 
 
+def _fits(name, *sizes):
+    """The library takes sizes in 32 bits, and a conversion would drop the
+    higher ones without a word: a size that does not fit is refused here."""
+    for v in sizes:
+        if not -1 << 31 <= v < 1 << 31:
+            raise GdrError(2, "%s has a size that does not fit 32 bits: %s" % (name, sizes))
+
+
 def _need_gpu(name, t):
     if not t.is_cuda:
         raise GdrError(8, "%s is on %s; the kernels run on an MI355X" % (name, t.device))
@@ -110,11 +118,17 @@ def _seqs(x, cu_seqlens, cu_seqlens_cpu):
         if cu_seqlens_cpu is not None:
             raise GdrError(6, "cu_seqlens_cpu is given without cu_seqlens")
         return x.shape[0], None, None
-    dev = cu_seqlens.to(device=x.device, dtype=torch.int32).contiguous()
     if cu_seqlens_cpu is None:
         # one blocking device-to-host copy (pass cu_seqlens_cpu to avoid it)
         cu_seqlens_cpu = cu_seqlens.detach().to("cpu")
-    host = cu_seqlens_cpu.to(device="cpu", dtype=torch.int32).contiguous()
+    for t in (cu_seqlens, cu_seqlens_cpu):
+        if t.dtype not in (torch.int32, torch.int64):
+            raise GdrError(6, "cu_seqlens must be int32 or int64, got %s" % t.dtype)
+    wide = cu_seqlens_cpu.to(device="cpu")
+    host = wide.to(torch.int32).contiguous()
+    if wide.dtype != torch.int32 and not torch.equal(host.to(wide.dtype), wide):
+        raise GdrError(6, "cu_seqlens has offsets that do not fit 32 bits")
+    dev = cu_seqlens.to(device=x.device, dtype=torch.int32).contiguous()
     if host.dim() != 1 or host.numel() < 2 or dev.shape != host.shape:
         raise GdrError(6, "cu_seqlens needs one offset per sequence and the end, got shape %s"
                        % (tuple(host.shape),))
@@ -142,9 +156,11 @@ class _Conv:
         if x.dim() != 3 or weight.dim() != 2:
             raise GdrError(2, "x must be [B, T, D] and weight [D, W], got %s and %s"
                            % (tuple(x.shape), tuple(weight.shape)))
-        _need_gpu("x", x)
         B, T, D = x.shape
         W = weight.shape[1]
+        _fits("x", B, T, D)
+        _fits("weight", W)
+        _need_gpu("x", x)
         dev = x.device
         dt = _code(x, "x")
         self.weight = _like("weight", weight, (D, W), (x.dtype, torch.float32), dev)
@@ -256,9 +272,11 @@ class _Ssm:
         if x.dim() != 4 or B.dim() != 4:
             raise GdrError(2, "x must be [B, T, H, V] and B [B, T, G, K], got %s and %s"
                            % (tuple(x.shape), tuple(B.shape)))
-        _need_gpu("x", x)
         b, T, H, V = x.shape
         G, K = B.shape[2], B.shape[3]
+        _fits("x", b, T, H, V)
+        _fits("B", G, K)
+        _need_gpu("x", x)
         dev = x.device
         code = _code(x, "x")
         _expect("B", B, (b, T, G, K), (x.dtype,), dev)
@@ -422,13 +440,17 @@ class _Norm:
         if x.dim() < 1 or weight.dim() != 1:
             raise GdrError(2, "x must be [..., D] and weight [D], got %s and %s"
                            % (tuple(x.shape), tuple(weight.shape)))
-        _need_gpu("x", x)
         D = x.shape[-1]
-        dt = _code(x, "x")
+        rows = x.numel() // D if D else 0
+        _fits("x", rows, D)
         if fmt not in _FORMATS:
             raise GdrError(10, "format must be 'fp8' or 'int8', got %r" % (fmt,))
+        # the number of scales follows from it before the library sees it
+        if group_size not in (0, 128):
+            raise GdrError(10, "group_size must be 0 (the row) or 128, got %r" % (group_size,))
+        _need_gpu("x", x)
+        dt = _code(x, "x")
         self.weight = _like("weight", weight, (D,), (x.dtype, torch.float32), x.device)
-        rows = x.numel() // D if D else 0
         # rows one stride apart (a slice of a wider tensor), else a copy
         stride = D
         if x.dim() == 1 or x.is_contiguous():
