@@ -497,6 +497,8 @@ def fused_recurrent_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state
             if output_final_state else None
     check(lib.gdr_recurrent_fwd(c.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                 _ptr(initial_state), _ptr(o), _ptr(ht), _stream(dev)))
+    if inplace_final_state:
+        torch.autograd.graph.increment_version(ht)   # written through its pointer
     return o, ht
 
 

@@ -135,6 +135,17 @@ def _seqs(x, cu_seqlens, cu_seqlens_cpu):
     return host.numel() - 1, dev, host
 
 
+_written = torch.autograd.graph.increment_version
+
+
+def _in_place(name, t):
+    """t is written through its pointer, unseen by autograd: no gradient can
+    pass the update (the caller then tells autograd of it: _written)."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise GdrError(10, "%s requires grad and is updated in place; no gradient passes the update "
+                           "(detach it, or call this under torch.no_grad())" % name)
+
+
 def _bytes(n, device):
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
@@ -250,15 +261,18 @@ def causal_conv1d(x, weight, bias=None, activation="silu", initial_state=None,
 def causal_conv1d_update(x, conv_state, weight, bias=None, activation="silu"):
     """One or a few tokens per sequence on a cached state (decode): returns y,
     shaped like x (``[B, D]`` or ``[B, T, D]``), and updates ``conv_state``
-    ``[B, W-1, D]`` in place.  No autograd."""
+    ``[B, W-1, D]`` in place.  No autograd: a graph that saved ``conv_state``
+    raises in its backward, as after any in-place operation."""
     squeeze = x.dim() == 2
     x3 = x.unsqueeze(1) if squeeze else x
     if not conv_state.is_contiguous():
         raise GdrError(10, "conv_state is updated in place and must be contiguous")
+    _in_place("conv_state", conv_state)
     c = _Conv(x3, weight, bias, activation, conv_state, None, None)
     y = _new(x3)
     _launch(x, lib.gdr_conv1d_update, c.ref, _ptr(c.x), _ptr(conv_state), _ptr(c.weight),
             _ptr(c.bias), _ptr(y))
+    _written(conv_state)
     return y.squeeze(1) if squeeze else y
 
 
@@ -411,10 +425,13 @@ def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_
     """The scan one token at a time (decode steps, a few speculative tokens):
     ``(y, final_state)`` of :func:`chunk_selective_scan`, the state read once
     and written once.  With ``inplace_final_state`` the fp32 ``initial_state``
-    is updated in place and returned.  No autograd."""
+    is updated in place and returned (a graph that saved it raises in its
+    backward, as after any in-place operation).  No autograd."""
     if inplace_final_state and (initial_state is None or not initial_state.is_contiguous()
                                 or initial_state.data_ptr() % 16):
         raise GdrError(10, "inplace_final_state needs a contiguous, 16-byte aligned initial_state")
+    if inplace_final_state:
+        _in_place("initial_state", initial_state)
     c = _Ssm(x, dt, A_log, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens,
              cu_seqlens_cpu)
     y = _new(x)
@@ -424,6 +441,8 @@ def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_
     elif output_final_state:
         last = x.new_empty(c.state_shape, dtype=torch.float32)
     _launch(x, lib.gdr_ssm_step, c.ref, *c.inputs(), _ptr(c.state), _ptr(y), _ptr(last))
+    if inplace_final_state:
+        _written(last)
     return y, last
 
 
