@@ -579,8 +579,8 @@ def rms_norm_quant(x, weight, eps=1e-6, residual=None, format="fp8", group_size=
     ``(q, scale, h)``.  ``format`` ``"fp8"`` (e4m3, largest 448) or ``"int8"``;
     fp32 scales of shape ``x.shape[:-1] + (groups,)``, one per row (``group_size=0``,
     one group) or one per 128 columns (``group_size=128``, ``ceil(D / 128)``):
-    ``scale = max(max|y| / top, 2**-126)`` and ``q = y / scale`` rounded to
-    nearest even.  ``h`` is ``None`` without a residual.  No autograd."""
+    ``scale = max(max|y| / top, 2**-126)`` and q the fp32 quotient ``y / scale``
+    rounded to nearest even.  ``h`` is ``None`` without a residual.  No autograd."""
     if format is None:
         raise GdrError(10, "format must be 'fp8' or 'int8', got None")
     q, scale, h, _ = _norm_fwd(x, weight, eps, residual, format, group_size, False)

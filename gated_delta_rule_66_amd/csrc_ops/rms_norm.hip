@@ -242,14 +242,12 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
       const float inv = 1.f / s;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        // the product with the reciprocal may lie on the other side of a tie,
+        // a whole step off in 8 bits: the residual makes it the fp32 quotient
+        // (where it is finite; infinities keep the product's NaN or 0)
         q[e] = f[i][e] * inv;
-        if (!fp8) {
-          // int8 keeps more bits than e4m3, and a product on the other side of
-          // a tie is a whole step off: the residual makes it the rounded
-          // quotient (where it is finite; infinities keep the product's NaN or 0)
-          const float left = __builtin_fmaf(-q[e], s, f[i][e]);
-          q[e] = fabsf(left) < __builtin_inff() ? __builtin_fmaf(left, inv, q[e]) : q[e];
-        }
+        const float left = __builtin_fmaf(-q[e], s, f[i][e]);
+        q[e] = fabsf(left) < __builtin_inff() ? __builtin_fmaf(left, inv, q[e]) : q[e];
         // a NaN passes both comparisons
         q[e] = q[e] > top ? top : q[e] < -top ? -top : q[e];
       }

@@ -528,7 +528,8 @@ gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const void* x, const void* dt,
  *     y = weight h / sqrt(mean(h^2) + eps)
  * in dtype, or quantised to 8 bits: scale = max(max|y| / top, 2^-126) over the
  * row or over each 128 columns (the last group of a row may be narrower),
- * q = y / scale rounded to nearest even; top = 448 (e4m3, OCP) or 127 (int8).
+ * q = the fp32 quotient y / scale rounded to nearest even; top = 448 (e4m3,
+ * OCP) or 127 (int8).
  * A NaN in a group makes its scale NaN (and an int8 value 0).
  *   x, y, dy, dx [rows, D] dtype (x with a row stride); residual, h, dh,
  *   dresidual [rows, D] res_dtype; weight, dweight [D] w_dtype; q [rows, D]
