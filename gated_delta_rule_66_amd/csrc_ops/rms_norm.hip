@@ -187,15 +187,17 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
       for (int e = 0; e < 8; ++e) f[i][e] = to_f(from_f<R>(f[i][e] + r[kRes ? i : 0][e]));
       if (v0 < a.D) store8<R, PART>(h + c, a.D, f[i]);
     }
-    float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += c + e >= v0 ? f[i][e] * f[i][e] : 0.f;
-    sum += ss;
+    for (int e = 0; e < 8; ++e) {
+      const double v = c + e >= v0 ? f[i][e] : 0.f;
+      sum = __builtin_fma(v, v, sum);
+    }
   }
-  // eight squares in 32 bits, their sums in 64: the mean is its 32-bit
-  // neighbour for any width and any split of the row
+  // squares, mean and root in 64 bits: fp32 values beyond 2^64 have squares
+  // past fp32's range and values below 2^-63 none at all, and the row's
+  // statistic is the same for any width and any split of the row
   sum = row_sum<NT>(sum, reinterpret_cast<double*>(lds));
-  const float rstd = rsqrtf((float)sum / (float)a.D + a.eps);
+  const float rstd = (float)(1.0 / __builtin_sqrt(sum / a.D + (double)a.eps));
   if (a.rstd && tid == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
