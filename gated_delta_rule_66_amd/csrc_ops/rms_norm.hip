@@ -241,15 +241,14 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
     }
     if (v0 < a.D) {
       float q[8];
-      const float inv = 1.f / s;
+      // (an infinite scale leaves the product's 0 or NaN as they are)
+      const float inv = 1.f / s, fin = s < __builtin_inff() ? s : 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         // the product with the reciprocal may lie on the other side of a tie,
         // a whole step off in 8 bits: the residual makes it the fp32 quotient
-        // (where it is finite; infinities keep the product's NaN or 0)
         q[e] = f[i][e] * inv;
-        const float left = __builtin_fmaf(-q[e], s, f[i][e]);
-        q[e] = fabsf(left) < __builtin_inff() ? __builtin_fmaf(left, inv, q[e]) : q[e];
+        q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], fin, f[i][e]), inv, q[e]);
         // a NaN passes both comparisons
         q[e] = q[e] > top ? top : q[e] < -top ? -top : q[e];
       }
