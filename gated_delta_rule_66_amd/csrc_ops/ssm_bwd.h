@@ -8,19 +8,30 @@
 //     dB_t = dt_t P_t x_t                 dC_t = S_t dy_t
 //     ddt_t = rate dg_t + x_t . u_t       dA_log = sum g_t dg_t
 // and dg_t, the gradient of the log decay, is the sum over all pairs i < t <=
-// r of E_ri = e^{g_{i+1} + .. + g_r} dt_i (C_r . B_i)(dy_r . x_i).  A pair
-// counts with + in its row r and - in its column i, so dg is a suffix sum of
-//     row_t - dt_t q_t,   row_r = sum_i E_ri,   q_i = x_i . u_i,
-// plus, at a segment's end, the pairs that span it: <S_end, P_end>.  No state
-// has to meet its gradient at every chunk, and none is stored: two walks, one
-// forward with S, one backward with P, keep them in accumulators.
-//   forward walk:  row_t = sum_{i <= t} (in the chunk) E_ti + e^{gamma_t} dy_t . S^T C_t
-//                  dC    = diag(e^gamma) dY S^T + W B,   W = (dY X^T) o L diag(dt)
+// r of E_ri = e^{g_{i+1} + .. + g_r} dt_i (C_r . B_i)(dy_r . x_i).  Over a
+// chunk these are the pairs inside it, those that end in it, those that begin
+// in it and those that span it, with A the sum over the pairs that span the
+// chunk's end, <S, P> there:
+//     dg_t = (A - sum_{i in chunk} dt_i far_i) + sum_{i < t} dt_i far_i
+//            + sum_{r >= t} (row_r - dt_r q_r)
+//   row_r = sum_{i < r, in the chunk} E_ri + e^{gamma_r} dy_r . S^T C_r,
+//   dt_i q_i = sum_{r > i, in the chunk} E_ri,   far_i = e^{gamma_end - gamma_i} x_i . P^T B_i
+// (the pair i = r spans no decay; it is part of u_i . x_i = q_i + far_i + own_i
+// only).  dg at the chunk's first token is the A of the chunk before: a chain
+// along the segment, from <S_end, P_end> at its end, that would add rounding
+// errors up without limit, since what spans a chunk is a difference of sums.
+// Two things end it.  Where a chunk decays by more than e^-24 nothing spans
+// it; and every kMid chunks the forward walk leaves its fp32 state, which the
+// backward walk multiplies by its own (one head of 4096 tokens, emulated: dA_log
+// off by 0.5 to 8 % of the root of its summed squares with one plain suffix
+// sum, by 0.03 % or less so).  No other state is stored: two walks, one forward
+// with S, one backward with P, keep them in accumulators.
+//   forward walk:  row_t, dC = diag(e^gamma) dY S^T + W B,   W = (dY X^T) o L diag(dt)
 //   backward walk: u     = (C B^T o L)^T dY + diag(e^{gamma_end - gamma}) B P
 //                  dB    = diag(dt e^{gamma_end - gamma}) X P^T + W^T C
 // The scores' row and column sums are taken in fp32 before any rounding, and
-// the state's share in them uses its 16-bit pair (hi + lo): the suffix sum
-// adds rounding errors up, so these must be near fp32.  The other products
+// the state's share in them uses its 16-bit pair (hi + lo): up to kMid chunks
+// of them are added up, so these must be near fp32.  The other products
 // round one operand (W, C B^T o L, S, P) to 16 bits, as their outputs are.
 //
 // One workgroup walks a segment for up to HPW heads of one group at once: they
@@ -42,6 +53,10 @@
 
 namespace gdr {
 
+// Chunks between the states that meet their gradients inside a segment: a
+// multiple of 512 tokens costs the walks 64 to 128 bytes per token and head.
+constexpr int kMid = 8;
+
 struct SsmGradArgs {
   SsmArgs f;            // the forward's inputs, the segments, their start states
   const void* dy;
@@ -54,8 +69,16 @@ struct SsmGradArgs {
   // fp32 [slots][tokens][G][K] when a group's heads take more than one workgroup
   float* part_dB;
   float* part_dC;
-  float* row;           // [H][tokens]
-  float* q;             // [H][tokens]
+  // [H][tokens], the sums above
+  float* row;
+  float* q;
+  float* far;
+  float* own;
+  // the states kMid chunks apart inside segments (register order) and their
+  // products with their gradients, in 8 waves' parts, at (tokens before) / (64 kMid)
+  float* mid_state;     // nullable: no segment has more than kMid chunks
+  float* mid;
+  int mid_parts;        // waves of a head
   float* span;          // [nids][H]: <S_end, P_end>
   float* part_dD;       // [nids][H]
   int slots;            // workgroups per group
@@ -85,7 +108,7 @@ struct GradSmem {
   T GL[REV ? HPW : 0][64 * 64];  // the decayed scores
   float gam[HPW][64];  // in powers of two
   float eg[HPW][64], es[HPW][64], wt[HPW][64], dts[HPW][64], decay[HPW];
-  float pe[HPW][4][64], pa[NW][64];
+  float pe[HPW][4][64], pa[NW][64], po[REV ? HPW : 0][64];
   int ex[NW];
   float fin[HPW][NW];
 };
@@ -315,11 +338,11 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
           const float gam_a = s.gam[hh][ia], dt_a = s.dts[hh][ia];
           const f32x4 gam_b = *reinterpret_cast<const f32x4*>(&s.gam[hh][ib]);
           const f32x4 dt_b = *reinterpret_cast<const f32x4*>(&s.dts[hh][ib]);
-          float sum = 0.f;
+          float sum = 0.f, own = 0.f;  // own: the pair of a token with itself
           x4 z;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const bool in = REV ? ib + e >= ia : ib + e <= ia;
+            const bool in = REV ? ib + e >= ia : ib + e <= ia, self = ib + e == ia;
             const float lx = exp2_fast(REV ? gam_b[e] - gam_a : gam_a - gam_b[e]);
             const float lm = in ? lx : 0.f;
             const float f = vt[e] * lm;
@@ -327,14 +350,20 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
             wsum[e] += fd;
             if (REV) {
               z[e] = from_f<T>(gt[e] * lm);
-              sum += gt[e] * f;
-              dsum[hh] += ib + e == ia ? vt[e] : 0.f;
+              const float one = gt[e] * f;
+              sum += self ? 0.f : one;
+              own += self ? one : 0.f;
+              dsum[hh] += self ? vt[e] : 0.f;
             } else {
-              sum += gt[e] * fd;
+              sum += self ? 0.f : gt[e] * fd;
             }
           }
           sum = sum4g(sum);
           if (g4 == 0) s.pe[hh][bb][ia] = sum;
+          if (REV && ab == bb) {
+            own = sum4g(own);
+            if (g4 == 0) s.po[REV ? hh : 0][ia] = own;
+          }
           if (REV) *row4(s.GL[hh], om, 16 * ab, 16 * bb) = z;
         }
         x4 z;
@@ -471,13 +500,44 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
     }
     if (w < nh && l < rows) {  // wave hh: head hh's sums
       const int blk = l >> 4;
-      float v = 0.f;
+      float v = 0.f, far = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (REV ? i >= blk : i <= blk) v += s.pe[w][i][l];
 #pragma unroll
-      for (int i = 0; i < WPH; ++i) v += s.pa[w * WPH + i][l];
-      (REV ? ga.q : ga.row)[(int64_t)(head0 + w) * ga.tokens + t + l] = v;
+      for (int i = 0; i < WPH; ++i) far += s.pa[w * WPH + i][l];
+      const int64_t o = (int64_t)(head0 + w) * ga.tokens + t + l;
+      if (REV) {
+        ga.q[o] = v;
+        ga.far[o] = far;
+        ga.own[o] = s.po[REV ? w : 0][l];
+      } else {
+        ga.row[o] = v + far;
+      }
+    }
+    // every kMid chunks: the state of the forward walk meets that of the backward one
+    const int edge = REV ? nch - 1 - c : c + 1;
+    if (ga.mid_state && active && edge % kMid == 0 && edge > 0 && edge < nch) {
+      const int64_t at = (sg.t0 + 64ll * edge) / (64 * kMid) * a.H + h;
+      float* ms = ga.mid_state + at * KV;
+      float d = 0.f;
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          f32x4* m = reinterpret_cast<f32x4*>(ms + (((ct0 + pt) * NT + nt) * 64 + l) * 4);
+          if (REV) {
+            const f32x4 v = *m;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d += S[pt][nt][e] * v[e];
+          } else {
+            *m = S[pt][nt];
+          }
+        }
+      if (REV) {
+        d = wave_sum(d);
+        if (l == 0) ga.mid[at * 8 + w % WPH] = d;
+      }
     }
 
     {

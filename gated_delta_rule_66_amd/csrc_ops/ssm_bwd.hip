@@ -8,15 +8,37 @@ namespace gdr {
 
 namespace {
 
-// dg is the suffix sum of row - dt q along a segment plus what spans its end;
-// from it the raw step sizes' gradient and the segment's shares of dA_log and
-// ddt_bias.  One workgroup per (segment, head), 1024 tokens at a time from
-// the end, four per thread.  10 us for 8192 tokens of 32 heads: the chain of
-// 1024-token steps, and reads of dt one head apart.
+// Sums over the 16 lanes of a chunk: of the lanes behind, of the lanes before.
+__device__ __forceinline__ float behind16(float x) {
+  x = dpp_zero<0x101>(x);
+  x += dpp_zero<0x101>(x);
+  x += dpp_zero<0x102>(x);
+  x += dpp_zero<0x104>(x);
+  return x + dpp_zero<0x108>(x);
+}
+__device__ __forceinline__ float before16(float x) {
+  x = dpp_zero<0x111>(x);
+  x += dpp_zero<0x111>(x);
+  x += dpp_zero<0x112>(x);
+  x += dpp_zero<0x114>(x);
+  return x + dpp_zero<0x118>(x);
+}
+__device__ __forceinline__ double wave_sum2(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// dg from the walks' sums (ssm_bwd.h), the raw step sizes' gradient and the
+// segment's shares of dA_log and ddt_bias.  One workgroup per (segment, head),
+// 16 chunks at a time from the end, four tokens per thread: sums inside a chunk
+// in fp32, the chain over the chunks and the shares in 64 bits.
 template <typename DT>
 __global__ __launch_bounds__(256) void ssm_dt_kernel(SsmGradArgs ga, DT* ddt, float* part_dA,
                                                      float* part_db) {
-  __shared__ float tot[4], red[2][4];
+  __shared__ float ends[16], begins[16], spans[16];
+  __shared__ int how[16];  // 0: from the chunk behind, 1: nothing spans the chunk, 2: from a kept state
+  __shared__ double red[2][4];
   const SsmArgs& a = ga.f;
   const int id = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const Segment sg = segment_of(a, id);
@@ -25,57 +47,77 @@ __global__ __launch_bounds__(256) void ssm_dt_kernel(SsmGradArgs ga, DT* ddt, fl
     if (threadIdx.x == 0) part_dA[out] = part_db[out] = 0.f;
     return;
   }
-  const int l = lane_id(), w = threadIdx.x >> 6;
+  const int l = lane_id(), w = threadIdx.x >> 6, c = threadIdx.x >> 4, i16 = threadIdx.x & 15;
   const float rate = -expf(load_scalar(a.A_log, h, a.p_dtype));
   const float bias = param(a.dt_bias, h, a.p_dtype);
-  const float* row = ga.row + (int64_t)h * ga.tokens;
-  const float* q = ga.q + (int64_t)h * ga.tokens;
-  float carry = ga.span[out], dA = 0.f, db = 0.f;
+  const int64_t first = (int64_t)h * ga.tokens;
   const int64_t len = sg.t1 - sg.t0;
+  const int nch = (int)((len + 63) / 64);
+  double chain = ga.span[out], dA = 0.0, db = 0.0;
   for (int64_t b = (len - 1) / 1024; b >= 0; --b) {
     const int64_t t0 = sg.t0 + 1024 * b + 4 * threadIdx.x;
-    float raw[4], step[4], qv[4], sum[4];
+    const int edge = (int)(16 * b) + c + 1;  // the chunk ends where chunk `edge` begins
+    float raw[4], step[4], u[4], sum[4], pre[4], g = 0.f;
 #pragma unroll
     for (int e = 3; e >= 0; --e) {
       const bool live = t0 + e < sg.t1;
+      const int64_t o = first + t0 + e;
       raw[e] = live ? load_scalar(a.dt, (t0 + e) * a.H + h, a.dt_dtype) : 0.f;
       step[e] = live ? ssm_step_size(raw[e], bias, a.softplus) : 0.f;
-      qv[e] = live ? q[t0 + e] : 0.f;
-      sum[e] = (live ? row[t0 + e] - step[e] * qv[e] : 0.f) + (e < 3 ? sum[e < 3 ? e + 1 : 3] : 0.f);
+      const float q = live ? ga.q[o] : 0.f, far = live ? ga.far[o] : 0.f;
+      u[e] = (q + far) + (live ? ga.own[o] : 0.f);
+      sum[e] = (live ? ga.row[o] - step[e] * q : 0.f) + (e < 3 ? sum[e < 3 ? e + 1 : 3] : 0.f);
+      pre[e] = step[e] * far;
+      g += rate * step[e];
     }
-    const float above = wave_suffix_excl(sum[0]);
-    if (l == 0) tot[w] = above + sum[0];
+    const float here = (pre[0] + pre[1]) + (pre[2] + pre[3]);
+    const float behind = behind16(sum[0]), before = before16(here);
+    const bool kept = ga.mid_state && edge % kMid == 0 && edge < nch;
+    float mid = 0.f;
+    if (kept && i16 < ga.mid_parts)
+      mid = ga.mid[((sg.t0 + 64ll * edge) / (64 * kMid) * a.H + h) * 8 + i16];
+    mid = sum16(mid);
+    g = sum16(g);
+    if (i16 == 0) {
+      ends[c] = behind + sum[0];
+      spans[c] = mid;
+      how[c] = g < -24.f ? 1 : kept ? 2 : 0;
+    }
+    if (i16 == 15) begins[c] = before + here;
     __syncthreads();
-    float later = carry, all = 0.f;
+    float over = 0.f;  // what spans this thread's chunk
 #pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      if (i > w) later += tot[i];
-      all += tot[i];
+    for (int i = 15; i >= 0; --i) {
+      if (how[i] == 2) chain = spans[i];
+      chain = how[i] == 1 ? 0.0 : chain - begins[i];
+      if (i == c) over = (float)chain;
+      chain += ends[i];
     }
+    float prefix = before;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (t0 + e < sg.t1) {
-        const float dg = later + above + sum[e];
-        float d = rate * dg + qv[e];
+        const float dg = over + prefix + (behind + sum[e]);
+        float d = rate * dg + u[e];
         if (a.softplus) d *= sigmoid(raw[e] + bias);
         ddt[(t0 + e) * a.H + h] = from_f<DT>(d);
-        dA += dg * rate * step[e];
+        dA += (double)dg * (rate * step[e]);
         db += d;
       }
+      prefix += pre[e];
     }
-    carry += all;
     __syncthreads();
   }
-  dA = wave_sum(dA);
-  db = wave_sum(db);
+  dA = wave_sum2(dA);
+  db = wave_sum2(db);
   if (l == 0) {
     red[0][w] = dA;
     red[1][w] = db;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    part_dA[out] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
-    part_db[out] = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    part_dA[out] = (float)((red[0][0] + red[0][1]) + (red[0][2] + red[0][3]));
+    part_db[out] = (float)((red[1][0] + red[1][1]) + (red[1][2] + red[1][3]));
   }
 }
 
@@ -138,7 +180,7 @@ GradPlan grad_plan(const gdr_ssm_problem* p) {
 
 // Byte offsets in the workspace.
 struct GradLayout {
-  size_t state, grad, sdec, gdec, row, q, span, params, pB, pC, total;
+  size_t state, grad, sdec, gdec, row, q, far, own, mid_state, mid, span, params, pB, pC, total;
 };
 GradLayout layout(const gdr_ssm_problem* p, const GradPlan& g) {
   GradLayout o{};
@@ -159,6 +201,13 @@ GradLayout layout(const gdr_ssm_problem* p, const GradPlan& g) {
   }
   o.row = take(tokens * p->H * sizeof(float));
   o.q = take(tokens * p->H * sizeof(float));
+  o.far = take(tokens * p->H * sizeof(float));
+  o.own = take(tokens * p->H * sizeof(float));
+  if (g.cut.seg > 64 * kMid) {
+    const size_t edges = (tokens / (64 * kMid) + 1) * p->H;
+    o.mid_state = take(edges * p->K * p->V * sizeof(float));
+    o.mid = take(edges * 8 * sizeof(float));
+  }
   o.span = take(ids * sizeof(float));
   o.params = take(3 * ids * sizeof(float));
   if (g.slots > 1) {
@@ -214,6 +263,13 @@ gdr_status launch_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* d
   }
   a.row = f32(o.row);
   a.q = f32(o.q);
+  a.far = f32(o.far);
+  a.own = f32(o.own);
+  if (g.cut.seg > 64 * kMid) {
+    a.mid_state = f32(o.mid_state);
+    a.mid = f32(o.mid);
+  }
+  a.mid_parts = p->V == 128 && g.heads == 1 ? 8 : 4;
   a.span = f32(o.span);
   a.part_dD = params + 2 * ids;
   a.slots = g.slots;
