@@ -515,31 +515,6 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
         ga.row[o] = v + far;
       }
     }
-    // every kMid chunks: the state of the forward walk meets that of the backward one
-    const int edge = REV ? nch - 1 - c : c + 1;
-    if (ga.mid_state && active && edge % kMid == 0 && edge > 0 && edge < nch) {
-      const int64_t at = (sg.t0 + 64ll * edge) / (64 * kMid) * a.H + h;
-      float* ms = ga.mid_state + at * KV;
-      float d = 0.f;
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          f32x4* m = reinterpret_cast<f32x4*>(ms + (((ct0 + pt) * NT + nt) * 64 + l) * 4);
-          if (REV) {
-            const f32x4 v = *m;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d += S[pt][nt][e] * v[e];
-          } else {
-            *m = S[pt][nt];
-          }
-        }
-      if (REV) {
-        d = wave_sum(d);
-        if (l == 0) ga.mid[at * 8 + w % WPH] = d;
-      }
-    }
-
     {
       const int row_bytes = a.G * K * (ga.slots == 1 ? (int)sizeof(T) : 4);
       const int64_t o = (t * a.G + grp) * K;
@@ -566,6 +541,31 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
       }
     }
     __syncthreads();  // D: the tiles may be overwritten
+    // every kMid chunks the forward walk's state meets the backward one's (here,
+    // where the chunk's other registers are free)
+    const int edge = REV ? nch - 1 - c : c + 1;
+    if (ga.mid_state && active && edge % kMid == 0 && edge > 0 && edge < nch) {
+      const int64_t at = (sg.t0 + 64ll * edge) / (64 * kMid) * a.H + h;
+      const auto rs = buf_rsrc(ga.mid_state + at * KV + ct0 * (16 * K), 64ll * PT * K);
+      float d = 0.f;
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int off = 16 * lf + 1024 * (pt * NT + nt);
+          if (REV) {
+            const f32x4 v = __builtin_bit_cast(f32x4, buf_load16(rs, off));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d += S[pt][nt][e] * v[e];
+          } else {
+            buf_store16(rs, off, __builtin_bit_cast(uint4, S[pt][nt]));
+          }
+        }
+      if (REV) {
+        d = wave_sum(d);
+        if (l == 0) ga.mid[at * 8 + w % WPH] = d;
+      }
+    }
   }
 
   // what spans the segment's end; the gradient of h0; dy . x
