@@ -106,6 +106,8 @@ struct GradSmem {
   T R[kPublished<K, V, HPW> * V * K];  // state columns [V][K]
   T W[64 * 64];
   T GL[REV ? HPW : 0][64 * 64];  // the decayed scores
+  // fp16: what undoes the scales of W's and GL's tiles
+  float wd[__is_same(T, __bf16) ? 0 : 16], gd[REV && !__is_same(T, __bf16) ? HPW : 0][16];
   float gam[HPW][64];  // in powers of two
   float eg[HPW][64], es[HPW][64], wt[HPW][64], dts[HPW][64], decay[HPW];
   float pe[HPW][4][64], pa[NW][64], po[REV ? HPW : 0][64];
@@ -339,7 +341,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
           const f32x4 gam_b = *reinterpret_cast<const f32x4*>(&s.gam[hh][ib]);
           const f32x4 dt_b = *reinterpret_cast<const f32x4*>(&s.dts[hh][ib]);
           float sum = 0.f, own = 0.f;  // own: the pair of a token with itself
-          x4 z;
+          f32x4 gl;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool in = REV ? ib + e >= ia : ib + e <= ia, self = ib + e == ia;
@@ -349,7 +351,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
             const float fd = f * (REV ? dt_a : dt_b[e]);
             wsum[e] += fd;
             if (REV) {
-              z[e] = from_f<T>(gt[e] * lm);
+              gl[e] = gt[e] * lm;
               const float one = gt[e] * f;
               sum += self ? 0.f : one;
               own += self ? one : 0.f;
@@ -364,12 +366,25 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
             own = sum4g(own);
             if (g4 == 0) s.po[REV ? hh : 0][ia] = own;
           }
-          if (REV) *row4(s.GL[hh], om, 16 * ab, 16 * bb) = z;
+          if (REV) {
+            x4* to = row4(s.GL[hh], om, 16 * ab, 16 * bb);
+            if constexpr (kScaled) {
+              float back;
+              *to = tile_f16(gl, back);
+              if (l == 0) s.gd[hh][4 * ab + bb] = back;
+            } else {
+              *to = round4<T>(gl);
+            }
+          }
         }
-        x4 z;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = from_f<T>(wsum[e]);
-        *row4(s.W, om, 16 * ab, 16 * bb) = z;
+        x4* to = row4(s.W, om, 16 * ab, 16 * bb);
+        if constexpr (kScaled) {
+          float back;
+          *to = tile_f16(wsum, back);
+          if (l == 0) s.wd[4 * ab + bb] = back;
+        } else {
+          *to = round4<T>(wsum);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -474,7 +489,14 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
         for (int sb = r >> 1; sb < 2; ++sb) {
           const x8 f = split_frag(s.GL[hw], om, 16 * r, 32 * sb);
 #pragma unroll
-          for (int pt = 0; pt < PT; ++pt) u[pt][r] = mfma16(xf[sb][pt], f, u[pt][r]);
+          for (int pt = 0; pt < PT; ++pt) {
+            if constexpr (kScaled) {
+              if (2 * sb >= r) u[pt][r] = mfma_tile<0>(xf[sb][pt], f, s.gd[hw][4 * r + 2 * sb], u[pt][r]);
+              u[pt][r] = mfma_tile<1>(xf[sb][pt], f, s.gd[hw][4 * r + 2 * sb + 1], u[pt][r]);
+            } else {
+              u[pt][r] = mfma16(xf[sb][pt], f, u[pt][r]);
+            }
+          }
         }
         const int row = 16 * r + col;
         const float di = s.dts[hw][row];
@@ -528,8 +550,15 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
         const int idx = wf * TPW + i, nt = idx >> 2, ab = idx & 3;
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
-          if (REV ? sb >= (ab >> 1) : sb <= (ab >> 1))
-            acc[i] = mfma16(tr_frag(Q, ok, 32 * sb, 16 * nt), split_frag(s.W, om, 16 * ab, 32 * sb), acc[i]);
+          if (REV ? sb >= (ab >> 1) : sb <= (ab >> 1)) {
+            const x8 qf = tr_frag(Q, ok, 32 * sb, 16 * nt), wt = split_frag(s.W, om, 16 * ab, 32 * sb);
+            if constexpr (kScaled) {  // of the two tiles one may be beyond the diagonal
+              if (!REV || 2 * sb >= ab) acc[i] = mfma_tile<0>(qf, wt, s.wd[4 * ab + 2 * sb], acc[i]);
+              if (REV || 2 * sb + 1 <= ab) acc[i] = mfma_tile<1>(qf, wt, s.wd[4 * ab + 2 * sb + 1], acc[i]);
+            } else {
+              acc[i] = mfma16(qf, wt, acc[i]);
+            }
+          }
         const int off = (16 * ab + col) * row_bytes, k0 = 16 * nt + 4 * g4;
         if (ga.slots == 1) {
           const x4 z{from_f<T>(acc[i][0]), from_f<T>(acc[i][1]), from_f<T>(acc[i][2]),

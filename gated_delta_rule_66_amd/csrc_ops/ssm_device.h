@@ -262,6 +262,55 @@ __device__ __forceinline__ int state_exponent(const f32x4* S) {
   return m > 0.f && m < __builtin_inff() ? min(max(e, -100), 100) : 100;
 }
 
+// The largest of the wave's v >= 0, in a scalar.
+__device__ __forceinline__ float wave_largest(float v) {
+  v = fmaxf(v, dpp_zero<0x111>(v));
+  v = fmaxf(v, dpp_zero<0x112>(v));
+  v = fmaxf(v, dpp_zero<0x114>(v));
+  v = fmaxf(v, dpp_zero<0x118>(v));
+  v = fmaxf(v, dpp_zero<0x142>(v));  // row 0's to row 1, 2's to 3; then both to row 3
+  v = fmaxf(v, dpp_zero<0x143>(v));
+  return lane_value(v, 63);
+}
+
+__device__ __forceinline__ float largest4(f32x4 v) {
+  return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+}
+
+// Decayed scores as fp16 operands.  A wave scales a tile of 16 x 16 of them (the
+// forward: the tiles of a column block) by a power of two such that the largest
+// lies in [2^13, 2^14): whatever step sizes and gradients make of the scores,
+// none overflows, and those down to 2^-27 of the largest keep the type's 11
+// bits; `down` undoes the scale in the fp32 sums.  Tiles with scales of their
+// own take products of 16 tokens instead of 32 (8 x 4096 tokens of 64 heads in
+// 8 groups, K = 128, V = 64: the outputs 397 -> 444 us, the gradient's walks 581
+// and 666 -> 594 and 710).
+__device__ __forceinline__ float tile_scale(float m, float& down) {
+  m = wave_largest(m);
+  const int e = 14 - __builtin_amdgcn_frexp_expf(m);
+  const int s = m > 0.f && m < __builtin_inff() ? min(max(e, -120), 120) : 0;
+  down = ldexpf(1.f, -s);
+  return ldexpf(1.f, s);
+}
+__device__ __forceinline__ f16x4 tile_f16(f32x4 v, float& down) {
+  const float up = tile_scale(largest4(v), down);
+  return f16x4{from_f<_Float16>(v[0] * up), from_f<_Float16>(v[1] * up), from_f<_Float16>(v[2] * up),
+               from_f<_Float16>(v[3] * up)};
+}
+
+template <typename T>
+__device__ __forceinline__ typename VT<T>::x4 round4(f32x4 v) {
+  return typename VT<T>::x4{from_f<T>(v[0]), from_f<T>(v[1]), from_f<T>(v[2]), from_f<T>(v[3])};
+}
+
+// c + a b down over one 16-token half (0 or 1) of two operands in split k order
+template <int HALF>
+__device__ __forceinline__ f32x4 mfma_tile(f16x8 a, f16x8 b, float down, f32x4 c) {
+  const f16x4 x{a[4 * HALF], a[4 * HALF + 1], a[4 * HALF + 2], a[4 * HALF + 3]};
+  const f16x4 y{b[4 * HALF], b[4 * HALF + 1], b[4 * HALF + 2], b[4 * HALF + 3]};
+  return c + __builtin_amdgcn_mfma_f32_16x16x16f16(x, y, zero4(), 0, 0, 0) * down;
+}
+
 // The weighted values of block tb of a chunk: column operand xf (split k order)
 // times its tokens' weights.
 template <typename T>

@@ -30,6 +30,7 @@ struct WalkSmem {
   T B[64 * K];
   T X[64 * HPW * V];
   T M[OUT ? HPW : 0][64 * 64];
+  float md[OUT && !__is_same(T, __bf16) ? HPW : 0][4];  // fp16: what undoes the scales of M's column blocks
   float gam[HPW][2][64];  // in powers of two
   float eg[HPW][2][64], wt[HPW][2][64], dts[HPW][2][64], decay[HPW][2];
 };
@@ -208,19 +209,29 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
         if (hh >= nh) continue;
         const f32x4 gi = *reinterpret_cast<const f32x4*>(&s.gam[hh][b][i]);
         const f32x4 di = *reinterpret_cast<const f32x4*>(&s.dts[hh][b][i]);
+        f32x4 o[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
+          if (kScaled) o[r] = zero4();
           if (r >= cb) {
             const int row = 16 * r + col;
             const float gr = s.gam[hh][b][row];
-            x4 o;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float v = sc[r][e] * exp2_fast(gr - gi[e]) * di[e];
-              o[e] = from_f<T>(row >= i + e ? v : 0.f);
+              o[r][e] = row >= i + e ? v : 0.f;
             }
-            *row4(s.M[hh], om, 16 * r, 16 * cb) = o;
+            if (!kScaled) *row4(s.M[hh], om, 16 * r, 16 * cb) = round4<T>(o[r]);
           }
+        }
+        if constexpr (kScaled) {
+          float back;
+          const float scale = tile_scale(
+              fmaxf(fmaxf(largest4(o[0]), largest4(o[1])), fmaxf(largest4(o[2]), largest4(o[3]))), back);
+          if (l == 0) s.md[hh][cb] = back;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (r >= cb) *row4(s.M[hh], om, 16 * r, 16 * cb) = round4<T>(o[r] * scale);
         }
       }
 #pragma unroll
@@ -247,7 +258,15 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
           for (int r = 2 * tb; r < 4; ++r) {
             const x8 mf = split_frag(s.M[hf], om, 16 * r, 32 * tb);
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) acc[pt][r] = mfma16(xf[tb][pt], mf, acc[pt][r]);
+            for (int pt = 0; pt < PT; ++pt) {
+              if constexpr (kScaled) {
+                acc[pt][r] = mfma_tile<0>(xf[tb][pt], mf, s.md[hf][2 * tb], acc[pt][r]);
+                if (2 * tb + 1 <= r)
+                  acc[pt][r] = mfma_tile<1>(xf[tb][pt], mf, s.md[hf][2 * tb + 1], acc[pt][r]);
+              } else {
+                acc[pt][r] = mfma16(xf[tb][pt], mf, acc[pt][r]);
+              }
+            }
           }
         __builtin_amdgcn_sched_barrier(0);
       }

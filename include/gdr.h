@@ -466,9 +466,9 @@ gdr_status gdr_conv1d_update(const gdr_conv_problem* p, const void* x, void* sta
  *   states         [N, H, K, V]   fp32, 16-byte aligned
  * K and V are 64 or 128.  Products run on 16-bit operands with fp32 sums; the
  * states and their gradients are as exact as fp32 inputs would make them, the
- * products inside a chunk (64 tokens) round their decayed scores to in_dtype:
- * with fp16 their magnitude |C_t . B_s| dt_s, and the state's, must stay below
- * 65504.  A chunk's decays are formed from prefix sums of the log decays in
+ * products inside a chunk (64 tokens) round their decayed scores to in_dtype,
+ * with fp16 after scaling them to its range: only inputs and results have to
+ * fit the type.  A chunk's decays are formed from prefix sums of the log decays in
  * fp32: each is within 2^-23 of the largest |sum| of its chunk, relatively.
  * Step sizes may be negative without softplus (the state then grows). */
 typedef struct {
