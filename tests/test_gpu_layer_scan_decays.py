@@ -146,3 +146,26 @@ def test_long_uncut_segments(rate, bias, B, T, H, G, K, V):
                                        t["dt_bias"], True, None)
     heads = [0, 1, H // 2, H // 2 + 1, H - 2, H - 1]
     check(got, reference(t, True, heads), t, heads)
+
+
+# sequences in one run of up to 33 chunks each, then sequences cut into segments
+# of more than 512 tokens, so that kept states and segment ends take turns
+@pytest.mark.parametrize("lens,H,G,K,V", [([700, 1, 1300, 64, 0, 2100, 1030], 128, 64, 64, 64),
+                                          ([9000, 300, 7084], 64, 16, 64, 64),
+                                          ([0, 513, 1025, 512, 1024], 256, 128, 128, 128)])
+@pytest.mark.parametrize("rate,bias", [(16, 0), (1, -4)])
+def test_long_packed_sequences(lens, H, G, K, V, rate, bias):
+    gen = torch.Generator(device="cuda").manual_seed(rate + H)
+    r = lambda *s, dt=BF: torch.randn(*s, generator=gen, device="cuda").to(dt)  # noqa: E731
+    T, n = sum(lens), len(lens)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    t = dict(x=r(1, T, H, V), B=r(1, T, G, K), C=r(1, T, G, K), dt=r(1, T, H, dt=F32), D=None,
+             cu=cu.cuda(), state=r(n, H, K, V, dt=F32), A_log=torch.full((H,), float(rate), device="cuda").log(),
+             dt_bias=torch.full((H,), float(bias), device="cuda"), dy=r(1, T, H, V),
+             dlast=r(n, H, K, V, dt=F32))
+    heads = [0, 1, H // 2, H // 2 + 1, H - 2, H - 1]
+    want = reference(t, True, heads)
+    got = run(t, True)
+    check(got, want, t, heads)
+    again = run(t, True, recompute_states=True)     # the same cut, the states formed anew
+    assert torch.equal(got[1], again[1]) and torch.equal(got[2], again[2])
