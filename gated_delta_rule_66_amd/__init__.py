@@ -12,7 +12,8 @@ states ``[N, Hv, K, V]`` (``[N, Hv, V, K]`` with ``state_v_first``), fp32.
 K = V = 128; bf16 or fp16 inputs; Hv a multiple of Hq.
 
 The operators around the recurrence in a layer (``_layer_ops``): the short
-causal convolution and the RMS norm with the residual's addition.
+causal convolution, the selective state space scan and the RMS norm with the
+residual's addition.
 """
 from __future__ import annotations
 

@@ -262,7 +262,8 @@ def causal_conv1d_update(x, conv_state, weight, bias=None, activation="silu"):
     """One or a few tokens per sequence on a cached state (decode): returns y,
     shaped like x (``[B, D]`` or ``[B, T, D]``), and updates ``conv_state``
     ``[B, W-1, D]`` in place.  No autograd: a graph that saved ``conv_state``
-    raises in its backward, as after any in-place operation."""
+    raises in its backward, as after any in-place operation, and a
+    ``conv_state`` that requires grad is refused while grad mode is on."""
     squeeze = x.dim() == 2
     x3 = x.unsqueeze(1) if squeeze else x
     if not conv_state.is_contiguous():
@@ -426,7 +427,8 @@ def fused_recurrent_selective_scan(x, dt, A_log, B, C, D=None, dt_bias=None, dt_
     ``(y, final_state)`` of :func:`chunk_selective_scan`, the state read once
     and written once.  With ``inplace_final_state`` the fp32 ``initial_state``
     is updated in place and returned (a graph that saved it raises in its
-    backward, as after any in-place operation).  No autograd."""
+    backward, as after any in-place operation, and one that requires grad is
+    refused while grad mode is on).  No autograd."""
     if inplace_final_state and (initial_state is None or not initial_state.is_contiguous()
                                 or initial_state.data_ptr() % 16):
         raise GdrError(10, "inplace_final_state needs a contiguous, 16-byte aligned initial_state")

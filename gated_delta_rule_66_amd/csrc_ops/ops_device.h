@@ -71,7 +71,7 @@ __device__ __forceinline__ void load_params(const void* p, int64_t i, int dtype,
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + __expf(-z)); }
 
-// Sum and maximum over a whole wave (every lane ends with the same bits).
+// Sum over a whole wave (every lane ends with the same bits).
 __device__ __forceinline__ float wave_sum(float v) { return sum4g(sum16(v)); }
 
 }  // namespace gdr

@@ -155,9 +155,9 @@ constexpr int block_of() {
 }
 
 // The forward.  RES: the residual's type, void without one.  Memory bounds it:
-// 16,384 rows of 4096 bf16 columns with a residual to e4m3 take 87 us for 472
-// MB (5.4 TB/s), 8192 of them to bf16 46 us for 268 MB (5.8); eight rows take 5
-// us, the latency of a load and two reductions.
+// 16,384 rows of 4096 bf16 columns with a residual to e4m3 take 89 us for 472
+// MB (5.3 TB/s; to int8 the same), 8192 of them to bf16 46 us for 268 MB (5.8);
+// eight rows take 5 us, the latency of a load and two reductions.
 template <typename T, typename RES, bool QUANT, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
   constexpr bool kRes = !std::is_void<RES>::value;
@@ -280,8 +280,11 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
 //   dw = sum_rows dy u.
 // A block walks rows blockIdx.x, + blocks, ... with dw in registers and
 // leaves its sum in `part`; norm_reduce_kernel adds the blocks in order.
-// Memory bounds it: 8192 rows of 4096 bf16 columns take 55 us for 285 MB (5.2
-// TB/s).
+// Memory bounds it up to 8192 columns: 8192 rows of 4096 bf16 columns take 55
+// us for 285 MB (5.2 TB/s).  Beyond, registers do, since five arrays of the row
+// are held in them: 32 MB of columns with a bf16 residual take 84 us at 16,384
+// columns (3.2 TB/s; up to 45 spilled registers at one wave per SIMD), 351 at
+// 32,768 (0.8; 219 to 312) and 870 at 65,536 (0.3; 620 to 747).
 template <typename T, typename RES, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void norm_bwd_kernel(NormArgs a) {
   constexpr bool kRes = !std::is_void<RES>::value;
@@ -389,7 +392,9 @@ __global__ __launch_bounds__(256) void norm_reduce_kernel(const float* part, int
 // rows would need no barriers but holds more of a row per thread: 16384 rows
 // of 4096 columns to e4m3 take 125 us with one wave a row and 88 us with 256
 // threads, 8192 rows with a residual 54 and 47 us.  Beyond 16384 columns 256
-// threads would hold more than 64 elements each, and spill.
+// threads would hold more than 64 elements each of a row; with 1024, which leave
+// a thread 128 registers, the forward spills at most 23 (8-bit outputs and fp32
+// beyond 32,768 columns), the gradient many (see there).
 template <typename F>
 void by_width(int D, F f) {
   const int nv = (D + 7) / 8;

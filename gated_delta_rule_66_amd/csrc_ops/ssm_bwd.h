@@ -45,16 +45,20 @@
 // in LDS, where registers allow (K = 64, V = 128, two heads, backward: 90
 // against 93 us; K = 128, V = 64: 82 against 86), and in the backward walk
 // with K = V = 128 after dx is stored.  With 8192 tokens, 32 heads in 16
-// groups, K = V = 128 the walks take 116 and 160 us; bound by LDS reads and by
-// latency at two waves per SIMD.
+// groups, K = V = 128 the walks take 117 and 157 us (fp16 132 and 197): matrix
+// units busy 19 % and LDS 30 % of the time, 36 to 56 bytes of spilled registers
+// a lane (fp16 36 and 136), two waves per SIMD that wait for each other at three
+// or four barriers a chunk.
 #pragma once
 
 #include "ssm_device.h"
 
 namespace gdr {
 
-// Chunks between the states that meet their gradients inside a segment: a
-// multiple of 512 tokens costs the walks 64 to 128 bytes per token and head.
+// Chunks between the states that meet their gradients inside a segment.  Each
+// costs 4 K V bytes written and read, 32 to 128 a token (8 x 4096 uncut tokens
+// of 64 heads, K = 128, V = 64: the walks 523 and 612 us without, 555 and 656
+// with).
 constexpr int kMid = 8;
 
 struct SsmGradArgs {

@@ -32,7 +32,8 @@ __device__ __forceinline__ double wave_sum2(double v) {
 // dg from the walks' sums (ssm_bwd.h), the raw step sizes' gradient and the
 // segment's shares of dA_log and ddt_bias.  One workgroup per (segment, head),
 // 16 chunks at a time from the end, four tokens per thread: sums inside a chunk
-// in fp32, the chain over the chunks and the shares in 64 bits.
+// in fp32, the chain over the chunks and the shares in 64 bits.  12 us for 8192
+// tokens of 32 heads: latency, and reads of dt one head apart.
 template <typename DT>
 __global__ __launch_bounds__(256) void ssm_dt_kernel(SsmGradArgs ga, DT* ddt, float* part_dA,
                                                      float* part_db) {

@@ -492,9 +492,11 @@ SsmArgs ssm_args(const gdr_ssm_problem* p, const SsmPlan& pl) {
 // least cost.  Workgroups run in rounds of `slots`; a round takes its
 // segments' chunks and about 1.5 chunks for the states at both ends, a last
 // round that fills a share f of the slots (0.45 + 0.55 f) of that (a CU's
-// workgroups share its units: one alone takes 3 us a chunk, three 7).  Cut,
-// every chunk's x and B are read once more for 0.4 of a chunk, and two
-// launches are added, worth about four chunks.
+// workgroups share its units.  Outputs, K = 128, V = 64, bf16: of one head one
+// workgroup alone takes 4.3 us a chunk, two 6.4, three 8.4; of two heads one
+// takes 6.2 and two 8.9; fp16 up to 1 more).  Cut, every chunk's x and B are read
+// once more for 0.4 of a chunk, and two launches are added, worth about four
+// chunks.
 SsmPlan ssm_plan(const gdr_ssm_problem* p, int64_t per_seg, int64_t slots) {
   int64_t longest = 0, tokens = 0;
   const int seqs = p->cu_seqlens_host ? p->N : 1;

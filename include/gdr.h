@@ -401,8 +401,9 @@ int gdr_profile_read(char* names, size_t name_stride, double* total_ms, int* lau
  * may run at once on different streams if they share no output or workspace.
  * Where a problem states a token stride, consecutive tokens' rows of that
  * input lie so many elements apart (a slice of a wider tensor); every other
- * tensor is contiguous.  Outputs overlap no input unless a function says so.  These operators ask only for the alignment of one
- * element unless a function says otherwise. */
+ * tensor is contiguous.  Outputs overlap no input unless a function says so.
+ * These operators ask only for the alignment of one element unless a function
+ * says otherwise. */
 
 /* ---- short causal depthwise convolution ----
  * Per channel d and token t of a sequence, with x[t'] for t' before the
@@ -468,9 +469,16 @@ gdr_status gdr_conv1d_update(const gdr_conv_problem* p, const void* x, void* sta
  * states and their gradients are as exact as fp32 inputs would make them, the
  * products inside a chunk (64 tokens) round their decayed scores to in_dtype,
  * with fp16 after scaling them to its range: only inputs and results have to
- * fit the type.  A chunk's decays are formed from prefix sums of the log decays in
- * fp32: each is within 2^-23 of the largest |sum| of its chunk, relatively.
- * Step sizes may be negative without softplus (the state then grows). */
+ * fit the type.  A chunk's decays are formed from prefix sums of the log
+ * decays in fp32.  A sum passes through up to 7 additions, is multiplied by
+ * log2(e), and a decay is the exponential of two sums' difference: with the
+ * roundings of step sizes and rates (a few 2^-24 of each term) a decay is
+ * within 2^-19 of the largest |sum| of its chunk, relatively, if the log
+ * decays have one sign, and within twice that otherwise.
+ * Step sizes may be negative without softplus (the state then grows).  An
+ * infinity or NaN in x may reach every output of its sequence from the start
+ * of its chunk on, other inputs' from their own token on; other sequences
+ * stay as they are. */
 typedef struct {
   int32_t B, T, H, G, K, V;
   int32_t N;                      /* sequences: B, or len(cu_seqlens) - 1 */
@@ -507,7 +515,12 @@ gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
  *   out: dx, ddt (with respect to the raw step sizes), dA_log, dB, dC; dD,
  *        ddt_bias, dinitial_state (each nullable = not written, and only with
  *        its input).  Parameters' gradients are in p_dtype, sums over all
- *        tokens in a fixed order. */
+ *        tokens in a fixed order.
+ * dx, dB and dC round one operand of their products in a chunk to in_dtype, as
+ * y does.  ddt, dA_log and ddt_bias come from fp32 sums, of which at most 512
+ * tokens' rounding errors add up: dA_log is within 2^-10 of the root of the
+ * summed squares of its terms g_t dg_t.  (The workspace holds fp32 states every
+ * 512 tokens of segments longer than that.) */
 size_t gdr_ssm_bwd_workspace_size(const gdr_ssm_problem* p);
 gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, const void* A_log,
                        const void* B, const void* C, const void* D, const void* dt_bias,
