@@ -46,7 +46,7 @@
 // against 93 us; K = 128, V = 64: 82 against 86), and in the backward walk
 // with K = V = 128 after dx is stored.  With 8192 tokens, 32 heads in 16
 // groups, K = V = 128 the walks take 117 and 157 us (fp16 132 and 197): matrix
-// units busy 19 % and LDS 30 % of the time, 36 to 56 bytes of spilled registers
+// units busy 15 % and LDS 22 to 25 % of the time, 36 to 56 bytes of spilled registers
 // a lane (fp16 36 and 136), two waves per SIMD that wait for each other at three
 // or four barriers a chunk.
 #pragma once

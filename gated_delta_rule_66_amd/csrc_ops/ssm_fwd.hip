@@ -47,8 +47,10 @@ struct WalkSmem {
 // 384 with 32), 16 for states, where twice the waves hide more latency
 // (136 us with 32, 133 with 16).  Per chunk,
 // the tiles of the next one are in registers (in flight), those of this one
-// in LDS, swizzled so that no operand read has bank conflicts; the last waves,
-// which have the fewest score tiles, form the next chunk's gates.
+// in LDS, swizzled so that operands are read as fast as linear rows (LDS is
+// active 29 % of the outputs' time, a third of that for conflicts, and 20 % of
+// the states', without any); the last waves, which have the fewest score tiles,
+// form the next chunk's gates.
 enum { kOut, kState, kGrad };
 template <typename T, int K, int V, int HPW, int PT, int MODE>
 __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 ? 3 : 2) void ssm_walk_kernel(SsmArgs a) {
