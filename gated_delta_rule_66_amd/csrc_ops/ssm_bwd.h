@@ -110,11 +110,13 @@ struct GradSmem {
   T R[kPublished<K, V, HPW> * V * K];  // state columns [V][K]
   T W[64 * 64];
   T GL[REV ? HPW : 0][64 * 64];  // the decayed scores
+  T Wd[REV ? 0 : 64 * 16];  // the rest of W's diagonal tiles (backward: in GL)
+  float od[REV ? HPW : 0][64];  // the rest of GL's diagonal
   // fp16: what undoes the scales of W's and GL's tiles
   float wd[__is_same(T, __bf16) ? 0 : 16], gd[REV && !__is_same(T, __bf16) ? HPW : 0][16];
   float gam[HPW][64];  // in powers of two
-  float eg[HPW][64], es[HPW][64], wt[HPW][64], dts[HPW][64], decay[HPW];
-  float pe[HPW][4][64], pa[NW][64], po[REV ? HPW : 0][64];
+  float eg[HPW][64], es[REV ? HPW : 0][64], wt[HPW][64], dts[HPW][64], decay[HPW];
+  float pe[HPW][160], pa[NW][64], po[REV ? HPW : 0][64];  // pe: sum_at
   int ex[NW];
   float fin[HPW][NW];
 };
@@ -130,6 +132,13 @@ __device__ __forceinline__ int tri_tile(int w, int s) {
   const int i = NW == 4 ? w + 4 * s : s == 0 ? w + 2 : w;
   const bool in = NW == 4 ? i < 10 : s == 0 || w < 2;
   return in ? (int)(all >> (4 * i)) & 15 : -1;
+}
+
+// Token a's sum over the tokens of block bb: on and below the diagonal of a
+// chunk's 64 x 4 such sums (backward: above it).
+template <bool REV>
+__device__ __forceinline__ int sum_at(int bb, int a) {
+  return REV ? 8 * bb * (bb + 1) + a : 56 * bb - 8 * bb * bb + a;
 }
 
 // The two walks are mirror images: with (P, Q, p, q) = (C, B, dY, X) forward
@@ -242,7 +251,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
     const float gam = wave_prefix(g), es = __expf(wave_suffix_excl(g));
     s.gam[gh][l] = gam * kLog2e;
     s.eg[gh][l] = __expf(gam);
-    s.es[gh][l] = es;
+    if (REV) s.es[REV ? gh : 0][l] = es;
     s.wt[gh][l] = step * es;
     s.dts[gh][l] = step;
     if (l == 0) s.decay[gh] = __expf(lane_value(gam, 63));
@@ -257,13 +266,6 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
   Sw<K> ok;
   Sw<V> ov;
   Sw<64> om;
-  // the tiles beyond the diagonal that the products read stay zero: (a, b) =
-  // (0, 1) and (2, 3) forward, (1, 0) and (3, 2) backward
-  for (int i = threadIdx.x; i < 128 * (REV ? 1 + HPW : 1); i += NTH) {
-    const int k = i & 127, z0 = (k >> 6) * 32, ar = z0 + (REV ? 16 : 0) + ((k >> 2) & 15),
-              bc = z0 + (REV ? 0 : 16) + 4 * (k & 3);
-    *reinterpret_cast<x4*>((i < 128 ? s.W : s.GL[(i >> 7) - 1]) + sw_off<64>(ar, bc)) = x4{};
-  }
   __syncthreads();
   for (int c = 0; c < nch; ++c) {
     const int64_t t = token(c);
@@ -320,6 +322,15 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
     __syncthreads();  // A: tiles, gates and the first state columns are in LDS
     if (kEarly && c + 1 < nch) request(c + 1);
 
+    // W is a pair of operands: the second one's tiles lie across the diagonal
+    // from the first's, those on it in tiles that nothing else uses (backward:
+    // on GL's empty side)
+    auto rest_of_w = [&](int ab, int bb) -> x4* {
+      if (ab != bb) return row4(s.W, om, 16 * bb, 16 * ab);
+      if (REV) return row4(s.GL[0], om, ab < 3 ? 48 : 32, ab < 3 ? 16 * ab : 0);
+      return reinterpret_cast<x4*>(s.Wd + 16 * (16 * ab + col) + 4 * g4);
+    };
+
     // scores (transposed: rows b, columns a), their sums over b, and W summed
     // over the heads
 #pragma unroll
@@ -365,30 +376,44 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
             }
           }
           sum = sum4g(sum);
-          if (g4 == 0) s.pe[hh][bb][ia] = sum;
+          if (g4 == 0) s.pe[hh][sum_at<REV>(bb, ia)] = sum;
           if (REV && ab == bb) {
             own = sum4g(own);
             if (g4 == 0) s.po[REV ? hh : 0][ia] = own;
           }
           if (REV) {
-            x4* to = row4(s.GL[hh], om, 16 * ab, 16 * bb);
+            float back = 1.f;
+            x4 z;
             if constexpr (kScaled) {
-              float back;
-              *to = tile_f16(gl, back);
+              z = tile_f16(gl, back);
               if (l == 0) s.gd[hh][4 * ab + bb] = back;
             } else {
-              *to = round4<T>(gl);
+              z = round4<T>(gl);
+            }
+            *row4(s.GL[hh], om, 16 * ab, 16 * bb) = z;
+            if (ab == bb && g4 == col >> 2) {  // what rounding took from the diagonal
+              float d = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d += ib + e == ia ? gl[e] - to_f(z[e]) * back : 0.f;
+              s.od[REV ? hh : 0][ia] = d;
             }
           }
         }
-        x4* to = row4(s.W, om, 16 * ab, 16 * bb);
         if constexpr (kScaled) {
           float back;
-          *to = tile_f16(wsum, back);
+          wsum *= tile_scale(largest4(wsum), back);
           if (l == 0) s.wd[4 * ab + bb] = back;
-        } else {
-          *to = round4<T>(wsum);
         }
+        x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float t = wsum[e];
+          asm("" : "+v"(t));  // one fp32 number (as in split8)
+          hi[e] = from_f<T>(t);
+          lo[e] = from_f<T>(t - to_f(hi[e]));
+        }
+        *row4(s.W, om, 16 * ab, 16 * bb) = hi;
+        *rest_of_w(ab, bb) = lo;
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -459,7 +484,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float sc = (REV ? s.es[hw] : s.eg[hw])[16 * r + col] * down;
+        const float sc = (REV ? s.es[REV ? hw : 0] : s.eg[hw])[16 * r + col] * down;
         float dot = 0.f;
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
@@ -498,18 +523,23 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
               if (2 * sb >= r) u[pt][r] = mfma_tile<0>(xf[sb][pt], f, s.gd[hw][4 * r + 2 * sb], u[pt][r]);
               u[pt][r] = mfma_tile<1>(xf[sb][pt], f, s.gd[hw][4 * r + 2 * sb + 1], u[pt][r]);
             } else {
-              u[pt][r] = mfma16(xf[sb][pt], f, u[pt][r]);
+              if (r % 2 == 0) {
+                u[pt][r] = mfma16(xf[sb][pt], f, u[pt][r]);
+              } else {
+                if (2 * sb >= r) u[pt][r] = mfma_half(half_of<0>(xf[sb][pt]), half_of<0>(f), u[pt][r]);
+                u[pt][r] = mfma_half(half_of<1>(xf[sb][pt]), half_of<1>(f), u[pt][r]);
+              }
             }
           }
         }
         const int row = 16 * r + col;
-        const float di = s.dts[hw][row];
+        const float di = s.dts[hw][row], dd = skip + di * s.od[hw][row];
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
           const x4 yv = *row4(s.Y[hr], ov, 16 * r, v0 + 16 * pt);
           x4 z;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = from_f<T>(di * u[pt][r][e] + skip * to_f(yv[e]));
+          for (int e = 0; e < 4; ++e) z[e] = from_f<T>(di * u[pt][r][e] + dd * to_f(yv[e]));
           buf_store8(rs, row * yb + (v0 + 16 * pt + 4 * g4) * (int)sizeof(T),
                      __builtin_bit_cast(u32x2, z));
         }
@@ -529,7 +559,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
       float v = 0.f, far = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (REV ? i >= blk : i <= blk) v += s.pe[w][i][l];
+        if (REV ? i >= blk : i <= blk) v += s.pe[w][sum_at<REV>(i, l)];
 #pragma unroll
       for (int i = 0; i < WPH; ++i) far += s.pa[w * WPH + i][l];
       const int64_t o = (int64_t)(head0 + w) * ga.tokens + t + l;
@@ -556,11 +586,18 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
         for (int sb = 0; sb < 2; ++sb)
           if (REV ? sb >= (ab >> 1) : sb <= (ab >> 1)) {
             const x8 qf = tr_frag(Q, ok, 32 * sb, 16 * nt), wt = split_frag(s.W, om, 16 * ab, 32 * sb);
-            if constexpr (kScaled) {  // of the two tiles one may be beyond the diagonal
-              if (!REV || 2 * sb >= ab) acc[i] = mfma_tile<0>(qf, wt, s.wd[4 * ab + 2 * sb], acc[i]);
-              if (REV || 2 * sb + 1 <= ab) acc[i] = mfma_tile<1>(qf, wt, s.wd[4 * ab + 2 * sb + 1], acc[i]);
-            } else {
-              acc[i] = mfma16(qf, wt, acc[i]);
+            // of the two tiles one may be beyond the diagonal
+            if (!REV || 2 * sb >= ab) {
+              const f32x4 w2 = mfma_half(half_of<0>(qf), *rest_of_w(ab, 2 * sb),
+                                         mfma_half(half_of<0>(qf), half_of<0>(wt), kScaled ? zero4() : acc[i]));
+              if constexpr (kScaled) acc[i] += w2 * s.wd[4 * ab + 2 * sb];
+              else acc[i] = w2;
+            }
+            if (REV || 2 * sb + 1 <= ab) {
+              const f32x4 w2 = mfma_half(half_of<1>(qf), *rest_of_w(ab, 2 * sb + 1),
+                                         mfma_half(half_of<1>(qf), half_of<1>(wt), kScaled ? zero4() : acc[i]));
+              if constexpr (kScaled) acc[i] += w2 * s.wd[4 * ab + 2 * sb + 1];
+              else acc[i] = w2;
             }
           }
         const int off = (16 * ab + col) * row_bytes, k0 = 16 * nt + 4 * g4;

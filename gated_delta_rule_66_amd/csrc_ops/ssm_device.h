@@ -303,12 +303,29 @@ __device__ __forceinline__ typename VT<T>::x4 round4(f32x4 v) {
   return typename VT<T>::x4{from_f<T>(v[0]), from_f<T>(v[1]), from_f<T>(v[2]), from_f<T>(v[3])};
 }
 
-// c + a b down over one 16-token half (0 or 1) of two operands in split k order
+// Products over 16 tokens, of the halves (0 or 1) of operands in split k order.
+// They are not chained with products over 32 through one accumulator: measured,
+// a 32-token product right behind a 16-token one took two of its four sums
+// before they were written.
+__device__ __forceinline__ f32x4 mfma_half(f16x4 a, f16x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x16f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_half(bf16x4 a, bf16x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(i16x4, a),
+                                                   __builtin_bit_cast(i16x4, b), c, 0, 0, 0);
+}
+template <int HALF>
+__device__ __forceinline__ f16x4 half_of(f16x8 v) {
+  return f16x4{v[4 * HALF], v[4 * HALF + 1], v[4 * HALF + 2], v[4 * HALF + 3]};
+}
+template <int HALF>
+__device__ __forceinline__ bf16x4 half_of(bf16x8 v) {
+  return bf16x4{v[4 * HALF], v[4 * HALF + 1], v[4 * HALF + 2], v[4 * HALF + 3]};
+}
+// c + a b down over one half
 template <int HALF>
 __device__ __forceinline__ f32x4 mfma_tile(f16x8 a, f16x8 b, float down, f32x4 c) {
-  const f16x4 x{a[4 * HALF], a[4 * HALF + 1], a[4 * HALF + 2], a[4 * HALF + 3]};
-  const f16x4 y{b[4 * HALF], b[4 * HALF + 1], b[4 * HALF + 2], b[4 * HALF + 3]};
-  return c + __builtin_amdgcn_mfma_f32_16x16x16f16(x, y, zero4(), 0, 0, 0) * down;
+  return c + mfma_half(half_of<HALF>(a), half_of<HALF>(b), zero4()) * down;
 }
 
 // The weighted values of block tb of a chunk: column operand xf (split k order)

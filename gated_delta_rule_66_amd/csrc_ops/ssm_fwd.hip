@@ -31,6 +31,7 @@ struct WalkSmem {
   T X[64 * HPW * V];
   T M[OUT ? HPW : 0][64 * 64];
   float md[OUT && !__is_same(T, __bf16) ? HPW : 0][4];  // fp16: what undoes the scales of M's column blocks
+  float od[OUT ? HPW : 0][64];                          // what rounding took from M's diagonal
   float gam[HPW][2][64];  // in powers of two
   float eg[HPW][2][64], wt[HPW][2][64], dts[HPW][2][64], decay[HPW][2];
 };
@@ -206,6 +207,16 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
       // M = (C B^T) o L diag(dt), rounded to T as an operand; its tiles are
       // transposed, so that a lane holds four neighbours of a row
       const int i = 16 * cb + 4 * g4;
+      auto put_m = [&](int hh, int r, int c, f32x4 v, f32x4 scaled, float back) {
+        const x4 z = round4<T>(scaled);
+        *row4(s.M[hh], om, 16 * r, 16 * c) = z;
+        if (r == c && g4 == col >> 2) {
+          float d = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d += 4 * g4 + e == col ? v[e] - to_f(z[e]) * back : 0.f;
+          s.od[hh][16 * r + col] = d;
+        }
+      };
 #pragma unroll
       for (int hh = 0; hh < HPW; ++hh) {
         if (hh >= nh) continue;
@@ -223,7 +234,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
               const float v = sc[r][e] * exp2_fast(gr - gi[e]) * di[e];
               o[r][e] = row >= i + e ? v : 0.f;
             }
-            if (!kScaled) *row4(s.M[hh], om, 16 * r, 16 * cb) = round4<T>(o[r]);
+            if (!kScaled) put_m(hh, r, cb, o[r], o[r], 1.f);
           }
         }
         if constexpr (kScaled) {
@@ -233,7 +244,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
           if (l == 0) s.md[hh][cb] = back;
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (r >= cb) *row4(s.M[hh], om, 16 * r, 16 * cb) = round4<T>(o[r] * scale);
+            if (r >= cb) put_m(hh, r, cb, o[r], o[r] * scale, back);
         }
       }
 #pragma unroll
@@ -279,12 +290,13 @@ __global__ __launch_bounds__(4 * HPW * V / PT, MODE != kOut ? 4 : HPW * PT == 1 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int row = 16 * r + col;
+          const float dd = skip + s.od[hf][row];
 #pragma unroll
           for (int pt = 0; pt < PT; ++pt) {
             const x4 xv = *row4(s.X, ov, 16 * r, v0 + 16 * pt);
             x4 o;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = from_f<T>(acc[pt][r][e] + skip * to_f(xv[e]));
+            for (int e = 0; e < 4; ++e) o[e] = from_f<T>(acc[pt][r][e] + dd * to_f(xv[e]));
             buf_store8(rs, row * ys + (v0 + 16 * pt + 4 * g4) * (int)sizeof(T),
                        __builtin_bit_cast(u32x2, o));
           }
