@@ -31,8 +31,11 @@
 //                  dB    = diag(dt e^{gamma_end - gamma}) X P^T + W^T C
 // The scores' row and column sums are taken in fp32 before any rounding, and
 // the state's share in them uses its 16-bit pair (hi + lo): up to kMid chunks
-// of them are added up, so these must be near fp32.  The other products
-// round one operand (W, C B^T o L, S, P) to 16 bits, as their outputs are.
+// of them are added up, so these must be near fp32.  W, one rounding of which
+// would be shared by a row of dB or dC, is a pair of operands too (dB and dC of a
+// short sequence 2.4 times as far from the definition with one), and C B^T o L
+// gives dx its diagonal in fp32.  The other products
+// round one operand (C B^T o L, S, P) to 16 bits, as their outputs are.
 //
 // One workgroup walks a segment for up to HPW heads of one group at once: they
 // share the B and C tiles and C B^T, and their dB and dC are summed in
@@ -44,11 +47,13 @@
 // LDS as they are formed.  The next chunk is requested as soon as this one is
 // in LDS, where registers allow (K = 64, V = 128, two heads, backward: 90
 // against 93 us; K = 128, V = 64: 82 against 86), and in the backward walk
-// with K = V = 128 after dx is stored.  With 8192 tokens, 32 heads in 16
-// groups, K = V = 128 the walks take 117 and 157 us (fp16 132 and 197): matrix
-// units busy 15 % and LDS 22 to 25 % of the time, 36 to 56 bytes of spilled registers
-// a lane (fp16 36 and 136), two waves per SIMD that wait for each other at three
-// or four barriers a chunk.
+// with K = V = 128 after dx is stored; with two heads of that size the second
+// one's rows follow later, since all of them at once are spilled as they arrive
+// (bf16 132 -> 113 and 172 -> 165 us, fp16 140 -> 123 and 201 -> 198).  With 8192
+// tokens, 32 heads in 16 groups, K = V = 128 the walks take 113 and 165 us (fp16
+// 123 and 198): matrix units busy 16 to 18 % and LDS 25 % of the time, none and 84
+// bytes of spilled registers a lane (fp16 20 and 152), two waves per SIMD that wait
+// for each other at three or four barriers a chunk.
 #pragma once
 
 #include "ssm_device.h"
@@ -57,8 +62,7 @@ namespace gdr {
 
 // Chunks between the states that meet their gradients inside a segment.  Each
 // costs 4 K V bytes written and read, 32 to 128 a token (8 x 4096 uncut tokens
-// of 64 heads, K = 128, V = 64: the walks 523 and 612 us without, 555 and 656
-// with).
+// of 64 heads, K = 128, V = 64: 6 and 7 % of the walks' 555 and 671 us).
 constexpr int kMid = 8;
 
 struct SsmGradArgs {
@@ -154,6 +158,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
   constexpr int NW = HPW * V / (16 * PT), WPH = NW / HPW, NTH = 64 * NW, NT = K / 16;
   constexpr int TPW = 4 * NT / NW, MT = kMostTiles<NW>, RB = kPublished<K, V, HPW>;
   constexpr bool kScaled = !__is_same(T, __bf16), kEarly = !REV || K * V < 128 * 128;
+  constexpr bool kSplit = RB < HPW;
   static_assert(TPW >= 1 && (NW == 4 || NW == 8), "tiles are dealt to all waves");
   __shared__ __align__(16) GradSmem<T, K, V, HPW, NW, REV> s;
   const SsmArgs& a = ga.f;
@@ -229,14 +234,17 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
   const int nch = (int)((sg.t1 - sg.t0 + 63) / 64);
   auto token = [&](int c) { return sg.t0 + 64ll * (REV ? nch - 1 - c : c); };
   auto rows_of = [&](int64_t t) { return (int)min((int64_t)64, sg.t1 - t); };
-  auto request = [&](int c) {
+  // chunk c's heads h0 <= hh < h1, with the first one B and C
+  auto request = [&](int c, int h0, int h1) {
     const int64_t t = token(c);
     const int rows = rows_of(t);
-    rb.load(bg + t * a.bs, a.bs, rows);
-    rc.load(cg + t * a.cs, a.cs, rows);
+    if (h0 == 0) {
+      rb.load(bg + t * a.bs, a.bs, rows);
+      rc.load(cg + t * a.cs, a.cs, rows);
+    }
 #pragma unroll
     for (int hh = 0; hh < HPW; ++hh)
-      if (hh < nh) {
+      if (hh >= h0 && hh < h1 && hh < nh) {
         rx[hh].load(xg + t * a.xs + hh * V, a.xs, rows);
         ry[hh].load(yg + t * ys + hh * V, ys, rows);
       }
@@ -257,7 +265,7 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
     if (l == 0) s.decay[gh] = __expf(lane_value(gam, 63));
   };
   if (nch > 0) {
-    request(0);
+    request(0, 0, HPW);
     if (gates) request_dt(0);
   }
 
@@ -320,7 +328,8 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
       if (c + 1 < nch) request_dt(c + 1);
     }
     __syncthreads();  // A: tiles, gates and the first state columns are in LDS
-    if (kEarly && c + 1 < nch) request(c + 1);
+    const bool more = c + 1 < nch;
+    if (kEarly && more) request(c + 1, 0, kSplit ? 1 : HPW);
 
     // W is a pair of operands: the second one's tiles lie across the diagonal
     // from the first's, those on it in tiles that nothing else uses (backward:
@@ -546,10 +555,12 @@ __global__ __launch_bounds__(4 * HPW * V / PT, REV && K == 128 && HPW * V / PT =
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (!kEarly && c + 1 < nch) request(c + 1);
+    if (!kEarly && more) request(c + 1, 0, kSplit ? 1 : HPW);
+    if (kEarly && kSplit && more) request(c + 1, 1, HPW);
     if (RB < HPW && nh > 1) inter(HPW - 1);
     if (active)
       update_state<T, K, REV>(S, Q, ok, xf, REV ? s.eg[hw] : s.wt[hw], g4, s.decay[hw]);
+    if (!kEarly && kSplit && more) request(c + 1, 1, HPW);
     if (kScaled) {
       const int e = exponent();
       if (l == 0) s.ex[w] = e;

@@ -12,7 +12,7 @@
 //
 // Measured at 65,536 tokens, 32 heads in 8 groups, K = 128, V = 64, bf16: the
 // state walk 133 us for 402 MB (3.0 TB/s; 104 us with the update left out), the
-// outputs' 270 us for 841 MB (206), the sums in between 17 us.  Both walks are
+// outputs' 280 us for 841 MB, the sums in between 17 us.  Both walks are
 // bound by their loads and, little less, by the vector and matrix
 // instructions of the update; two chunks in flight instead of one took as long.
 #include <algorithm>
