@@ -122,8 +122,8 @@ def _seqs(x, cu_seqlens, cu_seqlens_cpu):
         # one blocking device-to-host copy (pass cu_seqlens_cpu to avoid it)
         cu_seqlens_cpu = cu_seqlens.detach().to("cpu")
     for t in (cu_seqlens, cu_seqlens_cpu):
-        if t.dtype not in (torch.int32, torch.int64):
-            raise GdrError(6, "cu_seqlens must be int32 or int64, got %s" % t.dtype)
+        if t.dtype.is_floating_point or t.dtype.is_complex or t.dtype == torch.bool:
+            raise GdrError(6, "cu_seqlens must hold integers, got %s" % t.dtype)
     wide = cu_seqlens_cpu.to(device="cpu")
     host = wide.to(torch.int32).contiguous()
     if wide.dtype != torch.int32 and not torch.equal(host.to(wide.dtype), wide):

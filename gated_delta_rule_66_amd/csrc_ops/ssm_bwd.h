@@ -16,8 +16,8 @@
 //            + sum_{r >= t} (row_r - dt_r q_r)
 //   row_r = sum_{i < r, in the chunk} E_ri + e^{gamma_r} dy_r . S^T C_r,
 //   dt_i q_i = sum_{r > i, in the chunk} E_ri,   far_i = e^{gamma_end - gamma_i} x_i . P^T B_i
-// (the pair i = r spans no decay; it is part of u_i . x_i = q_i + far_i + own_i
-// only).  dg at the chunk's first token is the A of the chunk before: a chain
+// (The pair i = r spans no decay; it is part of u_i . x_i = q_i + far_i + own_i
+// only.)  dg at the chunk's first token is the A of the chunk before: a chain
 // along the segment, from <S_end, P_end> at its end, that would add rounding
 // errors up without limit, since what spans a chunk is a difference of sums.
 // Two things end it.  Where a chunk decays by more than e^-24 nothing spans
@@ -34,8 +34,8 @@
 // of them are added up, so these must be near fp32.  W, one rounding of which
 // would be shared by a row of dB or dC, is a pair of operands too (dB and dC of a
 // short sequence 2.4 times as far from the definition with one), and C B^T o L
-// gives dx its diagonal in fp32.  The other products
-// round one operand (C B^T o L, S, P) to 16 bits, as their outputs are.
+// gives dx its diagonal in fp32.  The other products round one operand (C B^T o
+// L, S, P) to 16 bits, as their outputs are.
 //
 // One workgroup walks a segment for up to HPW heads of one group at once: they
 // share the B and C tiles and C B^T, and their dB and dC are summed in

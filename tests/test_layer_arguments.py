@@ -46,7 +46,7 @@ def test_group_sizes(group):
 def test_offsets_beyond_32_bits_and_other_types():
     x = torch.zeros(1, 8, 4)
     ok = torch.tensor([0, 3, 8])
-    for cu in (ok, ok.int()):
+    for cu in (ok, ok.int(), ok.short()):
         n, dev, host = _layer_ops._seqs(x, cu, None)
         assert n == 2 and host.dtype == dev.dtype == torch.int32 and host.tolist() == [0, 3, 8]
     far = torch.tensor([0, 3, (1 << 32) + 8])
