@@ -59,9 +59,8 @@ def _new(t, dtype=None):
 def _fits(name, *sizes):
     """The library takes sizes in 32 bits, and a conversion would drop the
     higher ones without a word: a size that does not fit is refused here."""
-    for v in sizes:
-        if not -1 << 31 <= v < 1 << 31:
-            raise GdrError(2, "%s has a size that does not fit 32 bits: %s" % (name, sizes))
+    if max(sizes) >= 1 << 31:
+        raise GdrError(2, "%s has a size that does not fit 32 bits: %s" % (name, sizes))
 
 
 def _need_gpu(name, t):
@@ -169,8 +168,7 @@ class _Conv:
                            % (tuple(x.shape), tuple(weight.shape)))
         B, T, D = x.shape
         W = weight.shape[1]
-        _fits("x", B, T, D)
-        _fits("weight", W)
+        _fits("x or weight", B, T, D, W)
         _need_gpu("x", x)
         dev = x.device
         dt = _code(x, "x")
@@ -289,8 +287,7 @@ class _Ssm:
                            % (tuple(x.shape), tuple(B.shape)))
         b, T, H, V = x.shape
         G, K = B.shape[2], B.shape[3]
-        _fits("x", b, T, H, V)
-        _fits("B", G, K)
+        _fits("x or B", b, T, H, V, G, K)
         _need_gpu("x", x)
         dev = x.device
         code = _code(x, "x")
