@@ -13,7 +13,9 @@ K = V = 128; bf16 or fp16 inputs; Hv a multiple of Hq.
 
 The operators around the recurrence in a layer (``_layer_ops``): the short
 causal convolution, the selective state space scan and the RMS norm with the
-residual's addition.
+residual's addition.  Those at a layer's ends (``_block_ops``): the norm of the
+output with its gate, the norms on both sides of the residual's addition, rows
+in 8 bits and their product.
 """
 from __future__ import annotations
 
@@ -22,6 +24,9 @@ from typing import Optional
 
 import torch
 
+from ._block_ops import (gated_rms_norm, gated_rms_norm_bwd, gated_rms_norm_fwd,
+                         gated_rms_norm_quant, int8_matmul, quantize_rows, sandwich_rms_norm,
+                         sandwich_rms_norm_bwd, sandwich_rms_norm_fwd, sandwich_rms_norm_quant)
 from ._layer_ops import (causal_conv1d, causal_conv1d_bwd, causal_conv1d_fwd,
                          causal_conv1d_update, chunk_selective_scan,
                          chunk_selective_scan_bwd, chunk_selective_scan_fwd,
@@ -38,6 +43,9 @@ __all__ = [
     "chunk_selective_scan", "chunk_selective_scan_fwd", "chunk_selective_scan_bwd",
     "fused_recurrent_selective_scan",
     "rms_norm", "rms_norm_fwd", "rms_norm_bwd", "rms_norm_quant",
+    "gated_rms_norm", "gated_rms_norm_fwd", "gated_rms_norm_bwd", "gated_rms_norm_quant",
+    "sandwich_rms_norm", "sandwich_rms_norm_fwd", "sandwich_rms_norm_bwd",
+    "sandwich_rms_norm_quant", "quantize_rows", "int8_matmul",
 ]
 
 CHUNK = 64

@@ -73,6 +73,43 @@ class NormProblem(ctypes.Structure):
     ]
 
 
+class GatedNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("D", ctypes.c_int32), ("norm_size", ctypes.c_int32),
+        ("dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+        ("shared_weight", ctypes.c_int32), ("gate_first", ctypes.c_int32),
+        ("activation", ctypes.c_int32), ("quant", ctypes.c_int32),
+        ("scale_group", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+    ]
+
+
+class SandwichNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+        ("activation", ctypes.c_int32), ("quant", ctypes.c_int32),
+        ("group_size", ctypes.c_int32), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+        ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+    ]
+
+
+class QuantizeProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int),
+        ("quant", ctypes.c_int32), ("group_size", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+
+class Int8MatmulProblem(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int), ("bias_dtype", ctypes.c_int),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+
 # every symbol include/gdr.h declares
 EXPORTS = [
     "gdr_status_string", "gdr_last_error", "gdr_check_supported", "gdr_check_device",
@@ -89,6 +126,10 @@ EXPORTS = [
     "gdr_rms_norm_bwd_workspace_size", "gdr_rms_norm_bwd",
     "gdr_ssm_check", "gdr_ssm_fwd_workspace_size", "gdr_ssm_fwd", "gdr_ssm_step",
     "gdr_ssm_bwd_workspace_size", "gdr_ssm_bwd",
+    "gdr_gated_norm_check", "gdr_gated_norm_fwd", "gdr_gated_norm_bwd_workspace_size",
+    "gdr_gated_norm_bwd", "gdr_sandwich_norm_check", "gdr_sandwich_norm_fwd",
+    "gdr_sandwich_norm_bwd_workspace_size", "gdr_sandwich_norm_bwd", "gdr_quantize_check",
+    "gdr_quantize_rows", "gdr_int8_matmul_check", "gdr_int8_matmul",
 ]
 
 
@@ -185,6 +226,22 @@ def _declare_ops(lib):
     fn("gdr_rms_norm_fwd", [NP] + [P] * 8)
     fn("gdr_rms_norm_bwd_workspace_size", [NP], S)
     fn("gdr_rms_norm_bwd", [NP] + [P] * 9 + [S, P])
+    GP = ctypes.POINTER(GatedNormProblem)
+    fn("gdr_gated_norm_check", [GP, ctypes.c_char_p, S])
+    fn("gdr_gated_norm_fwd", [GP] + [P] * 7)
+    fn("gdr_gated_norm_bwd_workspace_size", [GP], S)
+    fn("gdr_gated_norm_bwd", [GP] + [P] * 9 + [S, P])
+    WP = ctypes.POINTER(SandwichNormProblem)
+    fn("gdr_sandwich_norm_check", [WP, ctypes.c_char_p, S])
+    fn("gdr_sandwich_norm_fwd", [WP] + [P] * 12)
+    fn("gdr_sandwich_norm_bwd_workspace_size", [WP], S)
+    fn("gdr_sandwich_norm_bwd", [WP] + [P] * 17 + [S, P])
+    QP = ctypes.POINTER(QuantizeProblem)
+    fn("gdr_quantize_check", [QP, ctypes.c_char_p, S])
+    fn("gdr_quantize_rows", [QP] + [P] * 4)
+    MP = ctypes.POINTER(Int8MatmulProblem)
+    fn("gdr_int8_matmul_check", [MP, ctypes.c_char_p, S])
+    fn("gdr_int8_matmul", [MP] + [P] * 7)
 
 
 def load():

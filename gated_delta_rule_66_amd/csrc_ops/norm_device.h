@@ -1,0 +1,232 @@
+// norm_device.h -- what the operators on rows share: a row in the registers of
+// its threads, sums over it, and its quantisation to 8 bits.
+//
+// A row's threads hold 8 elements each per step.  Where the width is no
+// multiple of 8 the row's last vector is moved back to end with the row: loads
+// need no bounds, the elements that it repeats are left out of sums and
+// maxima, and its stores repeat their bits.
+#pragma once
+
+#include <type_traits>
+
+#include "ops_device.h"
+#include "ops_internal.h"
+
+namespace gdr {
+
+constexpr float kTinyScale = 1.1754943508222875e-38f;  // 2^-126
+
+// Where vector vi of a row starts (PART: rows of fewer than 8 elements).
+template <bool PART>
+__device__ __forceinline__ int column_of(int vi, int D) {
+  return PART ? 0 : min(vi * 8, D - 8);
+}
+
+// Eight consecutive elements of any of the types, in fp32.
+template <typename T, bool PART>
+__device__ __forceinline__ void load8(const T* p, int D, float* f) {
+  constexpr int V = Vec<T>::n;
+#pragma unroll
+  for (int k = 0; k < 8; k += V) {
+    Vec<T> v;
+    if (PART) v.load_part(p + k, max(0, D - k));
+    else v.load(p + k);
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[k + e] = to_f(v.v[e]);
+  }
+}
+template <typename T, bool PART>
+__device__ __forceinline__ void store8(T* p, int D, const float* f) {
+  constexpr int V = Vec<T>::n;
+#pragma unroll
+  for (int k = 0; k < 8; k += V) {
+    Vec<T> v;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v.v[e] = from_f<T>(f[k + e]);
+    if (PART) v.store_part(p + k, max(0, D - k));
+    else v.store(p + k);
+  }
+}
+template <bool PART>
+__device__ __forceinline__ void load_weight(const void* p, int c, int D, int dtype, float* f) {
+  if (dtype == GDR_BF16) load8<__bf16, PART>(reinterpret_cast<const __bf16*>(p) + c, D, f);
+  else if (dtype == GDR_FP16) load8<_Float16, PART>(reinterpret_cast<const _Float16*>(p) + c, D, f);
+  else load8<float, PART>(reinterpret_cast<const float*>(p) + c, D, f);
+}
+
+// Largest magnitude that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  return (a > b || a != a) ? a : b;
+}
+// over the 16 lanes of a lane group; over the wave
+__device__ __forceinline__ float max16(float v) {
+  v = max_nan(v, dpp_mov<0xB1>(v));
+  v = max_nan(v, dpp_mov<0x4E>(v));
+  v = max_nan(v, dpp_mov<0x141>(v));
+  return max_nan(v, dpp_mov<0x140>(v));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = max16(v);
+  v = max_nan(v, __shfl_xor(v, 16, 64));
+  return max_nan(v, __shfl_xor(v, 32, 64));
+}
+
+// Sum (or largest) of v over the NT threads of a row; every thread of the
+// row gets the same bits.  Rows of one wave share a block, four at a time.
+template <int NT, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* lds) {
+  v = MAX ? wave_max(v) : wave_sum(v);
+  if (NT == 64) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = lds[0];
+#pragma unroll
+  for (int i = 1; i < NT / 64; ++i) s = MAX ? max_nan(s, lds[i]) : s + lds[i];
+  return s;
+}
+
+// The same for a sum in 64 bits.
+template <int CTRL>
+__device__ __forceinline__ double dpp_mov2(double v) {
+  const uint2 u = __builtin_bit_cast(uint2, v);
+  const uint2 r{__builtin_bit_cast(uint32_t, dpp_mov<CTRL>(__builtin_bit_cast(float, u.x))),
+                __builtin_bit_cast(uint32_t, dpp_mov<CTRL>(__builtin_bit_cast(float, u.y)))};
+  return __builtin_bit_cast(double, r);
+}
+template <int NT>
+__device__ __forceinline__ double row_sum(double v, double* lds) {
+  v += dpp_mov2<0xB1>(v);
+  v += dpp_mov2<0x4E>(v);
+  v += dpp_mov2<0x141>(v);
+  v += dpp_mov2<0x140>(v);
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  if (NT == 64) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = lds[0];
+#pragma unroll
+  for (int i = 1; i < NT / 64; ++i) s += lds[i];
+  return s;
+}
+
+__device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
+  int r = 0;
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+  return (uint32_t)r;
+}
+__device__ __forceinline__ uint32_t int8_of(float v) {
+  return v != v ? 0u : (uint32_t)(int)rintf(v) & 0xffu;
+}
+
+// A gate's activation (0: none, 1: silu, 2: sigmoid) and its derivative.  The
+// exponential is taken at -80 at the least, where the sigmoid is 2^-115: with
+// an infinity it would make silu's limit 0 and the slopes' products NaN.
+struct Gate {
+  float value, slope;
+};
+__device__ __forceinline__ Gate gate_and_slope(float z, int act) {
+  if (act == 0) return {z, 1.f};
+  const float zc = z < -80.f ? -80.f : z;  // a NaN passes
+  const float e = __expf(-zc), s = fast_rcp(1.f + e), rest = e * s;
+  if (act == 1) return {zc * s, s * (1.f + zc * rest)};
+  return {s, s * rest};
+}
+__device__ __forceinline__ float gate_of(float z, int act) {
+  if (act == 0) return z;
+  const float zc = z < -80.f ? -80.f : z;
+  const float s = fast_rcp(1.f + __expf(-zc));
+  return act == 1 ? zc * s : s;
+}
+
+// Threads of a block: one row of NT threads, or (NT == 64) four rows of one
+// wave each.
+template <int NT>
+constexpr int block_of() {
+  return NT == 64 ? 256 : NT;
+}
+
+// Eight values over the scale s, rounded to nearest even: e4m3 or int8.
+__device__ __forceinline__ void quantise8(const float (&f)[8], float s, bool fp8, uint32_t (&b)[2]) {
+  const float top = fp8 ? 448.f : 127.f;
+  float q[8];
+  // (an infinite scale leaves the product's 0 or NaN as they are)
+  const float inv = 1.f / s, fin = s < __builtin_inff() ? s : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // the product with the reciprocal may lie on the other side of a tie,
+    // a whole step off in 8 bits: the residual makes it the fp32 quotient
+    q[e] = f[e] * inv;
+    q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], fin, f[e]), inv, q[e]);
+    // a NaN passes both comparisons
+    q[e] = q[e] > top ? top : q[e] < -top ? -top : q[e];
+  }
+  if (fp8) {
+    b[0] = pack_fp8(q[0], q[1], q[2], q[3]);
+    b[1] = pack_fp8(q[4], q[5], q[6], q[7]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      b[k] = int8_of(q[4 * k]) | int8_of(q[4 * k + 1]) << 8 | int8_of(q[4 * k + 2]) << 16 |
+             int8_of(q[4 * k + 3]) << 24;
+  }
+}
+// Eight bytes to any address.
+__device__ __forceinline__ void store_bytes8(uint8_t* y, const uint32_t (&b)[2]) {
+  struct __attribute__((packed, aligned(1))) Raw {
+    uint32_t u[2];
+  };
+  *reinterpret_cast<Raw*>(y) = Raw{{b[0], b[1]}};
+}
+
+// A row's values f to 8 bits (`quant` 1: e4m3, 2: int8): scale = max |f| / top,
+// at least 2^-126 so that rows of zeros stay zeros, over the row (`group` 0) or
+// over each 128 columns; the quotient is rounded to nearest even.  `lds`: 16
+// floats that the row's threads share.
+template <int NT, int VPT, bool PART>
+__device__ __forceinline__ void quantise_row(const float (&f)[VPT][8], int64_t row, int tid, int D,
+                                             int quant, int group, uint8_t* q_out, float* scale,
+                                             float* lds) {
+  const bool fp8 = quant == 1;
+  const float top = fp8 ? 448.f : 127.f;
+  const int ngroups = (D + 127) / 128;
+  float row_scale = 0.f;
+  if (group == 0) {
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = max_nan(mx, fabsf(f[i][e]));
+    mx = row_reduce<NT, true>(mx, lds) / top;
+    row_scale = mx < kTinyScale ? kTinyScale : mx;
+    if (tid == 0) scale[row] = row_scale;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, D);
+    float s = row_scale;
+    if (group) {  // 16 consecutive lanes hold a group's 128 columns
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = c + e >= v0 ? max_nan(mx, fabsf(f[i][e])) : mx;
+      mx = max16(mx) / top;
+      s = mx < kTinyScale ? kTinyScale : mx;
+      if ((tid & 15) == 0 && v0 < D) scale[row * ngroups + v0 / 128] = s;
+    }
+    if (v0 < D) {
+      uint32_t b[2];
+      quantise8(f[i], s, fp8, b);
+      uint8_t* y = q_out + row * D + c;
+      if (!PART && c == v0) {
+        store_bytes8(y, b);
+      } else {  // what the vector repeats may belong to another scale
+        for (int e = v0 - c; e < min(8, D); ++e) y[e] = (uint8_t)(b[e >> 2] >> (8 * (e & 3)));
+      }
+    }
+  }
+}
+
+}  // namespace gdr

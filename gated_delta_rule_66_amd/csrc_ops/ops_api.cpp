@@ -1,5 +1,6 @@
 // ops_api.cpp -- the C ABI of the layer operators: argument validation and
 // workspace sizes.  Host code; validation finishes before the first HIP call.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -154,6 +155,112 @@ static gdr_status validate(const gdr_ssm_problem* p, char* reason, size_t len) {
   if (!is_flag(p->dt_softplus) || !is_flag(p->keep_states))
     return fail(GDR_ERR_ARG, reason, len, "dt_softplus and keep_states must be 0 or 1");
   return check_seqs(p->B, p->T, p->N, p->cu_seqlens_dev, p->cu_seqlens_host, reason, len);
+}
+
+// What the operators on rows share: sizes, types, strides, 8-bit outputs.
+static gdr_status check_rows(int rows, int D, int most, gdr_dtype dtype, int quant, int group,
+                             char* reason, size_t len) {
+  if (!is_type(dtype))
+    return fail(GDR_ERR_DTYPE, reason, len, "x must be bf16, fp16 or fp32 (got code %d)", (int)dtype);
+  if (rows < 1 || D < 1)
+    return fail(GDR_ERR_SHAPE, reason, len, "sizes must be positive (rows=%d D=%d)", rows, D);
+  if (D > most) return fail(GDR_ERR_SHAPE, reason, len, "at most %d columns, got %d", most, D);
+  // a launch holds fewer than 2^32 threads: 64, 256 or 1024 a row
+  if ((int64_t)rows * (D <= 1024 ? 64 : D <= 16384 ? 256 : 1024) > 0xffff0000ll)
+    return fail(GDR_ERR_SHAPE, reason, len, "too many rows (%d of %d columns)", rows, D);
+  if (quant < 0 || quant > 2)
+    return fail(GDR_ERR_ARG, reason, len, "quant must be 0 (none), 1 (e4m3) or 2 (int8)");
+  if (group != 0 && group != 128)
+    return fail(GDR_ERR_ARG, reason, len, "columns per scale must be 0 (the row) or 128, got %d",
+                group);
+  if (!quant && group)
+    return fail(GDR_ERR_ARG, reason, len, "columns per scale are for quantised outputs");
+  return GDR_OK;
+}
+static gdr_status check_stride(const char* name, int64_t stride, int D, char* reason, size_t len) {
+  if (stride < D)
+    return fail(GDR_ERR_SHAPE, reason, len, "%s_stride=%lld is below D=%d", name, (long long)stride,
+                D);
+  return GDR_OK;
+}
+
+static gdr_status validate(const gdr_gated_norm_problem* p, char* reason, size_t len) {
+  if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
+  gdr_status s = check_rows(p->rows, p->D, 16384, p->dtype, p->quant, p->scale_group, reason, len);
+  if (s != GDR_OK) return s;
+  if (p->w_dtype != p->dtype && p->w_dtype != GDR_FP32)
+    return fail(GDR_ERR_DTYPE, reason, len, "the weight must have x's dtype or fp32 (got code %d)",
+                (int)p->w_dtype);
+  if (p->norm_size < 1 || p->D % p->norm_size != 0)
+    return fail(GDR_ERR_SHAPE, reason, len, "D must be a multiple of norm_size (D=%d norm_size=%d)",
+                p->D, p->norm_size);
+  // groups that no wave's lanes hold have threads of their own, 64 or 256 each;
+  // their 8-bit outputs 256 a row
+  const int n = p->norm_size;
+  if ((n % 8 != 0 || n > 512 || (n & (n - 1)) != 0) &&
+      p->rows * std::max<int64_t>(256, (int64_t)(p->D / n) * (n <= 1024 ? 64 : 256)) > 0xffff0000ll)
+    return fail(GDR_ERR_SHAPE, reason, len, "too many groups (%d rows of %d)", p->rows, p->D / n);
+  if (!is_flag(p->shared_weight) || !is_flag(p->gate_first))
+    return fail(GDR_ERR_ARG, reason, len, "shared_weight and gate_first must be 0 or 1");
+  if (p->activation != 1 && p->activation != 2)
+    return fail(GDR_ERR_ARG, reason, len, "activation must be 1 (silu) or 2 (sigmoid)");
+  if (!std::isfinite(p->eps) || p->eps < 0.f)
+    return fail(GDR_ERR_ARG, reason, len, "eps must be finite and >= 0");
+  if ((s = check_stride("x", p->x_stride, p->D, reason, len)) != GDR_OK) return s;
+  return check_stride("gate", p->gate_stride, p->D, reason, len);
+}
+
+static gdr_status validate(const gdr_sandwich_norm_problem* p, char* reason, size_t len) {
+  if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
+  gdr_status s = check_rows(p->rows, p->D, 16384, p->dtype, p->quant, p->group_size, reason, len);
+  if (s != GDR_OK) return s;
+  if (p->res_dtype != p->dtype && p->res_dtype != GDR_FP32)
+    return fail(GDR_ERR_DTYPE, reason, len, "the residual must have x's dtype or fp32 (got code %d)",
+                (int)p->res_dtype);
+  if (p->w_dtype != p->dtype && p->w_dtype != GDR_FP32)
+    return fail(GDR_ERR_DTYPE, reason, len, "the weights must have x's dtype or fp32 (got code %d)",
+                (int)p->w_dtype);
+  if (p->activation < 0 || p->activation > 2)
+    return fail(GDR_ERR_ARG, reason, len, "activation must be 0 (none), 1 (silu) or 2 (sigmoid)");
+  if (!std::isfinite(p->eps) || p->eps < 0.f)
+    return fail(GDR_ERR_ARG, reason, len, "eps must be finite and >= 0");
+  if (!std::isfinite(p->alpha)) return fail(GDR_ERR_ARG, reason, len, "alpha must be finite");
+  if ((s = check_stride("x", p->x_stride, p->D, reason, len)) != GDR_OK) return s;
+  return check_stride("gate", p->gate_stride, p->D, reason, len);
+}
+
+static gdr_status validate(const gdr_quantize_problem* p, char* reason, size_t len) {
+  if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
+  gdr_status s = check_rows(p->rows, p->D, 65536, p->dtype, p->quant, p->group_size, reason, len);
+  if (s != GDR_OK) return s;
+  if (p->quant == 0)
+    return fail(GDR_ERR_ARG, reason, len, "quant must be 1 (e4m3) or 2 (int8)");
+  return check_stride("x", p->x_stride, p->D, reason, len);
+}
+
+static gdr_status validate(const gdr_int8_matmul_problem* p, char* reason, size_t len) {
+  if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
+  if (!is_type(p->out_dtype))
+    return fail(GDR_ERR_DTYPE, reason, len, "the output must be bf16, fp16 or fp32 (got code %d)",
+                (int)p->out_dtype);
+  if (p->bias_dtype != p->out_dtype && p->bias_dtype != GDR_FP32)
+    return fail(GDR_ERR_DTYPE, reason, len, "the bias must have the output's dtype or fp32 (got code %d)",
+                (int)p->bias_dtype);
+  if (p->M < 1 || p->N < 1 || p->K < 1)
+    return fail(GDR_ERR_SHAPE, reason, len, "sizes must be positive (M=%d N=%d K=%d)", p->M, p->N,
+                p->K);
+  // 65536 products of at most 2^14 stay below 2^31
+  if (p->K > 65536) return fail(GDR_ERR_SHAPE, reason, len, "at most K = 65536, got %d", p->K);
+  // a launch holds fewer than 2^32 threads: 256 for 128 x 128 outputs, 512 for 16
+  // channels of a few tokens
+  if ((((int64_t)p->M + 127) / 128) * (((int64_t)p->N + 127) / 128) > (1 << 23) ||
+      p->N > (1 << 26))
+    return fail(GDR_ERR_SHAPE, reason, len, "problem too large (M=%d N=%d)", p->M, p->N);
+  // the rows of a tile lie within 2^31 bytes
+  if (p->x_stride < p->K || p->x_stride > (1 << 22))
+    return fail(GDR_ERR_SHAPE, reason, len, "x_stride=%lld must be K=%d to 2^22",
+                (long long)p->x_stride, p->K);
+  return GDR_OK;
 }
 
 static bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
@@ -338,6 +445,138 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_problem* p, const void* dy, const voi
   if ((s = gdr_check_device()) != GDR_OK) return s;
   return launch_norm_bwd(p, dy, h, weight, rstd, dh, dx, dresidual, dweight, workspace,
                          (hipStream_t)stream);
+}
+
+gdr_status gdr_gated_norm_check(const gdr_gated_norm_problem* p, char* reason, size_t reason_len) {
+  const gdr_status s = validate(p, reason, reason_len);
+  if (s == GDR_OK && reason && reason_len) reason[0] = '\0';
+  return s;
+}
+
+gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x, const void* gate,
+                              const void* weight, void* y, float* scale, float* rstd,
+                              void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (!x || !gate || !weight || !y)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required gated-norm pointer is NULL");
+  if ((scale != nullptr) != (p->quant != 0))
+    return fail(GDR_ERR_NULL, nullptr, 0, "scale comes with a quantised output, and only then");
+  if (rstd && p->quant)
+    return fail(GDR_ERR_ARG, nullptr, 0, "rstd is for the gradient, which a quantised output has not");
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_gated_norm_fwd(p, x, gate, weight, y, scale, rstd, (hipStream_t)stream);
+}
+
+size_t gdr_gated_norm_bwd_workspace_size(const gdr_gated_norm_problem* p) {
+  return validate(p, nullptr, 0) == GDR_OK ? gated_norm_bwd_workspace(p) : 0;
+}
+
+gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem* p, const void* dy, const void* x,
+                              const void* gate, const void* weight, const float* rstd, void* dx,
+                              void* dgate, void* dweight, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (p->quant) return fail(GDR_ERR_ARG, nullptr, 0, "a quantised output has no gradient");
+  if (!dy || !x || !gate || !weight || !rstd || !dx || !dgate || !dweight)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required gated-norm-gradient pointer is NULL");
+  s = need_workspace(gated_norm_bwd_workspace(p), workspace, workspace_bytes, "gated-norm-gradient");
+  if (s != GDR_OK) return s;
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_gated_norm_bwd(p, dy, x, gate, weight, rstd, dx, dgate, dweight, workspace,
+                               (hipStream_t)stream);
+}
+
+gdr_status gdr_sandwich_norm_check(const gdr_sandwich_norm_problem* p, char* reason,
+                                   size_t reason_len) {
+  const gdr_status s = validate(p, reason, reason_len);
+  if (s == GDR_OK && reason && reason_len) reason[0] = '\0';
+  return s;
+}
+
+gdr_status gdr_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const void* x,
+                                 const void* residual, const void* gate, const void* post_weight,
+                                 const void* res_scale, const void* pre_weight, void* y,
+                                 float* scale, void* h, float* rstd_x, float* rstd_h,
+                                 void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (!x || !residual || !pre_weight || !y || !h)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required sandwich-norm pointer is NULL");
+  if ((scale != nullptr) != (p->quant != 0))
+    return fail(GDR_ERR_NULL, nullptr, 0, "scale comes with a quantised output, and only then");
+  if (rstd_x && !post_weight)
+    return fail(GDR_ERR_ARG, nullptr, 0, "rstd_x comes with post_weight");
+  if (h == residual) return fail(GDR_ERR_ARG, nullptr, 0, "h may not be residual");
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_sandwich_norm_fwd(p, x, residual, gate, post_weight, res_scale, pre_weight, y, scale,
+                                  h, rstd_x, rstd_h, (hipStream_t)stream);
+}
+
+size_t gdr_sandwich_norm_bwd_workspace_size(const gdr_sandwich_norm_problem* p) {
+  return validate(p, nullptr, 0) == GDR_OK ? sandwich_norm_bwd_workspace(p) : 0;
+}
+
+gdr_status gdr_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const void* dy, const void* dh,
+                                 const void* x, const void* h, const void* gate,
+                                 const void* post_weight, const void* res_scale,
+                                 const void* pre_weight, const float* rstd_x, const float* rstd_h,
+                                 void* dx, void* dresidual, void* dgate, void* dpost_weight,
+                                 void* dres_scale, void* dpre_weight, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (p->quant) return fail(GDR_ERR_ARG, nullptr, 0, "a quantised output has no gradient");
+  if (!dy || !x || !h || !pre_weight || !rstd_h || !dx || !dresidual || !dpre_weight)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required sandwich-norm-gradient pointer is NULL");
+  if ((gate != nullptr) != (dgate != nullptr))
+    return fail(GDR_ERR_NULL, nullptr, 0, "dgate comes with gate, and only then");
+  if ((post_weight != nullptr) != (rstd_x != nullptr))
+    return fail(GDR_ERR_NULL, nullptr, 0, "rstd_x comes with post_weight, and only then");
+  if ((dpost_weight && !post_weight) || (dres_scale && !res_scale))
+    return fail(GDR_ERR_ARG, nullptr, 0, "dpost_weight and dres_scale need their inputs");
+  s = need_workspace(sandwich_norm_bwd_workspace(p), workspace, workspace_bytes,
+                     "sandwich-norm-gradient");
+  if (s != GDR_OK) return s;
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_sandwich_norm_bwd(p, dy, dh, x, h, gate, post_weight, res_scale, pre_weight, rstd_x,
+                                  rstd_h, dx, dresidual, dgate, dpost_weight, dres_scale,
+                                  dpre_weight, workspace, (hipStream_t)stream);
+}
+
+gdr_status gdr_quantize_check(const gdr_quantize_problem* p, char* reason, size_t reason_len) {
+  const gdr_status s = validate(p, reason, reason_len);
+  if (s == GDR_OK && reason && reason_len) reason[0] = '\0';
+  return s;
+}
+
+gdr_status gdr_quantize_rows(const gdr_quantize_problem* p, const void* x, void* q, float* scale,
+                             void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (!x || !q || !scale)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required quantisation pointer is NULL");
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_quantize_rows(p, x, q, scale, (hipStream_t)stream);
+}
+
+gdr_status gdr_int8_matmul_check(const gdr_int8_matmul_problem* p, char* reason,
+                                 size_t reason_len) {
+  const gdr_status s = validate(p, reason, reason_len);
+  if (s == GDR_OK && reason && reason_len) reason[0] = '\0';
+  return s;
+}
+
+gdr_status gdr_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, const float* x_scale,
+                           const void* weight, const float* w_scale, const void* bias, void* y,
+                           void* stream) {
+  gdr_status s = validate(p, nullptr, 0);
+  if (s != GDR_OK) return s;
+  if (!x || !x_scale || !weight || !w_scale || !y)
+    return fail(GDR_ERR_NULL, nullptr, 0, "a required matrix-product pointer is NULL");
+  if ((s = gdr_check_device()) != GDR_OK) return s;
+  return launch_int8_matmul(p, x, x_scale, weight, w_scale, bias, y, (hipStream_t)stream);
 }
 
 }  // extern "C"

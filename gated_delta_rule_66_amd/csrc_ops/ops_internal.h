@@ -1,6 +1,6 @@
 // ops_internal.h -- host-side interface between the C ABI of the layer
-// operators (short convolution, selective scan, residual RMS norm) and their
-// launchers.
+// operators (short convolution, selective scan, residual RMS norm, gated and
+// sandwich norm, rows and products in 8 bits) and their launchers.
 #pragma once
 
 #include "../csrc/gdr_internal.h"
@@ -28,6 +28,39 @@ gdr_status launch_norm_fwd(const gdr_norm_problem* p, const void* x, const void*
 gdr_status launch_norm_bwd(const gdr_norm_problem* p, const void* dy, const void* h,
                            const void* weight, const float* rstd, const void* dh_out, void* dx,
                            void* dres, void* dw, void* ws, hipStream_t st);
+
+// out[c] = the sum of part[r][c] over the rows, in a fixed order.
+void launch_reduce_rows(const float* part, int rows, int cols, void* out, int dtype,
+                        hipStream_t st);
+
+// --- gated RMS norm (gated_norm.hip) ---
+gdr_status launch_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x, const void* gate,
+                                 const void* weight, void* y, float* scale, float* rstd,
+                                 hipStream_t st);
+size_t gated_norm_bwd_workspace(const gdr_gated_norm_problem* p);
+gdr_status launch_gated_norm_bwd(const gdr_gated_norm_problem* p, const void* dy, const void* x,
+                                 const void* gate, const void* weight, const float* rstd, void* dx,
+                                 void* dgate, void* dweight, void* ws, hipStream_t st);
+
+// --- sandwich RMS norm (sandwich_norm.hip) ---
+gdr_status launch_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const void* x,
+                                    const void* residual, const void* gate, const void* post,
+                                    const void* res_scale, const void* pre, void* y, float* scale,
+                                    void* h, float* rstd_x, float* rstd_h, hipStream_t st);
+size_t sandwich_norm_bwd_workspace(const gdr_sandwich_norm_problem* p);
+gdr_status launch_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const void* dy,
+                                    const void* dh, const void* x, const void* h, const void* gate,
+                                    const void* post, const void* res_scale, const void* pre,
+                                    const float* rstd_x, const float* rstd_h, void* dx,
+                                    void* dresidual, void* dgate, void* dpost, void* dscale,
+                                    void* dpre, void* ws, hipStream_t st);
+
+// --- rows and products in 8 bits (quantize.hip, int8_matmul.hip) ---
+gdr_status launch_quantize_rows(const gdr_quantize_problem* p, const void* x, void* q, float* scale,
+                                hipStream_t st);
+gdr_status launch_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, const float* x_scale,
+                              const void* w, const float* w_scale, const void* bias, void* y,
+                              hipStream_t st);
 
 // --- selective state space scan (ssm_fwd.hip, ssm_bwd.hip) ---
 struct SsmPlan {

@@ -5,117 +5,15 @@
 //
 // Memory bounds it: every operand is touched once.  A row stays in the
 // registers of its threads, 8 elements each per step, from its load through
-// the sum of squares to the store.  Where the width is no multiple of 8 the
-// row's last vector is moved back to end with the row: loads need no bounds,
-// the elements that it repeats are left out of sums and maxima, and its
-// stores repeat their bits.
+// the sum of squares to the store.
 #include <algorithm>
 #include <type_traits>
 
-#include "ops_device.h"
-#include "ops_internal.h"
+#include "norm_device.h"
 
 namespace gdr {
 
 namespace {
-
-constexpr float kTinyScale = 1.1754943508222875e-38f;  // 2^-126
-
-// Where vector vi of a row starts (PART: rows of fewer than 8 elements).
-template <bool PART>
-__device__ __forceinline__ int column_of(int vi, int D) {
-  return PART ? 0 : min(vi * 8, D - 8);
-}
-
-// Eight consecutive elements of any of the types, in fp32.
-template <typename T, bool PART>
-__device__ __forceinline__ void load8(const T* p, int D, float* f) {
-  constexpr int V = Vec<T>::n;
-#pragma unroll
-  for (int k = 0; k < 8; k += V) {
-    Vec<T> v;
-    if (PART) v.load_part(p + k, max(0, D - k));
-    else v.load(p + k);
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[k + e] = to_f(v.v[e]);
-  }
-}
-template <typename T, bool PART>
-__device__ __forceinline__ void store8(T* p, int D, const float* f) {
-  constexpr int V = Vec<T>::n;
-#pragma unroll
-  for (int k = 0; k < 8; k += V) {
-    Vec<T> v;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v.v[e] = from_f<T>(f[k + e]);
-    if (PART) v.store_part(p + k, max(0, D - k));
-    else v.store(p + k);
-  }
-}
-template <bool PART>
-__device__ __forceinline__ void load_weight(const void* p, int c, int D, int dtype, float* f) {
-  if (dtype == GDR_BF16) load8<__bf16, PART>(reinterpret_cast<const __bf16*>(p) + c, D, f);
-  else if (dtype == GDR_FP16) load8<_Float16, PART>(reinterpret_cast<const _Float16*>(p) + c, D, f);
-  else load8<float, PART>(reinterpret_cast<const float*>(p) + c, D, f);
-}
-
-// Largest magnitude that keeps a NaN.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  return (a > b || a != a) ? a : b;
-}
-// over the 16 lanes of a lane group; over the wave
-__device__ __forceinline__ float max16(float v) {
-  v = max_nan(v, dpp_mov<0xB1>(v));
-  v = max_nan(v, dpp_mov<0x4E>(v));
-  v = max_nan(v, dpp_mov<0x141>(v));
-  return max_nan(v, dpp_mov<0x140>(v));
-}
-__device__ __forceinline__ float wave_max(float v) {
-  v = max16(v);
-  v = max_nan(v, __shfl_xor(v, 16, 64));
-  return max_nan(v, __shfl_xor(v, 32, 64));
-}
-
-// Sum (or largest) of v over the NT threads of a row; every thread of the
-// row gets the same bits.  Rows of one wave share a block, four at a time.
-template <int NT, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* lds) {
-  v = MAX ? wave_max(v) : wave_sum(v);
-  if (NT == 64) return v;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = lds[0];
-#pragma unroll
-  for (int i = 1; i < NT / 64; ++i) s = MAX ? max_nan(s, lds[i]) : s + lds[i];
-  return s;
-}
-
-// The same for a sum in 64 bits.
-template <int CTRL>
-__device__ __forceinline__ double dpp_mov2(double v) {
-  const uint2 u = __builtin_bit_cast(uint2, v);
-  const uint2 r{__builtin_bit_cast(uint32_t, dpp_mov<CTRL>(__builtin_bit_cast(float, u.x))),
-                __builtin_bit_cast(uint32_t, dpp_mov<CTRL>(__builtin_bit_cast(float, u.y)))};
-  return __builtin_bit_cast(double, r);
-}
-template <int NT>
-__device__ __forceinline__ double row_sum(double v, double* lds) {
-  v += dpp_mov2<0xB1>(v);
-  v += dpp_mov2<0x4E>(v);
-  v += dpp_mov2<0x141>(v);
-  v += dpp_mov2<0x140>(v);
-  v += __shfl_xor(v, 16, 64);
-  v += __shfl_xor(v, 32, 64);
-  if (NT == 64) return v;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double s = lds[0];
-#pragma unroll
-  for (int i = 1; i < NT / 64; ++i) s += lds[i];
-  return s;
-}
 
 struct NormArgs {
   const void* x;
@@ -136,23 +34,6 @@ struct NormArgs {
   float* part;         // [blocks][D]
   int blocks;
 };
-
-__device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
-  int r = 0;
-  r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
-  r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
-  return (uint32_t)r;
-}
-__device__ __forceinline__ uint32_t int8_of(float v) {
-  return v != v ? 0u : (uint32_t)(int)rintf(v) & 0xffu;
-}
-
-// Threads of a block: one row of NT threads, or (NT == 64) four rows of one
-// wave each.
-template <int NT>
-constexpr int block_of() {
-  return NT == 64 ? 256 : NT;
-}
 
 // The forward.  RES: the residual's type, void without one.  Memory bounds it:
 // 16,384 rows of 4096 bf16 columns with a residual to e4m3 take 89 us for 472
@@ -211,68 +92,8 @@ __global__ __launch_bounds__(block_of<NT>()) void norm_fwd_kernel(NormArgs a) {
   }
   if (!QUANT) return;
 
-  // 8 bits: scale = max |y| / top, at least 2^-126 so that rows of zeros stay
-  // zeros; the quotient is rounded to nearest even
-  const bool fp8 = a.quant == 1;
-  const float top = fp8 ? 448.f : 127.f;
-  const int ngroups = (a.D + 127) / 128;
-  float row_scale = 0.f;
-  if (a.group == 0) {
-    float mx = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = max_nan(mx, fabsf(f[i][e]));
-    mx = row_reduce<NT, true>(mx, lds) / top;
-    row_scale = mx < kTinyScale ? kTinyScale : mx;
-    if (tid == 0) a.scale[row] = row_scale;
-  }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
-    float s = row_scale;
-    if (a.group) {  // 16 consecutive lanes hold a group's 128 columns
-      float mx = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = c + e >= v0 ? max_nan(mx, fabsf(f[i][e])) : mx;
-      mx = max16(mx) / top;
-      s = mx < kTinyScale ? kTinyScale : mx;
-      if ((tid & 15) == 0 && v0 < a.D) a.scale[row * ngroups + v0 / 128] = s;
-    }
-    if (v0 < a.D) {
-      float q[8];
-      // (an infinite scale leaves the product's 0 or NaN as they are)
-      const float inv = 1.f / s, fin = s < __builtin_inff() ? s : 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // the product with the reciprocal may lie on the other side of a tie,
-        // a whole step off in 8 bits: the residual makes it the fp32 quotient
-        q[e] = f[i][e] * inv;
-        q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], fin, f[i][e]), inv, q[e]);
-        // a NaN passes both comparisons
-        q[e] = q[e] > top ? top : q[e] < -top ? -top : q[e];
-      }
-      uint32_t b[2];
-      if (fp8) {
-        b[0] = pack_fp8(q[0], q[1], q[2], q[3]);
-        b[1] = pack_fp8(q[4], q[5], q[6], q[7]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          b[k] = int8_of(q[4 * k]) | int8_of(q[4 * k + 1]) << 8 | int8_of(q[4 * k + 2]) << 16 |
-                 int8_of(q[4 * k + 3]) << 24;
-      }
-      uint8_t* y = reinterpret_cast<uint8_t*>(a.y) + row * a.D + c;
-      if (!PART && c == v0) {
-        struct __attribute__((packed, aligned(1))) Raw {
-          uint32_t u[2];
-        };
-        *reinterpret_cast<Raw*>(y) = Raw{{b[0], b[1]}};
-      } else {  // what the vector repeats may belong to another scale
-        for (int e = v0 - c; e < min(8, a.D); ++e) y[e] = (uint8_t)(b[e >> 2] >> (8 * (e & 3)));
-      }
-    }
-  }
+  quantise_row<NT, VPT, PART>(f, row, tid, a.D, a.quant, a.group, reinterpret_cast<uint8_t*>(a.y),
+                              a.scale, lds);
 }
 
 // With u = h rstd (the unit row) and du = w dy:
@@ -450,6 +271,12 @@ NormArgs args_of(const gdr_norm_problem* p) {
 
 }  // namespace
 
+void launch_reduce_rows(const float* part, int rows, int cols, void* out, int dtype,
+                        hipStream_t st) {
+  GDR_LAUNCH("norm_reduce", norm_reduce_kernel, dim3((cols + 15) / 16), dim3(256), st, part, rows,
+             cols, out, dtype);
+}
+
 gdr_status launch_norm_fwd(const gdr_norm_problem* p, const void* x, const void* res,
                            const void* weight, void* y, void* scale, void* h, float* rstd,
                            hipStream_t st) {
@@ -495,8 +322,7 @@ gdr_status launch_norm_bwd(const gdr_norm_problem* p, const void* dy, const void
                  dim3(block_of<NT>()), st, a);
     });
   });
-  GDR_LAUNCH("norm_reduce", norm_reduce_kernel, dim3((p->D + 15) / 16), dim3(256), st, a.part,
-             a.blocks, p->D, dw, (int)p->w_dtype);
+  launch_reduce_rows(a.part, a.blocks, p->D, dw, (int)p->w_dtype, st);
   return launch_status("norm_bwd");
 }
 

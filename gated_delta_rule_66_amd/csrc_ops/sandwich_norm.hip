@@ -1,0 +1,412 @@
+// sandwich_norm.hip -- from one block to the next on gfx950: the norm of a
+// block's output, its gate, the residual scale, the residual's addition and
+// the next block's norm in one pass,
+//   n = w1 u(x)  (x without w1),   h = residual + alpha s act(g) n,
+//   y = w2 u(h),                   u(v) = v / sqrt(mean v^2 + eps)
+// with h rounded to the residual's type before it is normalised; y in the
+// input's type or in 8 bits; and the gradient.
+//
+// Memory bounds it: a row of every operand stays in the registers of the row's
+// threads from its load to its stores, so each is touched once.
+#include <algorithm>
+
+#include "norm_device.h"
+
+namespace gdr {
+
+namespace {
+
+struct SandwichArgs {
+  const void* x;
+  const void* res;
+  const void* gate;    // nullable
+  const void* post;    // w1, nullable
+  const void* scale;   // s, nullable
+  const void* pre;     // w2
+  void* y;
+  float* q_scale;
+  void* h;
+  float* rstd_x;       // nullable in the forward
+  float* rstd_h;
+  int64_t x_stride, gate_stride;
+  int rows, D, wdt, act, quant, group;
+  float eps, alpha;
+  // backward
+  const void* dy;
+  const void* dh;      // nullable
+  void* dx;
+  void* dres;
+  void* dgate;
+  float* part;         // [2][blocks][D]: dw2, and what dw1 and ds come from
+  int blocks;
+};
+
+// One over the root of the row's mean square, in 64 bits as the norm without a
+// gate has it.  `v0` excludes what a moved-back vector repeats.
+template <int NT, int VPT, bool PART>
+__device__ __forceinline__ float row_rstd(const float (&f)[VPT][8], int tid, int D, float eps,
+                                          float* lds) {
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, D);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double v = c + e >= v0 ? f[i][e] : 0.f;
+      sum = __builtin_fma(v, v, sum);
+    }
+  }
+  sum = row_sum<NT>(sum, reinterpret_cast<double*>(lds));
+  return (float)(1.0 / __builtin_sqrt(sum / D + (double)eps));
+}
+
+// The forward.
+template <typename T, typename R, bool QUANT, int NT, int VPT, bool PART>
+__global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichArgs a) {
+  __shared__ __align__(8) float lds[32];
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int64_t row = NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  if (row >= a.rows) return;  // a whole wave; the barriers below are for NT > 64 only
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
+  const T* gate = reinterpret_cast<const T*>(a.gate) + row * a.gate_stride;
+  const R* res = reinterpret_cast<const R*>(a.res) + row * a.D;
+  R* h = reinterpret_cast<R*>(a.h) + row * a.D;
+  float f[VPT][8], r[VPT][8], g[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = column_of<PART>(i * NT + tid, a.D);
+    load8<T, PART>(x + c, a.D, f[i]);
+    load8<R, PART>(res + c, a.D, r[i]);
+    if (a.gate) load8<T, PART>(gate + c, a.D, g[i]);
+  }
+  if (a.post) {
+    const float rstd = row_rstd<NT, VPT, PART>(f, tid, a.D, a.eps, lds);
+    if (a.rstd_x && tid == 0) a.rstd_x[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float w[8];
+      load_weight<PART>(a.post, column_of<PART>(i * NT + tid, a.D), a.D, a.wdt, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * rstd * w[e];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+    if (a.gate) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] *= gate_of(g[i][e], a.act);
+    }
+    if (a.scale) {
+      float s[8];
+      load_weight<PART>(a.scale, c, a.D, a.wdt, s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] *= s[e];
+    }
+    // the norm is of the stored stream, so that the gradient, which reads it,
+    // is the gradient of what was computed
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      f[i][e] = to_f(from_f<R>(__builtin_fmaf(f[i][e], a.alpha, r[i][e])));
+    if (v0 < a.D) store8<R, PART>(h + c, a.D, f[i]);
+  }
+  const float rstd = row_rstd<NT, VPT, PART>(f, tid, a.D, a.eps, lds);
+  if (a.rstd_h && tid == 0) a.rstd_h[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+    float w[8];
+    load_weight<PART>(a.pre, c, a.D, a.wdt, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * rstd * w[e];
+    if (!QUANT && v0 < a.D)
+      store8<T, PART>(reinterpret_cast<T*>(a.y) + row * a.D + c, a.D, f[i]);
+  }
+  if (QUANT)
+    quantise_row<NT, VPT, PART>(f, row, tid, a.D, a.quant, a.group,
+                                reinterpret_cast<uint8_t*>(a.y), a.q_scale, lds);
+}
+
+// The gradient.  With the unit rows uh of h and ux of x (x itself without w1),
+// A = act(g):
+//   dH = dh + rh (dy w2 - uh mean(dy w2 uh)) = dresidual,   dw2 = sum dy uh
+//   P = sum dH A ux,   dw1 = alpha s P,   ds = alpha w1 P
+//   dg = dH alpha s w1 ux A',   du = dH alpha s A w1
+//   dx = rx (du - ux mean(du ux))     (du without w1)
+// A block walks rows blockIdx.x, + blocks, ... with dw2 and P in registers and
+// leaves its sums in `part`.
+template <typename T, typename R, int NT, int VPT, bool PART>
+__global__ __launch_bounds__(block_of<NT>()) void sandwich_bwd_kernel(SandwichArgs a) {
+  constexpr int RPB = NT == 64 ? 4 : 1;
+  constexpr int COLS = NT * VPT * 8;
+  __shared__ float lds[16];
+  __shared__ float wsum[NT == 64 ? 4 * COLS : 1];
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int q = NT == 64 ? (threadIdx.x >> 6) : 0;
+  float dw[VPT][8], P[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = P[i][e] = 0.f;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + q; row < a.rows; row += (int64_t)a.blocks * RPB) {
+    const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
+    const T* gate = reinterpret_cast<const T*>(a.gate) + row * a.gate_stride;
+    const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.D;
+    const R* h = reinterpret_cast<const R*>(a.h) + row * a.D;
+    const R* dh = reinterpret_cast<const R*>(a.dh) + row * a.D;
+    const float rh = a.rstd_h[row], rx = a.post ? a.rstd_x[row] : 1.f;
+    float u[VPT][8], d[VPT][8], g[VPT][8], ux[VPT][8], s[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = column_of<PART>(i * NT + tid, a.D);
+      load8<R, PART>(h + c, a.D, u[i]);
+      load8<T, PART>(dy + c, a.D, d[i]);
+      load8<T, PART>(x + c, a.D, ux[i]);
+      if (a.gate) load8<T, PART>(gate + c, a.D, s[i]);
+      if (a.dh) {
+        load8<R, PART>(dh + c, a.D, g[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] = 0.f;
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+      float w[8];
+      load_weight<PART>(a.pre, c, a.D, a.wdt, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u[i][e] *= rh;
+        dw[i][e] += d[i][e] * u[i][e];
+        d[i][e] *= w[e];
+        dot += c + e >= v0 ? d[i][e] * u[i][e] : 0.f;
+      }
+    }
+    dot = row_reduce<NT, false>(dot, lds) / (float)a.D;
+    float dot2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+      float w[8], sc[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.f, sc[e] = a.alpha;
+      if (a.post) load_weight<PART>(a.post, c, a.D, a.wdt, w);
+      if (a.scale) {
+        load_weight<PART>(a.scale, c, a.D, a.wdt, sc);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sc[e] *= a.alpha;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[i][e] += rh * (d[i][e] - u[i][e] * dot);
+      if (v0 < a.D)
+        store8<R, PART>(reinterpret_cast<R*>(a.dres) + row * a.D + c, a.D, g[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const Gate t = a.gate ? gate_and_slope(s[i][e], a.act) : Gate{1.f, 0.f};
+        ux[i][e] *= rx;
+        const float b = g[i][e] * ux[i][e];
+        P[i][e] += b * t.value;
+        s[i][e] = b * sc[e] * w[e] * t.slope;
+        d[i][e] = g[i][e] * sc[e] * t.value * w[e];
+        dot2 += c + e >= v0 ? d[i][e] * ux[i][e] : 0.f;
+      }
+      if (a.gate && v0 < a.D)
+        store8<T, PART>(reinterpret_cast<T*>(a.dgate) + row * a.D + c, a.D, s[i]);
+    }
+    if (a.post) {
+      dot2 = row_reduce<NT, false>(dot2, lds) / (float)a.D;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[i][e] = rx * (d[i][e] - ux[i][e] * dot2);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if ((i * NT + tid) * 8 < a.D)
+        store8<T, PART>(reinterpret_cast<T*>(a.dx) + row * a.D +
+                            column_of<PART>(i * NT + tid, a.D), a.D, d[i]);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* part = a.part + ((int64_t)k * a.blocks + blockIdx.x) * a.D;
+    if (NT > 64) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if ((i * NT + tid) * 8 < a.D)
+          store8<float, PART>(part + column_of<PART>(i * NT + tid, a.D), a.D, k ? P[i] : dw[i]);
+    } else {
+      // columns of the block's four rows, each at its vector's place
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          wsum[q * COLS + (i * 64 + tid) * 8 + e] = k ? P[i][e] : dw[i][e];
+      __syncthreads();
+      for (int j = threadIdx.x; j < ((a.D + 7) / 8) * 8; j += 256) {
+        const int c = column_of<PART>(j / 8, a.D) + j % 8;
+        if (c < a.D)
+          part[c] = (wsum[j] + wsum[(NT == 64 ? 1 : 0) * COLS + j]) +
+                    (wsum[(NT == 64 ? 2 : 0) * COLS + j] + wsum[(NT == 64 ? 3 : 0) * COLS + j]);
+      }
+    }
+  }
+}
+
+// The parameters' gradients over the blocks, 16 columns by 16 shares of the
+// blocks: dw2 (blockIdx.y 0), and dw1 and ds from P.
+__global__ __launch_bounds__(256) void sandwich_reduce_kernel(SandwichArgs a, void* dpost,
+                                                              void* dscale, void* dpre) {
+  __shared__ float red[16][17];
+  const int l = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + l;
+  const float* part = a.part + (int64_t)blockIdx.y * a.blocks * a.D;
+  float s = 0.f;
+  if (c < a.D)
+#pragma unroll 8
+    for (int b = q; b < a.blocks; b += 16) s += part[(int64_t)b * a.D + c];
+  red[q][l] = s;
+  __syncthreads();
+  if (q || c >= a.D) return;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += red[i][l];
+  if (blockIdx.y == 0) {
+    store_scalar(dpre, c, a.wdt, s);
+    return;
+  }
+  s *= a.alpha;
+  if (dpost) store_scalar(dpost, c, a.wdt, a.scale ? s * load_scalar(a.scale, c, a.wdt) : s);
+  if (dscale) store_scalar(dscale, c, a.wdt, a.post ? s * load_scalar(a.post, c, a.wdt) : s);
+}
+
+#define GDR_W(NT, VPT) \
+  if (nv <= NT * VPT)  \
+  return f(std::integral_constant<int, NT>(), std::integral_constant<int, VPT>(), whole)
+// Threads per row and 8-element steps per thread, as the norm without a gate
+// has them up to its 16,384 columns.
+template <typename F>
+void by_width(int D, F f) {
+  const int nv = (D + 7) / 8;
+  const std::false_type whole;
+  if (D < 8)
+    return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>(), std::true_type());
+  GDR_W(64, 1);
+  GDR_W(64, 2);
+  GDR_W(256, 1);
+  GDR_W(256, 2);
+  GDR_W(256, 4);
+  GDR_W(256, 8);
+}
+// The gradient holds seven arrays of a row: at most two steps a thread.
+template <typename F>
+void by_width_bwd(int D, F f) {
+  const int nv = (D + 7) / 8;
+  const std::false_type whole;
+  if (D < 8)
+    return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>(), std::true_type());
+  GDR_W(64, 1);
+  GDR_W(64, 2);
+  GDR_W(256, 1);
+  GDR_W(256, 2);
+  GDR_W(512, 2);
+  GDR_W(1024, 2);
+}
+#undef GDR_W
+
+// The input's and the residual's types.
+template <typename F>
+void by_type(const gdr_sandwich_norm_problem* p, F f) {
+  auto res = [&](auto t) {
+    if (p->res_dtype == GDR_FP32) f(t, float());
+    else f(t, t);
+  };
+  if (p->dtype == GDR_BF16) res(__bf16());
+  else if (p->dtype == GDR_FP16) res(_Float16());
+  else f(float(), float());
+}
+
+int bwd_blocks(const gdr_sandwich_norm_problem* p) {
+  // as the norm without a gate: at least 8 rows a block, at most 1024 blocks
+  const int rpb = p->D <= 1024 ? 4 : 1;
+  const int64_t want = ((int64_t)p->rows + 8 * rpb - 1) / (8 * rpb);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(want, 1024));
+}
+
+SandwichArgs args_of(const gdr_sandwich_norm_problem* p) {
+  SandwichArgs a{};
+  a.x_stride = p->x_stride;
+  a.gate_stride = p->gate_stride;
+  a.rows = p->rows;
+  a.D = p->D;
+  a.wdt = (int)p->w_dtype;
+  a.act = p->activation;
+  a.quant = p->quant;
+  a.group = p->group_size;
+  a.eps = p->eps;
+  a.alpha = p->alpha;
+  return a;
+}
+
+}  // namespace
+
+gdr_status launch_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const void* x,
+                                    const void* residual, const void* gate, const void* post,
+                                    const void* res_scale, const void* pre, void* y, float* scale,
+                                    void* h, float* rstd_x, float* rstd_h, hipStream_t st) {
+  SandwichArgs a = args_of(p);
+  a.x = x; a.res = residual; a.gate = gate; a.post = post; a.scale = res_scale; a.pre = pre;
+  a.y = y; a.q_scale = scale; a.h = h; a.rstd_x = rstd_x; a.rstd_h = rstd_h;
+  by_type(p, [&](auto t, auto r) {
+    using T = decltype(t);
+    using R = decltype(r);
+    by_width(p->D, [&](auto nt, auto vpt, auto part) {
+      constexpr int NT = nt.value, VPT = vpt.value;
+      const dim3 grid((unsigned)(NT == 64 ? (p->rows + 3) / 4 : p->rows));
+      const dim3 block(block_of<NT>());
+      if (p->quant)
+        GDR_LAUNCH("sandwich_fwd", (sandwich_fwd_kernel<T, R, true, NT, VPT, part.value>), grid,
+                   block, st, a);
+      else
+        GDR_LAUNCH("sandwich_fwd", (sandwich_fwd_kernel<T, R, false, NT, VPT, part.value>), grid,
+                   block, st, a);
+    });
+  });
+  return launch_status("sandwich_norm_fwd");
+}
+
+size_t sandwich_norm_bwd_workspace(const gdr_sandwich_norm_problem* p) {
+  return align256((size_t)2 * bwd_blocks(p) * p->D * sizeof(float));
+}
+
+gdr_status launch_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const void* dy,
+                                    const void* dh, const void* x, const void* h, const void* gate,
+                                    const void* post, const void* res_scale, const void* pre,
+                                    const float* rstd_x, const float* rstd_h, void* dx,
+                                    void* dresidual, void* dgate, void* dpost, void* dscale,
+                                    void* dpre, void* ws, hipStream_t st) {
+  SandwichArgs a = args_of(p);
+  a.x = x; a.gate = gate; a.post = post; a.scale = res_scale; a.pre = pre;
+  a.h = const_cast<void*>(h);
+  a.rstd_x = const_cast<float*>(rstd_x);
+  a.rstd_h = const_cast<float*>(rstd_h);
+  a.dy = dy; a.dh = dh; a.dx = dx; a.dres = dresidual; a.dgate = dgate;
+  a.part = reinterpret_cast<float*>(ws);
+  a.blocks = bwd_blocks(p);
+  by_type(p, [&](auto t, auto r) {
+    using T = decltype(t);
+    using R = decltype(r);
+    by_width_bwd(p->D, [&](auto nt, auto vpt, auto part) {
+      constexpr int NT = nt.value, VPT = vpt.value;
+      GDR_LAUNCH("sandwich_bwd", (sandwich_bwd_kernel<T, R, NT, VPT, part.value>), dim3(a.blocks),
+                 dim3(block_of<NT>()), st, a);
+    });
+  });
+  GDR_LAUNCH("sandwich_reduce", sandwich_reduce_kernel,
+             dim3((p->D + 15) / 16, dpost || dscale ? 2 : 1), dim3(256), st, a, dpost, dscale, dpre);
+  return launch_status("sandwich_norm_bwd");
+}
+
+}  // namespace gdr

@@ -394,8 +394,10 @@ int gdr_profile_read(char* names, size_t name_stride, double* total_ms, int* lau
 
 /* ==== The operators around the recurrence in a layer =======================
  * The short causal convolution in front of it, the selective state space scan
- * (its sibling with one decay per head and no delta term) and the RMS norm
- * with the residual's addition.  The conventions above hold: the caller owns
+ * (its sibling with one decay per head and no delta term), the RMS norm with
+ * the residual's addition; and at the layer's ends the norm of the output with
+ * its gate, the norms on both sides of the residual's addition, rows in 8 bits
+ * and their product.  The conventions above hold: the caller owns
  * buffers and streams, every argument is validated on the host before any HIP
  * call, nothing is allocated or kept, results are deterministic.  Two calls
  * may run at once on different streams if they share no output or workspace.
@@ -580,6 +582,142 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_problem* p, const void* dy, const voi
                             const void* weight, const float* rstd, const void* dh, void* dx,
                             void* dresidual, void* dweight, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/* ---- root-mean-square norm with a gate ----
+ * Of a recurrence's output, over each group of norm_size consecutive columns
+ * (a head).  With u(v) = v / sqrt(mean(v^2) + eps) over the group:
+ *     y = weight u(x) act(gate), or weight u(x act(gate)) with gate_first
+ * in dtype, or quantised as gdr_rms_norm_fwd does it, with a scale per row or
+ * per 128 columns of the row of all groups.
+ *   x, gate, y, dy, dx, dgate [rows, D] dtype (x and gate with a row stride);
+ *   weight, dweight [D] w_dtype, or [norm_size] with shared_weight; q [rows, D]
+ *   8 bits; scale [rows] or [rows, ceil(D / 128)] fp32; rstd [rows, D /
+ *   norm_size] fp32
+ * D <= 16384, a multiple of norm_size.  An infinite gate has silu's and the
+ * sigmoid's limit; a NaN or an infinity in x reaches its group only, and in 8
+ * bits what its scale covers. */
+typedef struct {
+  int32_t rows, D, norm_size;
+  gdr_dtype dtype;                /* bf16, fp16 or fp32 */
+  gdr_dtype w_dtype;              /* dtype or GDR_FP32 */
+  int32_t shared_weight;          /* 1: weight [norm_size], for every group */
+  int32_t gate_first;
+  int32_t activation;             /* 1: silu, 2: sigmoid */
+  int32_t quant;                  /* 0: y in dtype, 1: e4m3, 2: int8 */
+  int32_t scale_group;            /* columns per scale: 0 = the row, or 128 */
+  float eps;                      /* finite, >= 0 */
+  int64_t x_stride, gate_stride;  /* elements between rows, >= D */
+} gdr_gated_norm_problem;
+
+gdr_status gdr_gated_norm_check(const gdr_gated_norm_problem* p, char* reason, size_t reason_len);
+
+/*   in : x, gate, weight
+ *   out: y (q when quantised); scale (iff quantised); rstd (nullable, not when
+ *        quantised: one over the root of each group's mean square, which the
+ *        gradient takes) */
+gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x, const void* gate,
+                              const void* weight, void* y, float* scale, float* rstd,
+                              void* stream);
+
+/* The gradient (quant = 0).  in: dy and the forward's x, gate, weight, rstd;
+ * out: dx, dgate, dweight (a sum over the rows in a fixed order). */
+size_t gdr_gated_norm_bwd_workspace_size(const gdr_gated_norm_problem* p);
+gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem* p, const void* dy, const void* x,
+                              const void* gate, const void* weight, const float* rstd, void* dx,
+                              void* dgate, void* dweight, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* ---- the norms on both sides of a residual's addition ----
+ * From a block's output x to the next block's input, with u as above over the
+ * row:
+ *     n = post_weight u(x)                     (x without post_weight)
+ *     h = residual + alpha res_scale act(gate) n, rounded to res_dtype
+ *     y = pre_weight u(h)
+ * (a factor that is not given is 1), y in dtype or quantised as
+ * gdr_rms_norm_fwd does it.
+ *   x, gate, y, dy, dx, dgate [rows, D] dtype (x and gate with a row stride);
+ *   residual, h, dh, dresidual [rows, D] res_dtype; post_weight, res_scale,
+ *   pre_weight and their gradients [D] w_dtype; q, scale as for
+ *   gdr_rms_norm_fwd; rstd_x, rstd_h [rows] fp32
+ * D <= 16384. */
+typedef struct {
+  int32_t rows, D;
+  gdr_dtype dtype;                /* bf16, fp16 or fp32 */
+  gdr_dtype res_dtype;            /* dtype or GDR_FP32 */
+  gdr_dtype w_dtype;              /* dtype or GDR_FP32 */
+  int32_t activation;             /* of the gate; 0: none, 1: silu, 2: sigmoid */
+  int32_t quant;                  /* 0: y in dtype, 1: e4m3, 2: int8 */
+  int32_t group_size;             /* columns per scale: 0 = the row, or 128 */
+  float eps;                      /* finite, >= 0 */
+  float alpha;                    /* finite */
+  int64_t x_stride, gate_stride;  /* elements between rows, >= D */
+} gdr_sandwich_norm_problem;
+
+gdr_status gdr_sandwich_norm_check(const gdr_sandwich_norm_problem* p, char* reason,
+                                   size_t reason_len);
+
+/*   in : x, residual, pre_weight; gate, post_weight, res_scale (nullable)
+ *   out: y (q when quantised), h; scale (iff quantised); rstd_x (nullable, only
+ *        with post_weight) and rstd_h (nullable), which the gradient takes */
+gdr_status gdr_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const void* x,
+                                 const void* residual, const void* gate, const void* post_weight,
+                                 const void* res_scale, const void* pre_weight, void* y,
+                                 float* scale, void* h, float* rstd_x, float* rstd_h,
+                                 void* stream);
+
+/* The gradient (quant = 0).
+ *   in : dy; dh (nullable = zero): the gradient of the stored h; the forward's
+ *        x, h, gate, post_weight, res_scale, pre_weight, rstd_x (iff
+ *        post_weight), rstd_h
+ *   out: dx, dresidual, dpre_weight; dgate (iff gate); dpost_weight and
+ *        dres_scale (each nullable = not written, and only with its input) */
+size_t gdr_sandwich_norm_bwd_workspace_size(const gdr_sandwich_norm_problem* p);
+gdr_status gdr_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const void* dy, const void* dh,
+                                 const void* x, const void* h, const void* gate,
+                                 const void* post_weight, const void* res_scale,
+                                 const void* pre_weight, const float* rstd_x, const float* rstd_h,
+                                 void* dx, void* dresidual, void* dgate, void* dpost_weight,
+                                 void* dres_scale, void* dpre_weight, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ---- rows to 8 bits ----
+ * q and scale of x as gdr_rms_norm_fwd forms them of its y: weights as they are
+ * loaded (a scale per channel), activations that come from no norm.  An
+ * infinity makes its scale infinite and what the scale covers 0 (itself NaN in
+ * e4m3); a NaN makes its scale NaN.
+ *   x [rows, D] dtype with a row stride; q [rows, D] 8 bits; scale [rows] or
+ *   [rows, ceil(D / 128)] fp32.   D <= 65536. */
+typedef struct {
+  int32_t rows, D;
+  gdr_dtype dtype;                /* bf16, fp16 or fp32 */
+  int32_t quant;                  /* 1: e4m3, 2: int8 */
+  int32_t group_size;             /* columns per scale: 0 = the row, or 128 */
+  int64_t x_stride;               /* elements between rows, >= D */
+} gdr_quantize_problem;
+
+gdr_status gdr_quantize_check(const gdr_quantize_problem* p, char* reason, size_t reason_len);
+gdr_status gdr_quantize_rows(const gdr_quantize_problem* p, const void* x, void* q, float* scale,
+                             void* stream);
+
+/* ---- product of 8-bit integers ----
+ *     y[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] weight[n][k] + bias[n]
+ * a projection of tokens quantised with a scale each by a weight quantised
+ * with a scale per channel.  The sums are exact; a scale or bias that is no
+ * number reaches its token or channel only.
+ *   x [M, K] int8 with a token stride; weight [N, K] int8; x_scale [M],
+ *   w_scale [N] fp32; bias [N] bias_dtype (nullable); y [M, N] out_dtype
+ * K <= 65536. */
+typedef struct {
+  int32_t M, N, K;
+  gdr_dtype out_dtype;            /* bf16, fp16 or fp32 */
+  gdr_dtype bias_dtype;           /* out_dtype or GDR_FP32 */
+  int64_t x_stride;               /* bytes between tokens, K to 2^22 */
+} gdr_int8_matmul_problem;
+
+gdr_status gdr_int8_matmul_check(const gdr_int8_matmul_problem* p, char* reason, size_t reason_len);
+gdr_status gdr_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, const float* x_scale,
+                           const void* weight, const float* w_scale, const void* bias, void* y,
+                           void* stream);
 
 #ifdef __cplusplus
 }

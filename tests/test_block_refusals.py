@@ -1,0 +1,247 @@
+"""Refusals of the operators at a layer's ends on the host (no GPU): every
+argument is checked before any HIP call."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_66_amd as gdr
+from gated_delta_rule_66_amd import _lib
+from gated_delta_rule_66_amd._lib import (GDR_BF16, GDR_FP16, GDR_FP32, GatedNormProblem,
+                                          Int8MatmulProblem, QuantizeProblem, SandwichNormProblem, lib)
+
+FAKE = 0x1000  # never dereferenced: validation happens on the host
+
+
+def gated(**kw):
+    base = dict(rows=4, D=256, norm_size=128, dtype=GDR_BF16, w_dtype=GDR_FP32, shared_weight=1,
+                gate_first=0, activation=1, quant=0, scale_group=0, eps=1e-6, x_stride=256,
+                gate_stride=300)
+    return GatedNormProblem(**{**base, **kw})
+
+
+def sandwich(**kw):
+    base = dict(rows=4, D=40, dtype=GDR_BF16, res_dtype=GDR_FP32, w_dtype=GDR_BF16, activation=2,
+                quant=0, group_size=0, eps=1e-6, alpha=1.0, x_stride=40, gate_stride=40)
+    return SandwichNormProblem(**{**base, **kw})
+
+
+def quantize(**kw):
+    base = dict(rows=4, D=40, dtype=GDR_BF16, quant=2, group_size=0, x_stride=40)
+    return QuantizeProblem(**{**base, **kw})
+
+
+def matmul(**kw):
+    base = dict(M=4, N=8, K=64, out_dtype=GDR_BF16, bias_dtype=GDR_FP32, x_stride=64)
+    return Int8MatmulProblem(**{**base, **kw})
+
+
+CHECK = {GatedNormProblem: lib.gdr_gated_norm_check, SandwichNormProblem: lib.gdr_sandwich_norm_check,
+         QuantizeProblem: lib.gdr_quantize_check, Int8MatmulProblem: lib.gdr_int8_matmul_check}
+WORKSPACE = {GatedNormProblem: lib.gdr_gated_norm_bwd_workspace_size,
+             SandwichNormProblem: lib.gdr_sandwich_norm_bwd_workspace_size}
+
+
+def verdict(p):
+    reason = ctypes.create_string_buffer(256)
+    return _lib.STATUS[CHECK[type(p)](ctypes.byref(p), reason, 256)], reason.value.decode()
+
+
+BAD = [
+    (gated(rows=0), "GDR_ERR_SHAPE", "positive"),
+    (gated(D=0, x_stride=0), "GDR_ERR_SHAPE", "positive"),
+    (gated(D=16512, x_stride=16512, gate_stride=16512), "GDR_ERR_SHAPE", "16384"),
+    (gated(norm_size=0), "GDR_ERR_SHAPE", "multiple"),
+    (gated(norm_size=100), "GDR_ERR_SHAPE", "multiple"),
+    (gated(norm_size=-128), "GDR_ERR_SHAPE", "multiple"),
+    (gated(norm_size=512), "GDR_ERR_SHAPE", "multiple"),
+    (gated(rows=1 << 28), "GDR_ERR_SHAPE", "rows"),
+    (gated(rows=1 << 20, norm_size=2), "GDR_ERR_SHAPE", "groups"),
+    (gated(rows=1 << 25, D=12, norm_size=12, x_stride=12), "GDR_ERR_SHAPE", "groups"),
+    (gated(x_stride=255), "GDR_ERR_SHAPE", "x_stride"),
+    (gated(gate_stride=255), "GDR_ERR_SHAPE", "gate_stride"),
+    (gated(dtype=5), "GDR_ERR_DTYPE", "x must"),
+    (gated(w_dtype=GDR_FP16), "GDR_ERR_DTYPE", "weight"),
+    (gated(shared_weight=2), "GDR_ERR_ARG", "shared"),
+    (gated(gate_first=-1), "GDR_ERR_ARG", "gate_first"),
+    (gated(activation=0), "GDR_ERR_ARG", "activation"),
+    (gated(activation=3), "GDR_ERR_ARG", "activation"),
+    (gated(quant=3), "GDR_ERR_ARG", "quant"),
+    (gated(quant=1, scale_group=64), "GDR_ERR_ARG", "scale"),
+    (gated(scale_group=128), "GDR_ERR_ARG", "quantised"),
+    (gated(eps=-1.0), "GDR_ERR_ARG", "eps"),
+    (gated(eps=float("nan")), "GDR_ERR_ARG", "eps"),
+    (sandwich(rows=-1), "GDR_ERR_SHAPE", "positive"),
+    (sandwich(D=16385, x_stride=16385, gate_stride=16385), "GDR_ERR_SHAPE", "16384"),
+    (sandwich(rows=1 << 28), "GDR_ERR_SHAPE", "rows"),
+    (sandwich(x_stride=39), "GDR_ERR_SHAPE", "x_stride"),
+    (sandwich(gate_stride=39), "GDR_ERR_SHAPE", "gate_stride"),
+    (sandwich(dtype=-1), "GDR_ERR_DTYPE", "x must"),
+    (sandwich(res_dtype=GDR_FP16), "GDR_ERR_DTYPE", "residual"),
+    (sandwich(w_dtype=GDR_FP16), "GDR_ERR_DTYPE", "weights"),
+    (sandwich(activation=3), "GDR_ERR_ARG", "activation"),
+    (sandwich(quant=-1), "GDR_ERR_ARG", "quant"),
+    (sandwich(group_size=128), "GDR_ERR_ARG", "quantised"),
+    (sandwich(eps=float("inf")), "GDR_ERR_ARG", "eps"),
+    (sandwich(alpha=float("nan")), "GDR_ERR_ARG", "alpha"),
+    (quantize(rows=0), "GDR_ERR_SHAPE", "positive"),
+    (quantize(D=65537, x_stride=65537), "GDR_ERR_SHAPE", "65536"),
+    (quantize(x_stride=39), "GDR_ERR_SHAPE", "x_stride"),
+    (quantize(dtype=9), "GDR_ERR_DTYPE", "x must"),
+    (quantize(quant=0), "GDR_ERR_ARG", "quant"),
+    (quantize(group_size=32), "GDR_ERR_ARG", "scale"),
+    (matmul(M=0), "GDR_ERR_SHAPE", "positive"),
+    (matmul(N=-5), "GDR_ERR_SHAPE", "positive"),
+    (matmul(K=0, x_stride=0), "GDR_ERR_SHAPE", "positive"),
+    (matmul(K=65537, x_stride=65537), "GDR_ERR_SHAPE", "65536"),
+    (matmul(M=(1 << 31) - 1, N=128), "GDR_ERR_SHAPE", "too large"),
+    (matmul(M=1 << 20, N=1 << 18), "GDR_ERR_SHAPE", "too large"),
+    (matmul(N=(1 << 26) + 1), "GDR_ERR_SHAPE", "too large"),
+    (matmul(x_stride=63), "GDR_ERR_SHAPE", "x_stride"),
+    (matmul(x_stride=(1 << 22) + 1), "GDR_ERR_SHAPE", "x_stride"),
+    (matmul(out_dtype=3), "GDR_ERR_DTYPE", "output"),
+    (matmul(bias_dtype=GDR_FP16), "GDR_ERR_DTYPE", "bias"),
+]
+
+
+@pytest.mark.parametrize("p", [gated(), gated(quant=2, scale_group=128), gated(dtype=GDR_FP32, D=16384,
+                               norm_size=16384, x_stride=16384, gate_stride=16384),
+                               sandwich(), sandwich(quant=1, D=16384, x_stride=16384, gate_stride=1 << 40),
+                               quantize(), quantize(D=65536, x_stride=65536, quant=1), matmul(),
+                               matmul(M=1 << 20, N=1 << 17), matmul(K=65536, x_stride=1 << 22)])
+def test_accepted(p):
+    assert verdict(p) == ("GDR_OK", "")
+
+
+@pytest.mark.parametrize("p,status,msg", BAD)
+def test_rejections(p, status, msg):
+    st, reason = verdict(p)
+    assert st == status and msg in reason and msg in lib.gdr_last_error().decode(), (st, reason)
+    if type(p) in WORKSPACE:
+        assert WORKSPACE[type(p)](ctypes.byref(p)) == 0
+
+
+def test_null_problems():
+    for f in CHECK.values():
+        assert _lib.STATUS[f(None, None, 0)] == "GDR_ERR_NULL"
+
+
+def test_pointers_and_workspaces():
+    p = ctypes.byref(gated())
+    ok = [FAKE] * 4 + [None, FAKE]                 # x, gate, weight, y, scale, rstd
+    for at in range(4):
+        a = list(ok)
+        a[at] = None
+        assert lib.gdr_gated_norm_fwd(p, *a, None) == 1
+    assert lib.gdr_gated_norm_fwd(p, *ok[:4], FAKE, FAKE, None) == 1          # scales of nothing
+    assert lib.gdr_gated_norm_fwd(ctypes.byref(gated(quant=1)), *ok, None) == 1
+    assert lib.gdr_gated_norm_fwd(ctypes.byref(gated(quant=1)), *ok[:4], FAKE, FAKE, None) == 10
+    n = lib.gdr_gated_norm_bwd_workspace_size(p)
+    assert n >= 256 * 4
+    for at in range(8):
+        a = [FAKE] * 8
+        a[at] = None
+        assert lib.gdr_gated_norm_bwd(p, *a, FAKE, n, None) == 1
+    assert lib.gdr_gated_norm_bwd(p, *[FAKE] * 8, FAKE, n - 1, None) == 7
+    assert lib.gdr_gated_norm_bwd(p, *[FAKE] * 8, None, n, None) == 7
+    assert lib.gdr_gated_norm_bwd(ctypes.byref(gated(quant=2)), *[FAKE] * 8, FAKE, n, None) == 10
+
+    p = ctypes.byref(sandwich())
+    # x, residual, gate, post, scale, pre, y, q_scale, h, rstd_x, rstd_h
+    ok = [FAKE, FAKE, None, None, None, FAKE, FAKE, None, 2 * FAKE, None, FAKE]
+    for at in (0, 1, 5, 6, 8):
+        a = list(ok)
+        a[at] = None
+        assert lib.gdr_sandwich_norm_fwd(p, *a, None) == 1
+    for at, v, code in ((7, FAKE, 1), (9, FAKE, 10), (8, FAKE, 10)):
+        a = list(ok)
+        a[at] = v
+        assert lib.gdr_sandwich_norm_fwd(p, *a, None) == code
+    n = lib.gdr_sandwich_norm_bwd_workspace_size(p)
+    assert n >= 2 * 40 * 4
+    # dy, dh, x, h, gate, post, scale, pre, rstd_x, rstd_h, dx, dres, dgate, dpost, dscale, dpre
+    ok = [FAKE, None, FAKE, FAKE, None, None, None, FAKE, None, FAKE, FAKE, FAKE, None, None, None, FAKE]
+
+    def call(at=None, v=None, ws=FAKE, size=n, q=p):
+        a = list(ok)
+        if at is not None:
+            a[at] = v
+        return lib.gdr_sandwich_norm_bwd(q, *a, ws, size, None)
+
+    for at in (0, 2, 3, 7, 9, 10, 11, 15):
+        assert call(at) == 1
+    assert call(4, FAKE) == 1 and call(12, FAKE) == 1                          # dgate with gate
+    assert call(5, FAKE) == 1 and call(8, FAKE) == 1                           # rstd_x with post_weight
+    assert call(13, FAKE) == 10 and call(14, FAKE) == 10
+    assert call(size=n - 1) == 7 and call(ws=None) == 7
+    assert call(q=ctypes.byref(sandwich(quant=1))) == 10
+
+    p = ctypes.byref(quantize())
+    for at in range(3):
+        a = [FAKE] * 3
+        a[at] = None
+        assert lib.gdr_quantize_rows(p, *a, None) == 1
+    p = ctypes.byref(matmul())
+    for at in (0, 1, 2, 3, 5):
+        a = [FAKE] * 6
+        a[at] = None
+        assert lib.gdr_int8_matmul(p, *a, None) == 1
+
+
+def meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+def refused(call, name):
+    with pytest.raises(gdr.GdrError) as e:
+        call()
+    assert e.value.name == name, e.value
+
+
+def test_sizes_beyond_32_bits():
+    BIG = (1 << 32) + 8
+    x, w = meta(BIG, 4), meta(4)
+    refused(lambda: gdr.gated_rms_norm(x, x, w), "GDR_ERR_SHAPE")
+    refused(lambda: gdr.gated_rms_norm_quant(x, x, w), "GDR_ERR_SHAPE")
+    refused(lambda: gdr.sandwich_rms_norm(x, x, w, w), "GDR_ERR_SHAPE")
+    refused(lambda: gdr.sandwich_rms_norm_quant(x, x, w, w), "GDR_ERR_SHAPE")
+    refused(lambda: gdr.quantize_rows(x), "GDR_ERR_SHAPE")
+    q, s = meta(BIG, 16, dtype=torch.int8), meta(BIG, dtype=torch.float32)
+    small, one = meta(4, 16, dtype=torch.int8), meta(4, dtype=torch.float32)
+    refused(lambda: gdr.int8_matmul(q, s, small, one), "GDR_ERR_SHAPE")
+    refused(lambda: gdr.int8_matmul(small, one, q, s), "GDR_ERR_SHAPE")
+
+
+@pytest.mark.parametrize("group", [(1 << 32) + 128, 1 << 32, -1, 64, 127.5, None])
+def test_group_sizes(group):
+    x, w = torch.zeros(2, 512), torch.ones(512)
+    refused(lambda: gdr.quantize_rows(x, group_size=group), "GDR_ERR_ARG")
+    refused(lambda: gdr.gated_rms_norm_quant(x, x, w, group_size=group), "GDR_ERR_ARG")
+    refused(lambda: gdr.sandwich_rms_norm_quant(x, x, w, w, group_size=group), "GDR_ERR_ARG")
+    if group != 64 and not (isinstance(group, int) and group > 0):
+        refused(lambda: gdr.gated_rms_norm(x, x, w, norm_group=group), "GDR_ERR_ARG")
+
+
+def test_arguments_that_need_no_device():
+    x, w = torch.zeros(2, 512), torch.ones(512)
+    for bad in ("gelu", 1, None, "none"):
+        refused(lambda: gdr.gated_rms_norm(x, x, w, activation=bad), "GDR_ERR_ARG")
+    refused(lambda: gdr.sandwich_rms_norm(x, x, w, w, activation="gelu"), "GDR_ERR_ARG")
+    for bad in ("int4", None):
+        refused(lambda: gdr.quantize_rows(x, format=bad), "GDR_ERR_ARG")
+        refused(lambda: gdr.gated_rms_norm_quant(x, x, w, format=bad), "GDR_ERR_ARG")
+        refused(lambda: gdr.sandwich_rms_norm_quant(x, x, w, w, format=bad), "GDR_ERR_ARG")
+    q = torch.zeros(2, 16, dtype=torch.int8)
+    s = torch.zeros(2)
+    refused(lambda: gdr.int8_matmul(q.float(), s, q, s), "GDR_ERR_DTYPE")
+    refused(lambda: gdr.int8_matmul(q, s, q, s, out_dtype=torch.int32), "GDR_ERR_DTYPE")
+    refused(lambda: gdr.int8_matmul(q, s, q[0], s), "GDR_ERR_SHAPE")
+
+
+def test_tensors_on_the_host_are_refused():
+    x, w = torch.zeros(2, 512), torch.ones(512)
+    q, s = torch.zeros(2, 16, dtype=torch.int8), torch.zeros(2)
+    for call in (lambda: gdr.gated_rms_norm(x, x, w), lambda: gdr.gated_rms_norm_quant(x, x, w),
+                 lambda: gdr.sandwich_rms_norm(x, x, w, w), lambda: gdr.sandwich_rms_norm_quant(x, x, None, w),
+                 lambda: gdr.quantize_rows(x), lambda: gdr.int8_matmul(q, s, q, s)):
+        refused(call, "GDR_ERR_DEVICE")
