@@ -322,6 +322,11 @@ def _scales(name, t, shape, device):
     return _like(name, t, shape, (torch.float32,), device)
 
 
+def _moved(t):
+    """A contiguous copy at an address of its own."""
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def int8_matmul(x, x_scale, weight, w_scale, bias=None, out_dtype=torch.bfloat16):
     """Product of 8-bit integers with a scale per token and per channel: y
     ``[..., N]`` in ``out_dtype`` (bf16, fp16 or fp32),
@@ -350,14 +355,17 @@ def int8_matmul(x, x_scale, weight, w_scale, bias=None, out_dtype=torch.bfloat16
     x_scale = _scales("x_scale", x_scale, lead, dev)
     w_scale = _scales("w_scale", w_scale, (N,), dev)
     bias = _like("bias", bias, (N,), (out_dtype, torch.float32), dev)
-    if x.is_contiguous():
-        src, stride = x, K
-    else:
-        src, stride = _rows(x)
-        if stride > 1 << 22:
-            src, stride = x.contiguous(), K
+    src, stride = (x, K) if x.is_contiguous() else _rows(x)
+    # a multiple of 16 bytes from row to row asks for such an address
+    if stride > 1 << 22 or (K % 16 == 0 and stride % 16 == 0 and src.data_ptr() % 16):
+        src, stride = _moved(src), K
+    if K % 16 == 0 and weight.data_ptr() % 16:
+        weight = _moved(weight)
     p = Int8MatmulProblem(M, N, K, out, out if bias is None else _DT[bias.dtype], stride)
+    ref = ctypes.byref(p)
+    n = lib.gdr_int8_matmul_workspace_size(ref) if M > 64 else 0
+    ws = _bytes(n, dev) if n else None
     y = x.new_empty(lead + (N,), dtype=out_dtype)
-    _launch(x, lib.gdr_int8_matmul, ctypes.byref(p), _ptr(src), _ptr(x_scale), _ptr(weight),
-            _ptr(w_scale), _ptr(bias), _ptr(y))
+    _launch(x, lib.gdr_int8_matmul, ref, _ptr(src), _ptr(x_scale), _ptr(weight), _ptr(w_scale),
+            _ptr(bias), _ptr(y), _ptr(ws), n)
     return y

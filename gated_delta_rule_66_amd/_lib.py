@@ -129,7 +129,8 @@ EXPORTS = [
     "gdr_gated_norm_check", "gdr_gated_norm_fwd", "gdr_gated_norm_bwd_workspace_size",
     "gdr_gated_norm_bwd", "gdr_sandwich_norm_check", "gdr_sandwich_norm_fwd",
     "gdr_sandwich_norm_bwd_workspace_size", "gdr_sandwich_norm_bwd", "gdr_quantize_check",
-    "gdr_quantize_rows", "gdr_int8_matmul_check", "gdr_int8_matmul",
+    "gdr_quantize_rows", "gdr_int8_matmul_check",
+    "gdr_int8_matmul_workspace_size", "gdr_int8_matmul",
 ]
 
 
@@ -241,7 +242,8 @@ def _declare_ops(lib):
     fn("gdr_quantize_rows", [QP] + [P] * 4)
     MP = ctypes.POINTER(Int8MatmulProblem)
     fn("gdr_int8_matmul_check", [MP, ctypes.c_char_p, S])
-    fn("gdr_int8_matmul", [MP] + [P] * 7)
+    fn("gdr_int8_matmul_workspace_size", [MP], S)
+    fn("gdr_int8_matmul", [MP] + [P] * 7 + [S, P])
 
 
 def load():

@@ -568,15 +568,26 @@ gdr_status gdr_int8_matmul_check(const gdr_int8_matmul_problem* p, char* reason,
   return s;
 }
 
+size_t gdr_int8_matmul_workspace_size(const gdr_int8_matmul_problem* p) {
+  return validate(p, nullptr, 0) == GDR_OK ? int8_matmul_workspace(p) : 0;
+}
+
 gdr_status gdr_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, const float* x_scale,
                            const void* weight, const float* w_scale, const void* bias, void* y,
-                           void* stream) {
+                           void* workspace, size_t workspace_bytes, void* stream) {
   gdr_status s = validate(p, nullptr, 0);
   if (s != GDR_OK) return s;
   if (!x || !x_scale || !weight || !w_scale || !y)
     return fail(GDR_ERR_NULL, nullptr, 0, "a required matrix-product pointer is NULL");
+  if (p->K % 16 == 0 && (misaligned(weight) || (p->x_stride % 16 == 0 && misaligned(x))))
+    return fail(GDR_ERR_ARG, nullptr, 0, "rows of a multiple of 16 bytes must be 16-byte aligned");
+  s = need_workspace(int8_matmul_workspace(p), workspace, workspace_bytes, "matrix-product");
+  if (s != GDR_OK) return s;
+  if (misaligned(workspace))
+    return fail(GDR_ERR_ARG, nullptr, 0, "the workspace must be 16-byte aligned");
   if ((s = gdr_check_device()) != GDR_OK) return s;
-  return launch_int8_matmul(p, x, x_scale, weight, w_scale, bias, y, (hipStream_t)stream);
+  return launch_int8_matmul(p, x, x_scale, weight, w_scale, bias, y, workspace,
+                            (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -58,9 +58,10 @@ gdr_status launch_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const vo
 // --- rows and products in 8 bits (quantize.hip, int8_matmul.hip) ---
 gdr_status launch_quantize_rows(const gdr_quantize_problem* p, const void* x, void* q, float* scale,
                                 hipStream_t st);
+size_t int8_matmul_workspace(const gdr_int8_matmul_problem* p);
 gdr_status launch_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, const float* x_scale,
                               const void* w, const float* w_scale, const void* bias, void* y,
-                              hipStream_t st);
+                              void* ws, hipStream_t st);
 
 // --- selective state space scan (ssm_fwd.hip, ssm_bwd.hip) ---
 struct SsmPlan {

@@ -185,7 +185,17 @@ def test_pointers_and_workspaces():
     for at in (0, 1, 2, 3, 5):
         a = [FAKE] * 6
         a[at] = None
-        assert lib.gdr_int8_matmul(p, *a, None) == 1
+        assert lib.gdr_int8_matmul(p, *a, None, 0, None) == 1
+    for q in (matmul(), matmul(K=60)):
+        assert lib.gdr_int8_matmul_workspace_size(ctypes.byref(q)) == 0
+    assert lib.gdr_int8_matmul(p, FAKE + 8, *[FAKE] * 5, None, 0, None) == 10
+    assert lib.gdr_int8_matmul(p, FAKE, FAKE, FAKE + 1, *[FAKE] * 3, None, 0, None) == 10
+    p = ctypes.byref(matmul(M=2000, N=2000, K=1001, x_stride=1001))
+    n = lib.gdr_int8_matmul_workspace_size(p)
+    assert n >= 4000 * 1008
+    assert lib.gdr_int8_matmul(p, *[FAKE + 1] * 6, FAKE, n - 1, None) == 7
+    assert lib.gdr_int8_matmul(p, *[FAKE + 1] * 6, None, n, None) == 7
+    assert lib.gdr_int8_matmul(p, *[FAKE + 1] * 6, FAKE + 4, n, None) == 10
 
 
 def meta(*shape, dtype=torch.bfloat16):

@@ -6,12 +6,15 @@ The product's sums are exact.  What is rounded: the sum's conversion to fp32
 the bias, which rounds once more) and the output: 2^-21 of the terms'
 magnitudes and half a step.  A row's scale is one fp32 division, a value the
 rounded quotient: 2^-22."""
+import ctypes
+
 import pytest
 import torch
 
 import _block_ref as bref
 import _layer_ref as ref
 import gated_delta_rule_66_amd as gdr
+from gated_delta_rule_66_amd import _lib
 
 pytestmark = pytest.mark.gpu
 SLACK = 2.0 ** -21
@@ -127,13 +130,14 @@ def test_outputs_stay_inside():
         t = make(M, N, K, bias=False)
         g = {k: v.cuda() for k, v in t.items() if v is not None}
         buf = torch.full((M * N + 1024,), 7.0, device="cuda", dtype=BF)
-        from gated_delta_rule_66_amd import _lib
-        p = _lib.Int8MatmulProblem(M, N, K, 0, 0, K)
-        import ctypes
-        _lib.check(_lib.lib.gdr_int8_matmul(ctypes.byref(p), g["x"].data_ptr(), g["xs"].data_ptr(),
-                                            g["w"].data_ptr(), g["ws"].data_ptr(), None,
-                                            buf[512:].data_ptr(), torch.cuda.current_stream().cuda_stream))
+        p = ctypes.byref(_lib.Int8MatmulProblem(M, N, K, 0, 0, K))
+        n = _lib.lib.gdr_int8_matmul_workspace_size(p)
+        ws = torch.full((n + 1024,), 7, device="cuda", dtype=torch.uint8)
+        _lib.check(_lib.lib.gdr_int8_matmul(p, g["x"].data_ptr(), g["xs"].data_ptr(), g["w"].data_ptr(),
+                                            g["ws"].data_ptr(), None, buf[512:].data_ptr(),
+                                            ws[512:].data_ptr(), n, torch.cuda.current_stream().cuda_stream))
         torch.cuda.synchronize()
+        assert (ws[:512] == 7).all() and (ws[512 + n:] == 7).all()
         assert (buf[:512] == 7).all() and (buf[512 + M * N:] == 7).all()
         assert torch.equal(buf[512:512 + M * N].view(M, N), run(t))
 
