@@ -41,6 +41,22 @@ __device__ __forceinline__ i32x4 load16(const int8_t* p) {
   const Raw r = *reinterpret_cast<const Raw*>(p);
   return i32x4{r.u[0], r.u[1], r.u[2], r.u[3]};
 }
+// The same from two aligned reads: a read at an odd address takes several times
+// as long.  (Bytes before p or past p + 16 share a word with the first or the
+// last byte that is asked for.)
+__device__ __forceinline__ i32x4 load16_shifted(const int8_t* p) {
+  struct __attribute__((aligned(4))) Raw {
+    int u[4];
+  };
+  const int shift = (int)((uintptr_t)p & 3);
+  const int8_t* q = p - shift;
+  const Raw r = *reinterpret_cast<const Raw*>(q);
+  const int end = *reinterpret_cast<const int*>(q + (shift ? 16 : 12));
+  return i32x4{(int)__builtin_amdgcn_alignbyte(r.u[1], r.u[0], shift),
+               (int)__builtin_amdgcn_alignbyte(r.u[2], r.u[1], shift),
+               (int)__builtin_amdgcn_alignbyte(r.u[3], r.u[2], shift),
+               (int)__builtin_amdgcn_alignbyte(end, r.u[3], shift)};
+}
 // Bytes [k, k + 16) of a row of K; those past its end are zero, and none past
 // it is read.
 __device__ __forceinline__ i32x4 load16_of_row(const int8_t* row, int k, int K) {
@@ -65,7 +81,8 @@ __device__ __forceinline__ O scaled(int acc, float xs, float ws, float bias) {
 // eighth of K each, read operands straight from memory to registers and add
 // up their sums in LDS.
 constexpr int kSplit = 8;
-template <int NB, int MB, typename O>
+// ODD: some row begins inside a word.
+template <int NB, int MB, bool ODD, typename O>
 __global__ __launch_bounds__(64 * kSplit) void int8_few_kernel(MatArgs a) {
   constexpr int BN = 16 * NB, BM = 16 * MB;
   __shared__ __align__(16) int part[kSplit][BM][BN + 4];
@@ -91,9 +108,9 @@ __global__ __launch_bounds__(64 * kSplit) void int8_few_kernel(MatArgs a) {
   for (; k < whole; k += 64) {
     i32x4 fw[NB], fx[MB];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) fw[i] = load16(wrow[i] + k + kq);
+    for (int i = 0; i < NB; ++i) fw[i] = ODD ? load16_shifted(wrow[i] + k + kq) : load16(wrow[i] + k + kq);
 #pragma unroll
-    for (int j = 0; j < MB; ++j) fx[j] = load16(xrow[j] + k + kq);
+    for (int j = 0; j < MB; ++j) fx[j] = ODD ? load16_shifted(xrow[j] + k + kq) : load16(xrow[j] + k + kq);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -359,14 +376,15 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(MatArgs a) {
   }
 }
 
-// Rows of K bytes at any address, copied to rows of a multiple of 16 bytes that
-// end with zeros: up to two matrices, a wave a row.
+// Rows of K bytes at any address, copied to rows that begin at multiples of 128
+// bytes (with ones at odd multiples of 16 the product takes 15 % longer) and end
+// with zeros up to one of 16: up to two matrices, a wave a row.
 struct PadArgs {
   const int8_t* src[2];
   int8_t* dst[2];
   int64_t stride[2];
   int rows[2];
-  int K, row;
+  int K, padded, row;
 };
 __global__ __launch_bounds__(256) void int8_pad_kernel(PadArgs a) {
   int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -374,16 +392,17 @@ __global__ __launch_bounds__(256) void int8_pad_kernel(PadArgs a) {
   if (which) r -= a.rows[0];
   if (which && r >= a.rows[1]) return;
   const int8_t* src = a.src[which] + r * a.stride[which];
-  int8_t* dst = a.dst[which] + r * a.row;
-  for (int k = 16 * (threadIdx.x & 63); k < a.row; k += 1024)
-    *reinterpret_cast<i32x4*>(dst + k) = load16_of_row(src, k, a.K);
+  int8_t* dst = a.dst[which] + r * (int64_t)a.row;
+  for (int k = 16 * (threadIdx.x & 63); k < a.padded; k += 1024)
+    *reinterpret_cast<i32x4*>(dst + k) =
+        k + 16 <= a.K ? load16_shifted(src + k) : load16_of_row(src, k, a.K);
 }
 
 // What a problem runs as, from its sizes.
 struct MatPlan {
   enum { kFew16, kFew32, kFew64, kTile64, kTile128, kTile256 } kernel;
   bool pad_x, pad_w;  // tiles of rows whose pieces of 16 bytes are not aligned
-  int row;            // bytes of a padded row
+  int row;            // bytes from one padded row to the next
 };
 // The kernel of the least estimated time, in us; bf16 outputs of random values.
 // Tiles: the card holds `slots` workgroups; a round of them takes `full` per 128
@@ -404,17 +423,18 @@ MatPlan plan_of(const gdr_int8_matmul_problem* p) {
     return 1 + std::ceil(K / 128) * (rounds * full + last);
   };
   MatPlan q{};
-  q.row = (p->K + 15) / 16 * 16;
+  q.row = (p->K + 127) / 128 * 128;
   q.pad_w = p->K % 16 != 0;
   q.pad_x = q.pad_w || p->x_stride % 16 != 0;
-  const double pad = (q.pad_w ? 3 + N * K / 2e6 : 0) + (q.pad_x ? 3 + M * K / 2e6 : 0);
+  const double pad = q.pad_x ? 3 + (q.pad_w ? N + M : M) * K / 2.8e6 : 0;
   // what a launch holds: 2^32 threads, 65535 rows of workgroups
   const double few = std::ceil(N / 32) * std::ceil(M / 64);
   const double small = std::ceil(N / 64) * std::ceil(M / 64);
+  const double odd = (p->K | p->x_stride) % 4 != 0 ? 1.65 : 1;
   const double us[6] = {
-      M <= 16 ? 2 + N * K / 5e6 * (0.8 + M / 40) : never,
-      M <= 32 ? 2 + N * K / 5e6 * 1.7 : never,
-      few < 1 << 22 && M < 1 << 21 ? 1 + K / 4096 * 12.5 * std::ceil(few / 256) : never,
+      M <= 16 ? 2 + odd * N * K / 5e6 * (0.8 + M / 40) : never,
+      M <= 32 ? 2 + odd * N * K / 5e6 * 1.7 : never,
+      few < 1 << 22 && M < 1 << 21 ? 1 + odd * K / 4096 * 12.5 * std::ceil(few / 256) : never,
       small < 1 << 23 ? pad + tile_us(64, 512, 0.44, 0.29) : never,
       pad + tile_us(128, 512, 1.28, 0.75),
       pad + tile_us(256, 256, 2.2, 1.45),
@@ -458,6 +478,7 @@ gdr_status launch_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, c
     int8_t* at = reinterpret_cast<int8_t*>(ws);
     PadArgs pad{};
     pad.K = p->K;
+    pad.padded = (p->K + 15) / 16 * 16;
     pad.row = q.row;
     if (q.pad_w) {
       pad.src[0] = a.w; pad.dst[0] = at; pad.stride[0] = p->K; pad.rows[0] = p->N;
@@ -468,7 +489,7 @@ gdr_status launch_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, c
     pad.src[1] = a.x; pad.dst[1] = at; pad.stride[1] = p->x_stride; pad.rows[1] = p->M;
     a.x = at;
     a.x_stride = q.row;
-    a.K = q.row;
+    a.K = pad.padded;
     const int64_t rows = (int64_t)pad.rows[0] + pad.rows[1];
     GDR_LAUNCH("int8_pad", int8_pad_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), st, pad);
   }
@@ -477,7 +498,11 @@ gdr_status launch_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, c
     auto few = [&](auto nb, auto mb) {
       constexpr int NB = nb.value, MB = mb.value;
       const dim3 grid((p->N + 16 * NB - 1) / (16 * NB), (p->M + 16 * MB - 1) / (16 * MB));
-      GDR_LAUNCH("int8_few", (int8_few_kernel<NB, MB, O>), grid, dim3(64 * kSplit), st, a);
+      const bool odd = (a.x_stride | a.w_stride | (intptr_t)a.x | (intptr_t)a.w) & 3;
+      if (odd)
+        GDR_LAUNCH("int8_few", (int8_few_kernel<NB, MB, true, O>), grid, dim3(64 * kSplit), st, a);
+      else
+        GDR_LAUNCH("int8_few", (int8_few_kernel<NB, MB, false, O>), grid, dim3(64 * kSplit), st, a);
     };
     auto tiles = [&](auto wn, auto wm, auto nb, auto mb, auto steps) {
       constexpr int WN = wn.value, WM = wm.value, NB = nb.value, MB = mb.value;
