@@ -139,7 +139,7 @@ def gated_rms_norm(x, gate, weight, eps=1e-6, norm_group=0, norm_before_gate=Tru
     autograd.
 
     Over each group of ``norm_group`` consecutive columns of the last dimension
-    (a head; 0: all of them) ``y = weight * x / rms(x) * act(gate)``, as a
+    (a head, 8 or more; 0: all of them) ``y = weight * x / rms(x) * act(gate)``, as a
     gated delta rule's layer has it, or with ``norm_before_gate=False`` ``y = weight
     * v / rms(v)``, ``v = x * act(gate)``, as a selective scan's has it; ``rms(v) =
     sqrt(mean(v^2) + eps)``, ``act`` ``"silu"`` or ``"sigmoid"``.  x and gate ``[..., D]``

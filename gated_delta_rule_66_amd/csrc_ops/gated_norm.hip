@@ -4,15 +4,13 @@
 // with u(v) = v / sqrt(mean v^2 + eps); y in the input's type or in 8 bits; and
 // the gradient.
 //
-// Memory bounds it: x and z are read once and y is written once.  Two layouts
-// of the same kernels:
-//   lanes: groups of 8 L columns, L = 1, 2, 4 ... 64.  A row of all groups
-//     lies in the registers of its threads, and L neighbouring lanes of a wave
-//     hold a group, whose sum needs no barrier;
-//   whole: any other width.  A group is a row of its own (blockIdx.y names the
-//     group), in the registers of its threads.
-// 8-bit outputs whose scale spans several groups of the second kind go through
-// LDS (gated_quant_kernel).
+// Memory bounds it: x and z are read once and y is written once.  A row lies in
+// the registers of its threads, and a group's sum is formed
+//   lanes:    groups of 8 L columns, L = 1, 2, 4 ... 64, by the L neighbouring
+//             lanes that hold them, without a barrier;
+//   units:    a group is a row of its own, held by a wave or a block;
+//   segments: groups of any width from 8 columns on, through LDS: a thread's 8
+//             columns belong to two groups at most.
 #include <algorithm>
 
 #include "norm_device.h"
@@ -20,6 +18,11 @@
 namespace gdr {
 
 namespace {
+
+// Narrower groups are summed as segments of whole rows.
+constexpr int kUnitColumns = 256;
+
+enum Sums { kLanes, kUnits, kSegments };
 
 struct GatedArgs {
   const void* x;
@@ -29,22 +32,33 @@ struct GatedArgs {
   float* scale;
   float* rstd;        // [rows][groups], nullable in the forward
   int64_t x_stride, z_stride;  // elements between rows
-  int rows, D;        // columns of a row
-  int width;          // columns that a row's threads hold: D, or a group
-  int lanes;          // lanes of a group, 0 where the threads hold one group
-  int size;           // columns of a group
-  int groups;         // groups of a row
+  int rows, D;
+  int lanes;          // lanes of a group (kLanes)
+  int size, groups;   // columns of a group, groups of a row
   int wdt, shared;    // shared: one group's weights for all
   int gate_first, act;  // act 1: silu, 2: sigmoid
   int quant, scale_group;
   float eps;
+  double share;       // 1 / size
   // backward
   const void* dy;
   void* dx;
   void* dz;
-  float* part;        // [blocks][shared ? size : D], whole: [blocks][D]
-  int blocks;
+  float* part;        // [sets][D], or [sets][size] of shared weights in lanes
+  int sets;           // walkers of rows, each with a row of `part`
 };
+
+// The row and group of the u-th unit, or row u where threads hold whole rows.
+struct Unit {
+  int64_t row;
+  int group;
+};
+template <Sums SUMS>
+__device__ __forceinline__ Unit unit_of(const GatedArgs& a, unsigned u) {
+  if (SUMS != kUnits || a.groups == 1) return {(int64_t)u, 0};
+  const unsigned row = u / (unsigned)a.groups;
+  return {(int64_t)row, (int)(u - row * (unsigned)a.groups)};
+}
 
 // Sum over `lanes` (a power of two) neighbouring lanes, the same bits in each.
 __device__ __forceinline__ double lanes_sum(double v, int lanes) {
@@ -66,140 +80,142 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   return v;
 }
 
-// Where a thread's weights stand: its column, or the column within its group
-// (a power of two in the lanes layout) where the groups share them.
-__device__ __forceinline__ int weight_at(const GatedArgs& a, int c) {
-  return a.shared && a.lanes ? c & (a.size - 1) : c;
+// The groups of the columns [c, c + 8): the first up to `bound`, and the next.
+struct Span {
+  int group, bound;
+};
+__device__ __forceinline__ Span span_of(const GatedArgs& a, int c) {
+  const int g = c / a.size;
+  return {g, (g + 1) * a.size};
 }
 
-// The forward.
-template <typename T, bool QUANT, int NT, int VPT, bool PART>
+// kSegments: the sums of all groups of a row from each vector's parts (a: of
+// its first group, b: of the next), to total[group] in LDS for all threads.
+// `part` holds two values a vector.  A group's vectors are added in a fixed
+// order by one wave.
+template <typename S, int VPT>
+__device__ __forceinline__ void segment_sums(const GatedArgs& a, const Span* sp, const S* va,
+                                             const S* vb, S* part, S* total) {
+  const int nv = (a.D + 7) / 8;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int vi = i * blockDim.x + threadIdx.x;
+    if (vi < nv) part[2 * vi] = va[i], part[2 * vi + 1] = vb[i];
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  for (int g = threadIdx.x >> 6; g < a.groups; g += waves) {
+    const int c0 = g * a.size, c1 = c0 + a.size;
+    S s = 0;
+    for (int vi = c0 / 8 + lane; vi * 8 < c1; vi += 64) {
+      // the part that belongs to this group: the vector begins in it, or the
+      // one before
+      const int c = min(vi * 8, a.D - 8);
+      s += part[2 * vi + (c >= c0 ? 0 : 1)];
+    }
+    s = lanes_sum(s, 64);
+    if (lane == 0) total[g] = s;
+  }
+  __syncthreads();
+}
+
+// Most vectors, and groups, of a row in segments of VPT steps a thread.
+template <int VPT>
+constexpr int most_vectors() {
+  return 1024 * VPT;
+}
+
+// The forward.  Memory bounds it up to 16-bit outputs: FWDNOTE
+template <typename T, bool QUANT, Sums SUMS, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) {
   __shared__ __align__(8) float lds[32];
-  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
-  const int64_t row = NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (row >= a.rows) return;  // a whole wave; the barriers below are for NT > 64 only
-  const int g = blockIdx.y;   // the group of the whole layout
-  const int64_t first = (int64_t)g * a.width;
+  constexpr bool kSeg = SUMS == kSegments;
+  __shared__ double part[kSeg ? 2 * most_vectors<VPT>() : 1], total[kSeg ? most_vectors<VPT>() : 1];
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x, nt = row_threads<NT>();
+  const Unit unit = unit_of<SUMS>(a, NT == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x);
+  const int64_t row = unit.row;
+  if (row >= a.rows) return;  // a whole wave; the barriers below are for rows of a block
+  const int width = SUMS == kUnits ? a.size : a.D, first = unit.group * a.size;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride + first;
   const T* z = reinterpret_cast<const T*>(a.z) + row * a.z_stride + first;
   float f[VPT][8], t[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = column_of<PART>(i * NT + tid, a.width);
-    load8<T, PART>(x + c, a.width, f[i]);
-    load8<T, PART>(z + c, a.width, t[i]);
+    const int c = column_of<PART>(i * nt + tid, width);
+    load8<T, PART>(x + c, width, f[i]);
+    load8<T, PART>(z + c, width, t[i]);
   }
   // squares, mean and root in 64 bits, as the norm without a gate has them
-  double sum[VPT];
+  double sum[VPT], next[kSeg ? VPT : 1];
+  Span sp[kSeg ? VPT : 1];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.width);
+    const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
     sum[i] = 0.0;
+    if (kSeg) next[i] = 0.0, sp[i] = span_of(a, c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       t[i][e] = gate_of(t[i][e], a.act);
       if (a.gate_first) f[i][e] *= t[i][e];
       const double v = c + e >= v0 ? f[i][e] : 0.f;
-      sum[i] = __builtin_fma(v, v, sum[i]);
+      if (kSeg && c + e >= sp[i].bound) next[i] = __builtin_fma(v, v, next[i]);
+      else sum[i] = __builtin_fma(v, v, sum[i]);
     }
   }
-  float rstd[VPT];
-  if (a.lanes) {
+  float rstd[VPT], rnext[kSeg ? VPT : 1];
+  if (SUMS == kLanes) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v0 = (i * NT + tid) * 8;
-      rstd[i] = (float)(1.0 / __builtin_sqrt(lanes_sum(sum[i], a.lanes) / a.size + (double)a.eps));
+      const int v0 = (i * nt + tid) * 8;
+      rstd[i] = inverse_root(lanes_sum(sum[i], a.lanes) * a.share + (double)a.eps);
       if (a.rstd && v0 < a.D && (tid & (a.lanes - 1)) == 0)
         a.rstd[row * a.groups + v0 / a.size] = rstd[i];
     }
-  } else {
+  } else if (SUMS == kUnits) {
 #pragma unroll
     for (int i = 1; i < VPT; ++i) sum[0] += sum[i];
     const double all = row_sum<NT>(sum[0], reinterpret_cast<double*>(lds));
+    rstd[0] = inverse_root(all * a.share + (double)a.eps);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      rstd[i] = (float)(1.0 / __builtin_sqrt(all / a.size + (double)a.eps));
-    if (a.rstd && tid == 0) a.rstd[row * a.groups + g] = rstd[0];
+    for (int i = 1; i < VPT; ++i) rstd[i] = rstd[0];
+    if (a.rstd && tid == 0) a.rstd[row * a.groups + unit.group] = rstd[0];
+  } else {
+    segment_sums<double, VPT>(a, sp, sum, next, part, total);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      rstd[i] = inverse_root(total[sp[i].group] * a.share + (double)a.eps);
+      rnext[i] = inverse_root(total[min(sp[i].group + 1, a.groups - 1)] * a.share + (double)a.eps);
+    }
+    if (a.rstd)
+      for (int g = tid; g < a.groups; g += nt)
+        a.rstd[row * a.groups + g] = inverse_root(total[g] * a.share + (double)a.eps);
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.width);
+    const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
     float w[8];
-    load_weight<PART>(a.w, weight_at(a, c) + (a.shared ? 0 : (int)first), a.width, a.wdt, w);
+    if (!kSeg || !a.shared) {
+      // (a power of two of columns in the lanes' groups)
+      const int at = !a.shared ? first + c : SUMS == kLanes ? c & (a.size - 1) : c;
+      load_weight<PART>(a.w, at, width, a.wdt, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        w[e] = load_scalar(a.w, c + e - sp[i].bound + (c + e >= sp[i].bound ? 0 : a.size), a.wdt);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      f[i][e] = f[i][e] * rstd[i] * w[e];
+      f[i][e] = f[i][e] * (kSeg && c + e >= sp[i].bound ? rnext[i] : rstd[i]) * w[e];
       if (!a.gate_first) f[i][e] *= t[i][e];
-      // (past the row's end the lanes layout holds groups that are none)
-      if (QUANT && a.lanes && v0 >= a.D) f[i][e] = 0.f;
+      // (past the row's end the lanes hold groups that are none)
+      if (QUANT && SUMS == kLanes && v0 >= a.D) f[i][e] = 0.f;
     }
-    if (!QUANT && v0 < a.width)
-      store8<T, PART>(reinterpret_cast<T*>(a.y) + row * a.D + first + c, a.width, f[i]);
+    if (!QUANT && v0 < width)
+      store8<T, PART>(reinterpret_cast<T*>(a.y) + row * a.D + first + c, width, f[i]);
   }
   if (QUANT)
     quantise_row<NT, VPT, PART>(f, row, tid, a.D, a.quant, a.scale_group,
                                 reinterpret_cast<uint8_t*>(a.y), a.scale, lds);
-}
-
-// 8-bit outputs of rows of several groups that the lanes layout does not take.
-// The row's values pass through LDS between the norm, where a wave walks one
-// group at a time, and the quantisation, where a thread holds 8 columns.
-constexpr int kQuantCols = 16384;
-template <typename T>
-__global__ __launch_bounds__(256) void gated_quant_kernel(GatedArgs a) {
-  __shared__ __align__(16) float val[kQuantCols];
-  __shared__ float red[16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = blockIdx.x;
-  const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
-  const T* z = reinterpret_cast<const T*>(a.z) + row * a.z_stride;
-  float mx = 0.f;
-  for (int g = wave; g < a.groups; g += 4) {
-    const int c0 = g * a.size;
-    double sum = 0.0;
-    for (int c = lane; c < a.size; c += 64) {
-      const float s = gate_of(to_f(z[c0 + c]), a.act);
-      float f = to_f(x[c0 + c]);
-      if (a.gate_first) f *= s;
-      sum = __builtin_fma((double)f, (double)f, sum);
-      val[c0 + c] = f;
-    }
-    const float rstd =
-        (float)(1.0 / __builtin_sqrt(lanes_sum(sum, 64) / a.size + (double)a.eps));
-    for (int c = lane; c < a.size; c += 64) {
-      float f = val[c0 + c] * rstd * load_scalar(a.w, a.shared ? c : c0 + c, a.wdt);
-      if (!a.gate_first) f *= gate_of(to_f(z[c0 + c]), a.act);
-      val[c0 + c] = f;
-      mx = max_nan(mx, fabsf(f));
-    }
-  }
-  const bool fp8 = a.quant == 1;
-  const float top = fp8 ? 448.f : 127.f;
-  mx = row_reduce<256, true>(mx, red) / top;  // (its barriers hand `val` over, too)
-  const float row_scale = mx < kTinyScale ? kTinyScale : mx;
-  if (!a.scale_group && threadIdx.x == 0) a.scale[row] = row_scale;
-  uint8_t* y = reinterpret_cast<uint8_t*>(a.y) + row * a.D;
-  const int scales = (a.D + 127) / 128;
-  for (int c0 = threadIdx.x * 8; c0 < scales * 128; c0 += 2048) {  // whole groups of 16 lanes
-    float f[8], s = row_scale;
-    float big = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      f[e] = c0 + e < a.D ? val[c0 + e] : 0.f;
-      big = max_nan(big, fabsf(f[e]));
-    }
-    if (a.scale_group) {
-      big = max16(big) / top;
-      s = big < kTinyScale ? kTinyScale : big;
-      if ((threadIdx.x & 15) == 0) a.scale[row * scales + c0 / 128] = s;
-    }
-    uint32_t b[2];
-    quantise8(f, s, fp8, b);
-    if (c0 + 8 <= a.D) store_bytes8(y + c0, b);
-    else
-      for (int e = 0; e < a.D - c0; ++e) y[c0 + e] = (uint8_t)(b[e >> 2] >> (8 * (e & 3)));
-  }
 }
 
 // The gradient.  norm first, with u the unit rows:
@@ -208,90 +224,117 @@ __global__ __launch_bounds__(256) void gated_quant_kernel(GatedArgs a) {
 //   du = dy w,  dv = r (du - u mean(du u)),  dx = dv a,  dz = dv x a',
 //   dw = sum dy u
 // A block walks rows blockIdx.x, + blocks, ... with dw in registers and leaves
-// its sum in `part`, which reduce_rows_kernel adds in order.  Where the groups
-// of a row share their weights the block adds up its groups first.
-template <typename T, int NT, int VPT, bool PART>
-__global__ __launch_bounds__(block_of<NT>()) void gated_bwd_kernel(GatedArgs a) {
+// its sum in `part`, which launch_reduce_rows adds in order.  Where lanes hold
+// groups that share their weights the block adds up its groups first.
+// BWDNOTE
+template <typename T, Sums SUMS, int NT, int VPT, bool PART>
+__global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void gated_bwd_kernel(GatedArgs a) {
   constexpr int RPB = NT == 64 ? 4 : 1;
-  constexpr int COLS = NT * VPT * 8;
-  constexpr int WAVES = block_of<NT>() / 64;
+  constexpr int COLS = 64 * VPT * 8;  // of a wave's row
+  constexpr bool kSeg = SUMS == kSegments;
   __shared__ float lds[16];
-  // columns of four rows, or (shared weights) each wave's group
-  __shared__ float wsum[NT == 64 ? 4 * COLS : WAVES * 512];
-  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  // columns of four rows, or (shared weights in lanes) each wave's group
+  __shared__ float wsum[NT == 64 ? 4 * COLS : SUMS == kLanes ? 16 * 512 : 1];
+  __shared__ float segs[kSeg ? 2 * most_vectors<VPT>() : 1], total[kSeg ? most_vectors<VPT>() : 1];
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x, nt = row_threads<NT>();
   const int q = NT == 64 ? (threadIdx.x >> 6) : 0;
-  const int g = blockIdx.y;
-  const int64_t first = (int64_t)g * a.width;
+  const Unit unit = unit_of<SUMS>(a, blockIdx.x * RPB + q);  // (its row: the walker)
+  const int width = SUMS == kUnits ? a.size : a.D, first = unit.group * a.size;
   float dw[VPT][8], w[VPT][8];
+  Span sp[kSeg ? VPT : 1];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = column_of<PART>(i * NT + tid, a.width);
+    const int c = column_of<PART>(i * nt + tid, width);
+    if (kSeg) sp[i] = span_of(a, c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
-    load_weight<PART>(a.w, weight_at(a, c) + (a.shared ? 0 : (int)first), a.width, a.wdt, w[i]);
+    if (!kSeg || !a.shared) {
+      const int at = !a.shared ? first + c : SUMS == kLanes ? c & (a.size - 1) : c;
+      load_weight<PART>(a.w, at, width, a.wdt, w[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        w[i][e] = load_scalar(a.w, c + e - sp[i].bound + (c + e >= sp[i].bound ? 0 : a.size), a.wdt);
+    }
   }
-  for (int64_t row = (int64_t)blockIdx.x * RPB + q; row < a.rows; row += (int64_t)a.blocks * RPB) {
+  for (int64_t row = unit.row < a.sets ? unit.row : a.rows; row < a.rows; row += a.sets) {
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride + first;
     const T* z = reinterpret_cast<const T*>(a.z) + row * a.z_stride + first;
     const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.D + first;
-    float u[VPT][8], s[VPT][8], du[VPT][8], r[VPT];
+    const float* rs = a.rstd + row * a.groups;
+    float u[VPT][8], z8[VPT][8], s[VPT][8], du[VPT][8], r[VPT], rnext[kSeg ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = column_of<PART>(i * NT + tid, a.width);
-      load8<T, PART>(x + c, a.width, u[i]);
-      load8<T, PART>(z + c, a.width, s[i]);
-      load8<T, PART>(dy + c, a.width, du[i]);
-      r[i] = a.rstd[row * a.groups + (a.lanes ? c / a.size : g)];
+      const int c = column_of<PART>(i * nt + tid, width);
+      load8<T, PART>(x + c, width, u[i]);
+      load8<T, PART>(z + c, width, z8[i]);
+      load8<T, PART>(dy + c, width, du[i]);
+      r[i] = rs[kSeg ? sp[i].group : SUMS == kLanes ? c / a.size : unit.group];
+      if (kSeg) rnext[i] = rs[min(sp[i].group + 1, a.groups - 1)];
     }
-    float dot[VPT];
+    float dot[VPT], dnext[kSeg ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.width);
-      const bool live = !a.lanes || v0 < a.D;
+      const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
+      const bool live = SUMS != kLanes || v0 < a.D;
       dot[i] = 0.f;
+      if (kSeg) dnext[i] = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float act = gate_of(s[i][e], a.act);
-        const float unit = u[i][e] * r[i] * (a.gate_first ? act : 1.f);
+        const bool second = kSeg && c + e >= sp[i].bound;
+        z8[i][e] = gate_input(z8[i][e]);
+        s[i][e] = sigmoid(z8[i][e]);
+        const float act = a.act == 1 ? z8[i][e] * s[i][e] : s[i][e];
+        const float unit = u[i][e] * (second ? rnext[i] : r[i]) * (a.gate_first ? act : 1.f);
         const float k = a.gate_first ? 1.f : act;
         if (live) dw[i][e] += du[i][e] * unit * k;
-        const float d = du[i][e] * w[i][e] * k;
-        dot[i] += c + e >= v0 ? d * unit : 0.f;
+        du[i][e] *= w[i][e];
+        const float term = c + e >= v0 ? du[i][e] * k * unit : 0.f;
+        if (second) dnext[i] += term;
+        else dot[i] += term;
       }
     }
-    if (a.lanes) {
+    if (SUMS == kLanes) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) dot[i] = lanes_sum(dot[i], a.lanes) / (float)a.size;
-    } else {
+    } else if (SUMS == kUnits) {
 #pragma unroll
       for (int i = 1; i < VPT; ++i) dot[0] += dot[i];
       dot[0] = row_reduce<NT, false>(dot[0], lds) / (float)a.size;
 #pragma unroll
       for (int i = 1; i < VPT; ++i) dot[i] = dot[0];
+    } else {
+      segment_sums<float, VPT>(a, sp, dot, dnext, segs, total);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        dot[i] = total[sp[i].group] / (float)a.size;
+        dnext[i] = total[min(sp[i].group + 1, a.groups - 1)] / (float)a.size;
+      }
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.width);
-      if (v0 >= a.width) continue;
+      const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
+      if (v0 >= width) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const Gate t = gate_and_slope(s[i][e], a.act);
-        const float xr = u[i][e] * r[i];
+        const bool second = kSeg && c + e >= sp[i].bound;
+        const float re = second ? rnext[i] : r[i], mean = second ? dnext[i] : dot[i];
+        const Gate t = gate_and_slope(z8[i][e], s[i][e], a.act);
+        const float xr = u[i][e] * re, d = du[i][e];
         if (a.gate_first) {
-          const float dv = r[i] * (du[i][e] * w[i][e] - xr * t.value * dot[i]);
+          const float dv = re * (d - xr * t.value * mean);
           s[i][e] = dv * u[i][e] * t.slope;
           u[i][e] = dv * t.value;
         } else {
-          const float d = du[i][e] * w[i][e];
           s[i][e] = d * xr * t.slope;
-          u[i][e] = r[i] * (d * t.value - xr * dot[i]);
+          u[i][e] = re * (d * t.value - xr * mean);
         }
       }
-      store8<T, PART>(reinterpret_cast<T*>(a.dx) + row * a.D + first + c, a.width, u[i]);
-      store8<T, PART>(reinterpret_cast<T*>(a.dz) + row * a.D + first + c, a.width, s[i]);
+      store8<T, PART>(reinterpret_cast<T*>(a.dx) + row * a.D + first + c, width, u[i]);
+      store8<T, PART>(reinterpret_cast<T*>(a.dz) + row * a.D + first + c, width, s[i]);
     }
   }
-  if (a.shared && a.lanes) {
+  if (SUMS == kLanes && a.shared) {
     // over the thread's steps, the wave's groups and the block's waves
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -303,57 +346,35 @@ __global__ __launch_bounds__(block_of<NT>()) void gated_bwd_kernel(GatedArgs a) 
       if (lane < a.lanes) wsum[(threadIdx.x >> 6) * 512 + lane * 8 + e] = v;
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < a.size; k += block_of<NT>()) {
+    for (int k = threadIdx.x; k < a.size; k += blockDim.x) {
       float v = wsum[k];
-#pragma unroll
-      for (int i = 1; i < WAVES; ++i) v += wsum[i * 512 + k];
+      for (int i = 1; i < (int)blockDim.x >> 6; ++i) v += wsum[i * 512 + k];
       a.part[(int64_t)blockIdx.x * a.size + k] = v;
     }
     return;
   }
-  float* part = a.part + (int64_t)blockIdx.x * a.D + first;
-  if (NT > 64) {
+  if (NT == 0 || (SUMS == kUnits && a.groups > 1)) {
+    float* part = a.part + unit.row * a.D + first;
+    if (unit.row < a.sets)
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if ((i * NT + tid) * 8 < a.width)
-        store8<float, PART>(part + column_of<PART>(i * NT + tid, a.width), a.width, dw[i]);
+      for (int i = 0; i < VPT; ++i)
+        if ((i * nt + tid) * 8 < width)
+          store8<float, PART>(part + column_of<PART>(i * nt + tid, width), width, dw[i]);
   } else {
     // columns of the block's four rows, each at its vector's place
+    float* part = a.part + (int64_t)blockIdx.x * a.D;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) wsum[q * COLS + (i * 64 + tid) * 8 + e] = dw[i][e];
     __syncthreads();
-    for (int k = threadIdx.x; k < ((a.width + 7) / 8) * 8; k += 256) {
-      const int c = column_of<PART>(k / 8, a.width) + k % 8;
-      if (c < a.width)
+    for (int k = threadIdx.x; k < ((a.D + 7) / 8) * 8; k += 256) {
+      const int c = column_of<PART>(k / 8, a.D) + k % 8;
+      if (c < a.D)
         part[c] = (wsum[k] + wsum[(NT == 64 ? 1 : 0) * COLS + k]) +
                   (wsum[(NT == 64 ? 2 : 0) * COLS + k] + wsum[(NT == 64 ? 3 : 0) * COLS + k]);
     }
   }
-}
-
-// Groups of 8 L columns, L a power of two up to a wave's 64 lanes.
-bool in_lanes(int size) { return size % 8 == 0 && size <= 512 && (size & (size - 1)) == 0; }
-
-// Threads per row and 8-element steps per thread, as the norm without a gate
-// has them up to its 16,384 columns.
-template <typename F>
-void by_width(int D, F f) {
-  const int nv = (D + 7) / 8;
-  const std::false_type whole;
-#define GDR_W(NT, VPT) \
-  if (nv <= NT * VPT)  \
-  return f(std::integral_constant<int, NT>(), std::integral_constant<int, VPT>(), whole)
-  if (D < 8)
-    return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>(), std::true_type());
-  GDR_W(64, 1);
-  GDR_W(64, 2);
-  GDR_W(256, 1);
-  GDR_W(256, 2);
-  GDR_W(256, 4);
-  GDR_W(256, 8);
-#undef GDR_W
 }
 
 template <typename F>
@@ -361,6 +382,63 @@ void by_type(const gdr_gated_norm_problem* p, F f) {
   if (p->dtype == GDR_BF16) f(__bf16());
   else if (p->dtype == GDR_FP16) f(_Float16());
   else f(float());
+}
+
+// How the sums of a problem's groups are formed.  Units hold a wave or a block a
+// group, wherever no scale spans several groups and a wave's lanes are busy
+// enough: UNITNOTE
+Sums sums_of(const gdr_gated_norm_problem* p) {
+  const int n = p->norm_size;
+  if (n % 8 == 0 && n <= 512 && (n & (n - 1)) == 0) return kLanes;
+  return n == p->D || (!p->quant && n >= kUnitColumns) ? kUnits : kSegments;
+}
+template <Sums SUMS>
+using SumsTag = std::integral_constant<Sums, SUMS>;
+using Zero = std::integral_constant<int, 0>;
+using One = std::integral_constant<int, 1>;
+using Two = std::integral_constant<int, 2>;
+
+// Threads of a row in segments: a block's, also where a wave could hold it.
+template <typename F>
+void by_segments(int D, F f) {
+  auto form = [&](auto vpt) {
+    constexpr int C = 512 * vpt.value;
+    f(dim3(64 * ((D + C - 1) / C)), 1, SumsTag<kSegments>(), Zero(), vpt, std::false_type());
+  };
+  if (D <= 8192) form(One());
+  else form(Two());
+}
+// f(threads of a block, its rows, SUMS, NT, VPT, PART)
+template <typename F>
+void by_form(const gdr_gated_norm_problem* p, F f) {
+  const Sums sums = sums_of(p);
+  if (sums == kSegments) return by_segments(p->D, f);
+  by_row<2>(sums == kLanes ? p->D : p->norm_size, [&](dim3 block, int rows, auto nt, auto vpt, auto part) {
+    if constexpr (!part.value) {
+      if (sums == kLanes) return f(block, rows, SumsTag<kLanes>(), nt, vpt, part);
+    }
+    f(block, rows, SumsTag<kUnits>(), nt, vpt, part);
+  });
+}
+// The gradient holds six arrays of a row: one step a thread as far as a block
+// reaches (4096 columns by 256 threads of two steps took 193 registers and 75
+// us, by 512 threads of one 111 and 61), two for a wave's units.
+template <typename F>
+void by_form_bwd(const gdr_gated_norm_problem* p, F f) {
+  const Sums sums = sums_of(p);
+  if (sums == kSegments) return by_segments(p->D, f);
+  const int width = sums == kLanes ? p->D : p->norm_size;
+  auto form = [&](dim3 block, int rows, auto nt, auto vpt, auto part) {
+    if constexpr (!part.value) {
+      if (sums == kLanes) return f(block, rows, SumsTag<kLanes>(), nt, vpt, part);
+    }
+    f(block, rows, SumsTag<kUnits>(), nt, vpt, part);
+  };
+  if (sums == kUnits && width > 512 && width <= 1024)
+    return f(dim3(256), 4, SumsTag<kUnits>(), std::integral_constant<int, 64>(), Two(),
+             std::false_type());
+  if (width <= 8192) return by_row<1>(width, form);
+  form(dim3(64 * ((width + 1023) / 1024)), 1, Zero(), Two(), std::false_type());
 }
 
 GatedArgs args_of(const gdr_gated_norm_problem* p) {
@@ -371,8 +449,7 @@ GatedArgs args_of(const gdr_gated_norm_problem* p) {
   a.D = p->D;
   a.size = p->norm_size;
   a.groups = p->D / p->norm_size;
-  a.lanes = in_lanes(p->norm_size) ? p->norm_size / 8 : 0;
-  a.width = a.lanes ? p->D : p->norm_size;
+  a.lanes = p->norm_size / 8;
   a.wdt = (int)p->w_dtype;
   a.shared = p->shared_weight;
   a.gate_first = p->gate_first;
@@ -380,14 +457,31 @@ GatedArgs args_of(const gdr_gated_norm_problem* p) {
   a.quant = p->quant;
   a.scale_group = p->scale_group;
   a.eps = p->eps;
+  a.share = 1.0 / p->norm_size;
   return a;
 }
 
-int bwd_blocks(const GatedArgs& a) {
-  // as the norm without a gate: at least 8 rows a block, at most 1024 blocks
-  const int rpb = a.width <= 1024 ? 4 : 1, across = a.lanes ? 1 : a.groups;
-  const int64_t want = ((int64_t)a.rows + 8 * rpb - 1) / (8 * rpb);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, std::max(1, 1024 / across)));
+// Blocks of the gradient, and their walkers of rows (sets).  4096 waves fill the
+// card; a block (a wave of units) walks at least 8 rows, against its partial
+// sums.
+struct Walk {
+  int blocks, sets;
+  int parts;  // rows of partial sums
+};
+Walk walk_of(const gdr_gated_norm_problem* p) {
+  Walk w{};
+  const bool units = sums_of(p) == kUnits;
+  const int64_t groups = units ? p->D / p->norm_size : 1;
+  by_form_bwd(p, [&](dim3 block, int rows, auto, auto, auto, auto) {
+    // `rows` walkers a block
+    const int64_t most = std::max<int64_t>(1, 4096 * 64 / block.x * rows / groups);
+    int64_t sets = std::max<int64_t>(1, std::min<int64_t>(most, ((int64_t)p->rows + 7) / 8));
+    if (groups == 1) sets = (sets + rows - 1) / rows * rows;
+    w.sets = (int)sets;
+    w.blocks = (int)((sets * groups + rows - 1) / rows);
+    w.parts = groups == 1 ? w.blocks : w.sets;
+  });
+  return w;
 }
 
 }  // namespace
@@ -399,26 +493,25 @@ gdr_status launch_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x,
   a.x = x; a.z = gate; a.w = weight; a.y = y; a.scale = scale; a.rstd = rstd;
   by_type(p, [&](auto t) {
     using T = decltype(t);
-    if (p->quant && !a.lanes && a.groups > 1) {
-      GDR_LAUNCH("gated_quant", gated_quant_kernel<T>, dim3(a.rows), dim3(256), st, a);
-      return;
-    }
-    by_width(a.width, [&](auto nt, auto vpt, auto part) {
+    by_form(p, [&](dim3 block, int rows, auto sums, auto nt, auto vpt, auto part) {
+      constexpr Sums SUMS = sums.value;
       constexpr int NT = nt.value, VPT = vpt.value;
-      const dim3 grid((unsigned)(NT == 64 ? (a.rows + 3) / 4 : a.rows), a.lanes ? 1 : a.groups);
-      const dim3 block(block_of<NT>());
+      const int64_t units = (int64_t)a.rows * (SUMS == kUnits ? a.groups : 1);
+      const dim3 grid((unsigned)((units + rows - 1) / rows));
       if (p->quant)
-        GDR_LAUNCH("gated_fwd", (gated_fwd_kernel<T, true, NT, VPT, part.value>), grid, block, st, a);
+        GDR_LAUNCH("gated_fwd", (gated_fwd_kernel<T, true, SUMS, NT, VPT, part.value>), grid, block,
+                   st, a);
       else
-        GDR_LAUNCH("gated_fwd", (gated_fwd_kernel<T, false, NT, VPT, part.value>), grid, block, st, a);
+        GDR_LAUNCH("gated_fwd", (gated_fwd_kernel<T, false, SUMS, NT, VPT, part.value>), grid, block,
+                   st, a);
     });
   });
   return launch_status("gated_norm_fwd");
 }
 
 size_t gated_norm_bwd_workspace(const gdr_gated_norm_problem* p) {
-  const GatedArgs a = args_of(p);
-  return align256((size_t)bwd_blocks(a) * a.D * sizeof(float));
+  // a row more for the groups' own sums
+  return align256(((size_t)walk_of(p).parts + 1) * p->D * sizeof(float));
 }
 
 gdr_status launch_gated_norm_bwd(const gdr_gated_norm_problem* p, const void* dy, const void* x,
@@ -428,19 +521,23 @@ gdr_status launch_gated_norm_bwd(const gdr_gated_norm_problem* p, const void* dy
   a.x = x; a.z = gate; a.w = weight; a.rstd = const_cast<float*>(rstd);
   a.dy = dy; a.dx = dx; a.dz = dgate;
   a.part = reinterpret_cast<float*>(ws);
-  a.blocks = bwd_blocks(a);
+  const Walk walk = walk_of(p);
+  a.sets = walk.sets;
   by_type(p, [&](auto t) {
     using T = decltype(t);
-    by_width(a.width, [&](auto nt, auto vpt, auto part) {
-      constexpr int NT = nt.value, VPT = vpt.value;
-      GDR_LAUNCH("gated_bwd", (gated_bwd_kernel<T, NT, VPT, part.value>),
-                 dim3(a.blocks, a.lanes ? 1 : a.groups), dim3(block_of<NT>()), st, a);
+    by_form_bwd(p, [&](dim3 block, int, auto sums, auto nt, auto vpt, auto part) {
+      GDR_LAUNCH("gated_bwd",
+                 (gated_bwd_kernel<T, sums.value, nt.value, vpt.value, part.value>),
+                 dim3(walk.blocks), block, st, a);
     });
   });
-  // [blocks][D] is [blocks * groups][size] where the groups share their weights
-  const int cols = a.shared ? a.size : a.D;
-  const int rows = a.shared && !a.lanes ? a.blocks * a.groups : a.blocks;
-  launch_reduce_rows(a.part, rows, cols, dweight, a.wdt, st);
+  if (a.shared && a.groups > 1 && sums_of(p) != kLanes) {
+    float* sums = a.part + (int64_t)walk.parts * a.D;
+    launch_reduce_rows(a.part, walk.parts, a.D, sums, GDR_FP32, st);
+    launch_reduce_rows(sums, a.groups, a.size, dweight, a.wdt, st);
+  } else {
+    launch_reduce_rows(a.part, walk.parts, a.shared ? a.size : a.D, dweight, a.wdt, st);
+  }
   return launch_status("gated_norm_bwd");
 }
 

@@ -71,8 +71,14 @@ __device__ __forceinline__ float wave_max(float v) {
   return max_nan(v, __shfl_xor(v, 32, 64));
 }
 
-// Sum (or largest) of v over the NT threads of a row; every thread of the
-// row gets the same bits.  Rows of one wave share a block, four at a time.
+// Threads of a row: NT, or the whole block where that is 0.
+template <int NT>
+__device__ __forceinline__ int row_threads() {
+  return NT ? NT : (int)blockDim.x;
+}
+
+// Sum (or largest) of v over the threads of a row; every thread of the row gets
+// the same bits.  Rows of one wave share a block, four at a time.
 template <int NT, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* lds) {
   v = MAX ? wave_max(v) : wave_sum(v);
@@ -80,6 +86,11 @@ __device__ __forceinline__ float row_reduce(float v, float* lds) {
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
+  if (NT == 0) {  // up to 16 waves, a lane each
+    const int l = threadIdx.x & 15;
+    v = l < (int)blockDim.x >> 6 ? lds[l] : 0.f;
+    return MAX ? max16(v) : sum16(v);
+  }
   float s = lds[0];
 #pragma unroll
   for (int i = 1; i < NT / 64; ++i) s = MAX ? max_nan(s, lds[i]) : s + lds[i];
@@ -94,18 +105,26 @@ __device__ __forceinline__ double dpp_mov2(double v) {
                 __builtin_bit_cast(uint32_t, dpp_mov<CTRL>(__builtin_bit_cast(float, u.y)))};
   return __builtin_bit_cast(double, r);
 }
-template <int NT>
-__device__ __forceinline__ double row_sum(double v, double* lds) {
+__device__ __forceinline__ double sum16(double v) {
   v += dpp_mov2<0xB1>(v);
   v += dpp_mov2<0x4E>(v);
   v += dpp_mov2<0x141>(v);
   v += dpp_mov2<0x140>(v);
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ double row_sum(double v, double* lds) {
+  v = sum16(v);
   v += __shfl_xor(v, 16, 64);
   v += __shfl_xor(v, 32, 64);
   if (NT == 64) return v;
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
+  if (NT == 0) {
+    const int l = threadIdx.x & 15;
+    return sum16(l < (int)blockDim.x >> 6 ? lds[l] : 0.0);
+  }
   double s = lds[0];
 #pragma unroll
   for (int i = 1; i < NT / 64; ++i) s += lds[i];
@@ -118,60 +137,72 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d)
   r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
   return (uint32_t)r;
 }
-__device__ __forceinline__ uint32_t int8_of(float v) {
-  return v != v ? 0u : (uint32_t)(int)rintf(v) & 0xffu;
+
+// 1 / sqrt(a) to more than fp32's precision: the instruction's estimate and one
+// step of Newton's (0 for an infinity, as the quotient has it).
+__device__ __forceinline__ float inverse_root(double a) {
+  const double y = __builtin_amdgcn_rsq(a);
+  const double z = y * __builtin_fma(-0.5 * a * y, y, 1.5);
+  return (float)(a < __builtin_inf() && a > 0.0 ? z : y);
 }
 
 // A gate's activation (0: none, 1: silu, 2: sigmoid) and its derivative.  The
 // exponential is taken at -80 at the least, where the sigmoid is 2^-115: with
 // an infinity it would make silu's limit 0 and the slopes' products NaN.
+__device__ __forceinline__ float gate_input(float z) { return z < -80.f ? -80.f : z; }  // a NaN passes
+__device__ __forceinline__ float gate_of(float z, int act) {
+  if (act == 0) return z;
+  const float zc = gate_input(z), s = sigmoid(zc);
+  return act == 1 ? zc * s : s;
+}
 struct Gate {
   float value, slope;
 };
-__device__ __forceinline__ Gate gate_and_slope(float z, int act) {
+// From z as gate_input gives it and s, its sigmoid.
+__device__ __forceinline__ Gate gate_and_slope(float z, float s, int act) {
   if (act == 0) return {z, 1.f};
-  const float zc = z < -80.f ? -80.f : z;  // a NaN passes
-  const float e = __expf(-zc), s = fast_rcp(1.f + e), rest = e * s;
-  if (act == 1) return {zc * s, s * (1.f + zc * rest)};
+  const float rest = 1.f - s;
+  if (act == 1) return {z * s, s * __builtin_fmaf(z, rest, 1.f)};
   return {s, s * rest};
 }
-__device__ __forceinline__ float gate_of(float z, int act) {
-  if (act == 0) return z;
-  const float zc = z < -80.f ? -80.f : z;
-  const float s = fast_rcp(1.f + __expf(-zc));
-  return act == 1 ? zc * s : s;
-}
 
-// Threads of a block: one row of NT threads, or (NT == 64) four rows of one
-// wave each.
+// Threads of a block (the most, where NT is 0): one row of NT threads, or (NT ==
+// 64) four rows of one wave each.
 template <int NT>
 constexpr int block_of() {
-  return NT == 64 ? 256 : NT;
+  return NT == 64 ? 256 : NT == 0 ? 1024 : NT;
 }
 
-// Eight values over the scale s, rounded to nearest even: e4m3 or int8.
+// Eight values over the scale s, rounded to nearest even: e4m3 or int8.  With s
+// from the largest of them a quotient passes the type's largest value by a
+// rounding at most, which the conversion's takes away.
 __device__ __forceinline__ void quantise8(const float (&f)[8], float s, bool fp8, uint32_t (&b)[2]) {
-  const float top = fp8 ? 448.f : 127.f;
   float q[8];
   // (an infinite scale leaves the product's 0 or NaN as they are)
-  const float inv = 1.f / s, fin = s < __builtin_inff() ? s : 0.f;
+  const bool finite = s < __builtin_inff();
+  const float inv = 1.f / s, fin = finite ? s : 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     // the product with the reciprocal may lie on the other side of a tie,
     // a whole step off in 8 bits: the residual makes it the fp32 quotient
     q[e] = f[e] * inv;
     q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], fin, f[e]), inv, q[e]);
-    // a NaN passes both comparisons
-    q[e] = q[e] > top ? top : q[e] < -top ? -top : q[e];
   }
   if (fp8) {
     b[0] = pack_fp8(q[0], q[1], q[2], q[3]);
     b[1] = pack_fp8(q[4], q[5], q[6], q[7]);
   } else {
+    // 1.5 2^23 + q holds q's nearest whole number in its lowest byte; a scale
+    // that is no number or infinite leaves 0
+    uint32_t u[8];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      b[k] = int8_of(q[4 * k]) | int8_of(q[4 * k + 1]) << 8 | int8_of(q[4 * k + 2]) << 16 |
-             int8_of(q[4 * k + 3]) << 24;
+    for (int e = 0; e < 8; ++e) u[e] = __builtin_bit_cast(uint32_t, q[e] + 12582912.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t lo = __builtin_amdgcn_perm(u[4 * k + 1], u[4 * k], 0x0c0c0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(u[4 * k + 3], u[4 * k + 2], 0x04000c0cu);
+      b[k] = finite ? lo | hi : 0u;
+    }
   }
 }
 // Eight bytes to any address.
@@ -190,6 +221,7 @@ template <int NT, int VPT, bool PART>
 __device__ __forceinline__ void quantise_row(const float (&f)[VPT][8], int64_t row, int tid, int D,
                                              int quant, int group, uint8_t* q_out, float* scale,
                                              float* lds) {
+  const int nt = row_threads<NT>();
   const bool fp8 = quant == 1;
   const float top = fp8 ? 448.f : 127.f;
   const int ngroups = (D + 127) / 128;
@@ -206,7 +238,7 @@ __device__ __forceinline__ void quantise_row(const float (&f)[VPT][8], int64_t r
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, D);
+    const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, D);
     float s = row_scale;
     if (group) {  // 16 consecutive lanes hold a group's 128 columns
       float mx = 0.f;
@@ -227,6 +259,25 @@ __device__ __forceinline__ void quantise_row(const float (&f)[VPT][8], int64_t r
       }
     }
   }
+}
+
+// How a row of D columns is held: by one wave (four rows a block) or by a block
+// of just as many waves as it takes, MOST 8-element steps a thread (one where
+// the row is as short as that).  f(threads of the block, rows of a block, NT,
+// VPT, PART).
+template <int MOST, typename F>
+void by_row(int D, F f) {
+  const int nv = (D + 7) / 8;
+  const std::false_type whole;
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, MOST> most;
+  const std::integral_constant<int, 64> wave;
+  const std::integral_constant<int, 0> block;
+  auto threads = [&](int steps) { return dim3(64 * ((nv + 64 * steps - 1) / (64 * steps))); };
+  if (D < 8) f(dim3(256), 4, wave, one, std::true_type());
+  else if (nv <= 64) f(dim3(256), 4, wave, one, whole);
+  else if (MOST == 2 && nv <= 128) f(dim3(256), 4, wave, most, whole);
+  else f(threads(MOST), 1, block, most, whole);
 }
 
 }  // namespace gdr

@@ -1,6 +1,5 @@
 // ops_api.cpp -- the C ABI of the layer operators: argument validation and
 // workspace sizes.  Host code; validation finishes before the first HIP call.
-#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -177,6 +176,12 @@ static gdr_status check_rows(int rows, int D, int most, gdr_dtype dtype, int qua
     return fail(GDR_ERR_ARG, reason, len, "columns per scale are for quantised outputs");
   return GDR_OK;
 }
+// The same for rows held by 64 threads for each 512 columns.
+static gdr_status check_blocks(int rows, int D, char* reason, size_t len) {
+  if ((int64_t)rows * (64 * ((D + 511) / 512)) > 0xffff0000ll)
+    return fail(GDR_ERR_SHAPE, reason, len, "too many rows (%d of %d columns)", rows, D);
+  return GDR_OK;
+}
 static gdr_status check_stride(const char* name, int64_t stride, int D, char* reason, size_t len) {
   if (stride < D)
     return fail(GDR_ERR_SHAPE, reason, len, "%s_stride=%lld is below D=%d", name, (long long)stride,
@@ -194,12 +199,14 @@ static gdr_status validate(const gdr_gated_norm_problem* p, char* reason, size_t
   if (p->norm_size < 1 || p->D % p->norm_size != 0)
     return fail(GDR_ERR_SHAPE, reason, len, "D must be a multiple of norm_size (D=%d norm_size=%d)",
                 p->D, p->norm_size);
-  // groups that no wave's lanes hold have threads of their own, 64 or 256 each;
-  // their 8-bit outputs 256 a row
-  const int n = p->norm_size;
-  if ((n % 8 != 0 || n > 512 || (n & (n - 1)) != 0) &&
-      p->rows * std::max<int64_t>(256, (int64_t)(p->D / n) * (n <= 1024 ? 64 : 256)) > 0xffff0000ll)
-    return fail(GDR_ERR_SHAPE, reason, len, "too many groups (%d rows of %d)", p->rows, p->D / n);
+  if (p->norm_size < 8 && p->norm_size != p->D)
+    return fail(GDR_ERR_SHAPE, reason, len, "norm_size must be D or at least 8, got %d",
+                p->norm_size);
+  // a group may have 64 threads for each 512 of its columns
+  if ((int64_t)p->rows * (p->D / p->norm_size) * (64 * ((p->norm_size + 511) / 512)) > 0xffff0000ll)
+    return fail(GDR_ERR_SHAPE, reason, len, "too many rows (%d of %d columns in groups of %d)",
+                p->rows, p->D, p->norm_size);
+  if ((s = check_blocks(p->rows, p->D, reason, len)) != GDR_OK) return s;
   if (!is_flag(p->shared_weight) || !is_flag(p->gate_first))
     return fail(GDR_ERR_ARG, reason, len, "shared_weight and gate_first must be 0 or 1");
   if (p->activation != 1 && p->activation != 2)
@@ -214,6 +221,7 @@ static gdr_status validate(const gdr_sandwich_norm_problem* p, char* reason, siz
   if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
   gdr_status s = check_rows(p->rows, p->D, 16384, p->dtype, p->quant, p->group_size, reason, len);
   if (s != GDR_OK) return s;
+  if ((s = check_blocks(p->rows, p->D, reason, len)) != GDR_OK) return s;
   if (p->res_dtype != p->dtype && p->res_dtype != GDR_FP32)
     return fail(GDR_ERR_DTYPE, reason, len, "the residual must have x's dtype or fp32 (got code %d)",
                 (int)p->res_dtype);

@@ -46,10 +46,11 @@ struct SandwichArgs {
 template <int NT, int VPT, bool PART>
 __device__ __forceinline__ float row_rstd(const float (&f)[VPT][8], int tid, int D, float eps,
                                           float* lds) {
+  const int nt = row_threads<NT>();
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, D);
+    const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, D);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const double v = c + e >= v0 ? f[i][e] : 0.f;
@@ -57,16 +58,16 @@ __device__ __forceinline__ float row_rstd(const float (&f)[VPT][8], int tid, int
     }
   }
   sum = row_sum<NT>(sum, reinterpret_cast<double*>(lds));
-  return (float)(1.0 / __builtin_sqrt(sum / D + (double)eps));
+  return inverse_root(sum / D + (double)eps);
 }
 
 // The forward.
 template <typename T, typename R, bool QUANT, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichArgs a) {
   __shared__ __align__(8) float lds[32];
-  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x, nt = row_threads<NT>();
   const int64_t row = NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (row >= a.rows) return;  // a whole wave; the barriers below are for NT > 64 only
+  if (row >= a.rows) return;  // a whole wave; the barriers below are for rows of a block
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
   const T* gate = reinterpret_cast<const T*>(a.gate) + row * a.gate_stride;
   const R* res = reinterpret_cast<const R*>(a.res) + row * a.D;
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
   float f[VPT][8], r[VPT][8], g[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = column_of<PART>(i * NT + tid, a.D);
+    const int c = column_of<PART>(i * nt + tid, a.D);
     load8<T, PART>(x + c, a.D, f[i]);
     load8<R, PART>(res + c, a.D, r[i]);
     if (a.gate) load8<T, PART>(gate + c, a.D, g[i]);
@@ -85,14 +86,14 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       float w[8];
-      load_weight<PART>(a.post, column_of<PART>(i * NT + tid, a.D), a.D, a.wdt, w);
+      load_weight<PART>(a.post, column_of<PART>(i * nt + tid, a.D), a.D, a.wdt, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * rstd * w[e];
     }
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+    const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, a.D);
     if (a.gate) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[i][e] *= gate_of(g[i][e], a.act);
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
   if (a.rstd_h && tid == 0) a.rstd_h[row] = rstd;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+    const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, a.D);
     float w[8];
     load_weight<PART>(a.pre, c, a.D, a.wdt, w);
 #pragma unroll
@@ -136,12 +137,12 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
 // A block walks rows blockIdx.x, + blocks, ... with dw2 and P in registers and
 // leaves its sums in `part`.
 template <typename T, typename R, int NT, int VPT, bool PART>
-__global__ __launch_bounds__(block_of<NT>()) void sandwich_bwd_kernel(SandwichArgs a) {
+__global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(SandwichArgs a) {
   constexpr int RPB = NT == 64 ? 4 : 1;
-  constexpr int COLS = NT * VPT * 8;
+  constexpr int COLS = 64 * VPT * 8;  // of a wave's row
   __shared__ float lds[16];
   __shared__ float wsum[NT == 64 ? 4 * COLS : 1];
-  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x, nt = row_threads<NT>();
   const int q = NT == 64 ? (threadIdx.x >> 6) : 0;
   float dw[VPT][8], P[VPT][8];
 #pragma unroll
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_bwd_kernel(SandwichAr
     float u[VPT][8], d[VPT][8], g[VPT][8], ux[VPT][8], s[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = column_of<PART>(i * NT + tid, a.D);
+      const int c = column_of<PART>(i * nt + tid, a.D);
       load8<R, PART>(h + c, a.D, u[i]);
       load8<T, PART>(dy + c, a.D, d[i]);
       load8<T, PART>(x + c, a.D, ux[i]);
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_bwd_kernel(SandwichAr
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+      const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, a.D);
       float w[8];
       load_weight<PART>(a.pre, c, a.D, a.wdt, w);
 #pragma unroll
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_bwd_kernel(SandwichAr
     float dot2 = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v0 = (i * NT + tid) * 8, c = column_of<PART>(i * NT + tid, a.D);
+      const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, a.D);
       float w[8], sc[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = 1.f, sc[e] = a.alpha;
@@ -204,7 +205,8 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_bwd_kernel(SandwichAr
         store8<R, PART>(reinterpret_cast<R*>(a.dres) + row * a.D + c, a.D, g[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const Gate t = a.gate ? gate_and_slope(s[i][e], a.act) : Gate{1.f, 0.f};
+        const float z = gate_input(s[i][e]);
+        const Gate t = a.gate ? gate_and_slope(a.act ? z : s[i][e], sigmoid(z), a.act) : Gate{1.f, 0.f};
         ux[i][e] *= rx;
         const float b = g[i][e] * ux[i][e];
         P[i][e] += b * t.value;
@@ -224,18 +226,18 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_bwd_kernel(SandwichAr
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if ((i * NT + tid) * 8 < a.D)
+      if ((i * nt + tid) * 8 < a.D)
         store8<T, PART>(reinterpret_cast<T*>(a.dx) + row * a.D +
-                            column_of<PART>(i * NT + tid, a.D), a.D, d[i]);
+                            column_of<PART>(i * nt + tid, a.D), a.D, d[i]);
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float* part = a.part + ((int64_t)k * a.blocks + blockIdx.x) * a.D;
-    if (NT > 64) {
+    if (NT == 0) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
-        if ((i * NT + tid) * 8 < a.D)
-          store8<float, PART>(part + column_of<PART>(i * NT + tid, a.D), a.D, k ? P[i] : dw[i]);
+        if ((i * nt + tid) * 8 < a.D)
+          store8<float, PART>(part + column_of<PART>(i * nt + tid, a.D), a.D, k ? P[i] : dw[i]);
     } else {
       // columns of the block's four rows, each at its vector's place
       __syncthreads();
@@ -282,40 +284,6 @@ __global__ __launch_bounds__(256) void sandwich_reduce_kernel(SandwichArgs a, vo
   if (dscale) store_scalar(dscale, c, a.wdt, a.post ? s * load_scalar(a.post, c, a.wdt) : s);
 }
 
-#define GDR_W(NT, VPT) \
-  if (nv <= NT * VPT)  \
-  return f(std::integral_constant<int, NT>(), std::integral_constant<int, VPT>(), whole)
-// Threads per row and 8-element steps per thread, as the norm without a gate
-// has them up to its 16,384 columns.
-template <typename F>
-void by_width(int D, F f) {
-  const int nv = (D + 7) / 8;
-  const std::false_type whole;
-  if (D < 8)
-    return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>(), std::true_type());
-  GDR_W(64, 1);
-  GDR_W(64, 2);
-  GDR_W(256, 1);
-  GDR_W(256, 2);
-  GDR_W(256, 4);
-  GDR_W(256, 8);
-}
-// The gradient holds seven arrays of a row: at most two steps a thread.
-template <typename F>
-void by_width_bwd(int D, F f) {
-  const int nv = (D + 7) / 8;
-  const std::false_type whole;
-  if (D < 8)
-    return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>(), std::true_type());
-  GDR_W(64, 1);
-  GDR_W(64, 2);
-  GDR_W(256, 1);
-  GDR_W(256, 2);
-  GDR_W(512, 2);
-  GDR_W(1024, 2);
-}
-#undef GDR_W
-
 // The input's and the residual's types.
 template <typename F>
 void by_type(const gdr_sandwich_norm_problem* p, F f) {
@@ -328,11 +296,22 @@ void by_type(const gdr_sandwich_norm_problem* p, F f) {
   else f(float(), float());
 }
 
+// The gradient holds seven arrays of a row: one step a thread as far as a block
+// reaches.
+template <typename F>
+void by_row_bwd(int D, F f) {
+  if (D <= 8192) return by_row<1>(D, f);
+  f(dim3(64 * ((D + 1023) / 1024)), 1, std::integral_constant<int, 0>(),
+    std::integral_constant<int, 2>(), std::false_type());
+}
+
 int bwd_blocks(const gdr_sandwich_norm_problem* p) {
-  // as the norm without a gate: at least 8 rows a block, at most 1024 blocks
-  const int rpb = p->D <= 1024 ? 4 : 1;
-  const int64_t want = ((int64_t)p->rows + 8 * rpb - 1) / (8 * rpb);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, 1024));
+  // 4096 waves fill the card; at least 8 rows a block, against its partial sums
+  int64_t blocks = 1;
+  by_row_bwd(p->D, [&](dim3 block, int rows, auto, auto, auto) {
+    blocks = std::min<int64_t>(4096 * 64 / block.x, ((int64_t)p->rows + 8 * rows - 1) / (8 * rows));
+  });
+  return (int)std::max<int64_t>(1, blocks);
 }
 
 SandwichArgs args_of(const gdr_sandwich_norm_problem* p) {
@@ -362,10 +341,9 @@ gdr_status launch_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const vo
   by_type(p, [&](auto t, auto r) {
     using T = decltype(t);
     using R = decltype(r);
-    by_width(p->D, [&](auto nt, auto vpt, auto part) {
+    by_row<2>(p->D, [&](dim3 block, int rows, auto nt, auto vpt, auto part) {
       constexpr int NT = nt.value, VPT = vpt.value;
-      const dim3 grid((unsigned)(NT == 64 ? (p->rows + 3) / 4 : p->rows));
-      const dim3 block(block_of<NT>());
+      const dim3 grid((unsigned)(((int64_t)p->rows + rows - 1) / rows));
       if (p->quant)
         GDR_LAUNCH("sandwich_fwd", (sandwich_fwd_kernel<T, R, true, NT, VPT, part.value>), grid,
                    block, st, a);
@@ -398,10 +376,10 @@ gdr_status launch_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const vo
   by_type(p, [&](auto t, auto r) {
     using T = decltype(t);
     using R = decltype(r);
-    by_width_bwd(p->D, [&](auto nt, auto vpt, auto part) {
+    by_row_bwd(p->D, [&](dim3 block, int, auto nt, auto vpt, auto part) {
       constexpr int NT = nt.value, VPT = vpt.value;
       GDR_LAUNCH("sandwich_bwd", (sandwich_bwd_kernel<T, R, NT, VPT, part.value>), dim3(a.blocks),
-                 dim3(block_of<NT>()), st, a);
+                 block, st, a);
     });
   });
   GDR_LAUNCH("sandwich_reduce", sandwich_reduce_kernel,

@@ -56,8 +56,9 @@ BAD = [
     (gated(norm_size=-128), "GDR_ERR_SHAPE", "multiple"),
     (gated(norm_size=512), "GDR_ERR_SHAPE", "multiple"),
     (gated(rows=1 << 28), "GDR_ERR_SHAPE", "rows"),
-    (gated(rows=1 << 20, norm_size=2), "GDR_ERR_SHAPE", "groups"),
-    (gated(rows=1 << 25, D=12, norm_size=12, x_stride=12), "GDR_ERR_SHAPE", "groups"),
+    (gated(norm_size=4), "GDR_ERR_SHAPE", "at least 8"),
+    (gated(rows=1 << 23, D=8192, x_stride=8192, gate_stride=8192), "GDR_ERR_SHAPE", "rows"),
+    (sandwich(rows=1 << 23, D=8192, x_stride=8192, gate_stride=8192), "GDR_ERR_SHAPE", "rows"),
     (gated(x_stride=255), "GDR_ERR_SHAPE", "x_stride"),
     (gated(gate_stride=255), "GDR_ERR_SHAPE", "gate_stride"),
     (gated(dtype=5), "GDR_ERR_DTYPE", "x must"),

@@ -49,7 +49,11 @@ GATED = {
     "half_wave": (70, 768, 256, BF, False, None),
     "whole_wave": (3, 16384, 512, HF, True, None),
     "row_ends_in_a_step": (11, 2304, 64, F32, True, None),
-    "few_columns": (6, 12, 3, BF, True, None),
+    "few_columns": (6, 7, 7, BF, True, None),
+    "few_in_segments": (6, 18, 9, BF, True, None),
+    "segments_that_end_in_vectors": (5, 1001, 13, F32, False, None),
+    "many_segments": (3, 16380, 12, HF, True, F32),
+    "wide_segments": (3, 15990, 5330, BF, False, None),
     "odd_groups": (17, 5005, 715, HF, False, F32),
     "odd_groups_shared": (33, 4995, 45, BF, True, None),
     "wide_groups": (4, 8192, 4096, BF, False, None),
@@ -81,6 +85,8 @@ def test_gated_forward_and_gradients(name, first, act):
 @pytest.mark.parametrize("group", [0, 128])
 @pytest.mark.parametrize("fmt", ["fp8", "int8"])
 @pytest.mark.parametrize("name", ["one_value", "heads", "heads_own_weights", "groups_of_16", "whole_wave",
+                                  "few_in_segments", "segments_that_end_in_vectors", "many_segments",
+                                  "wide_segments",
                                   "row_ends_in_a_step", "few_columns", "odd_groups",
                                   "odd_groups_shared", "wide_groups", "one_group", "widest"])
 def test_gated_eight_bits(name, fmt, group):
