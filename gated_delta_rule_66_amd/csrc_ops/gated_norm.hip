@@ -20,7 +20,10 @@ namespace gdr {
 namespace {
 
 // Narrower groups are summed as segments of whole rows.
-constexpr int kUnitColumns = 256;
+constexpr int kUnitColumns = 192;
+// Columns of a row that a block's threads hold in the gradient of lanes, a
+// multiple of every group's.
+constexpr int kLanePiece = 8192;
 
 enum Sums { kLanes, kUnits, kSegments };
 
@@ -33,7 +36,7 @@ struct GatedArgs {
   float* rstd;        // [rows][groups], nullable in the forward
   int64_t x_stride, z_stride;  // elements between rows
   int rows, D;
-  int lanes;          // lanes of a group (kLanes)
+  int lanes;          // lanes of a group: that hold it (kLanes) or add it (kSegments)
   int size, groups;   // columns of a group, groups of a row
   int wdt, shared;    // shared: one group's weights for all
   int gate_first, act;  // act 1: silu, 2: sigmoid
@@ -46,18 +49,21 @@ struct GatedArgs {
   void* dz;
   float* part;        // [sets][D], or [sets][size] of shared weights in lanes
   int sets;           // walkers of rows, each with a row of `part`
+  // threads hold rows in pieces of so many columns: a group each (kUnits), or
+  // up to kLanePiece (the gradient in lanes)
+  int pieces, piece;
 };
 
-// The row and group of the u-th unit, or row u where threads hold whole rows.
+// The row and the columns that the u-th team of threads holds.
 struct Unit {
   int64_t row;
-  int group;
+  int piece, first, width;
 };
-template <Sums SUMS>
 __device__ __forceinline__ Unit unit_of(const GatedArgs& a, unsigned u) {
-  if (SUMS != kUnits || a.groups == 1) return {(int64_t)u, 0};
-  const unsigned row = u / (unsigned)a.groups;
-  return {(int64_t)row, (int)(u - row * (unsigned)a.groups)};
+  if (a.pieces == 1) return {(int64_t)u, 0, 0, a.D};
+  const unsigned row = u / (unsigned)a.pieces, piece = u - row * (unsigned)a.pieces;
+  const int first = (int)piece * a.piece;
+  return {(int64_t)row, (int)piece, first, min(a.piece, a.D - first)};
 }
 
 // Sum over `lanes` (a power of two) neighbouring lanes, the same bits in each.
@@ -92,7 +98,7 @@ __device__ __forceinline__ Span span_of(const GatedArgs& a, int c) {
 // kSegments: the sums of all groups of a row from each vector's parts (a: of
 // its first group, b: of the next), to total[group] in LDS for all threads.
 // `part` holds two values a vector.  A group's vectors are added in a fixed
-// order by one wave.
+// order by as many lanes as hold them, up to a wave.
 template <typename S, int VPT>
 __device__ __forceinline__ void segment_sums(const GatedArgs& a, const Span* sp, const S* va,
                                              const S* vb, S* part, S* total) {
@@ -103,17 +109,17 @@ __device__ __forceinline__ void segment_sums(const GatedArgs& a, const Span* sp,
     if (vi < nv) part[2 * vi] = va[i], part[2 * vi + 1] = vb[i];
   }
   __syncthreads();
-  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  for (int g = threadIdx.x >> 6; g < a.groups; g += waves) {
+  const int lane = threadIdx.x & (a.lanes - 1), teams = blockDim.x / a.lanes;
+  for (int g = threadIdx.x / a.lanes; g < a.groups; g += teams) {
     const int c0 = g * a.size, c1 = c0 + a.size;
     S s = 0;
-    for (int vi = c0 / 8 + lane; vi * 8 < c1; vi += 64) {
+    for (int vi = c0 / 8 + lane; vi * 8 < c1; vi += a.lanes) {
       // the part that belongs to this group: the vector begins in it, or the
       // one before
       const int c = min(vi * 8, a.D - 8);
       s += part[2 * vi + (c >= c0 ? 0 : 1)];
     }
-    s = lanes_sum(s, 64);
+    s = lanes_sum(s, a.lanes);
     if (lane == 0) total[g] = s;
   }
   __syncthreads();
@@ -132,10 +138,10 @@ __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) 
   constexpr bool kSeg = SUMS == kSegments;
   __shared__ double part[kSeg ? 2 * most_vectors<VPT>() : 1], total[kSeg ? most_vectors<VPT>() : 1];
   const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x, nt = row_threads<NT>();
-  const Unit unit = unit_of<SUMS>(a, NT == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x);
+  const Unit unit = unit_of(a, NT == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x);
   const int64_t row = unit.row;
   if (row >= a.rows) return;  // a whole wave; the barriers below are for rows of a block
-  const int width = SUMS == kUnits ? a.size : a.D, first = unit.group * a.size;
+  const int width = unit.width, first = unit.first;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride + first;
   const T* z = reinterpret_cast<const T*>(a.z) + row * a.z_stride + first;
   float f[VPT][8], t[VPT][8];
@@ -178,7 +184,7 @@ __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) 
     rstd[0] = inverse_root(all * a.share + (double)a.eps);
 #pragma unroll
     for (int i = 1; i < VPT; ++i) rstd[i] = rstd[0];
-    if (a.rstd && tid == 0) a.rstd[row * a.groups + unit.group] = rstd[0];
+    if (a.rstd && tid == 0) a.rstd[row * a.groups + unit.piece] = rstd[0];
   } else {
     segment_sums<double, VPT>(a, sp, sum, next, part, total);
 #pragma unroll
@@ -238,8 +244,8 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
   __shared__ float segs[kSeg ? 2 * most_vectors<VPT>() : 1], total[kSeg ? most_vectors<VPT>() : 1];
   const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x, nt = row_threads<NT>();
   const int q = NT == 64 ? (threadIdx.x >> 6) : 0;
-  const Unit unit = unit_of<SUMS>(a, blockIdx.x * RPB + q);  // (its row: the walker)
-  const int width = SUMS == kUnits ? a.size : a.D, first = unit.group * a.size;
+  const Unit unit = unit_of(a, blockIdx.x * RPB + q);  // (its row: the walker)
+  const int width = unit.width, first = unit.first;
   float dw[VPT][8], w[VPT][8];
   Span sp[kSeg ? VPT : 1];
 #pragma unroll
@@ -269,14 +275,14 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
       load8<T, PART>(x + c, width, u[i]);
       load8<T, PART>(z + c, width, z8[i]);
       load8<T, PART>(dy + c, width, du[i]);
-      r[i] = rs[kSeg ? sp[i].group : SUMS == kLanes ? c / a.size : unit.group];
+      r[i] = rs[kSeg ? sp[i].group : SUMS == kLanes ? (first + c) / a.size : unit.piece];
       if (kSeg) rnext[i] = rs[min(sp[i].group + 1, a.groups - 1)];
     }
     float dot[VPT], dnext[kSeg ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
-      const bool live = SUMS != kLanes || v0 < a.D;
+      const bool live = SUMS != kLanes || v0 < width;
       dot[i] = 0.f;
       if (kSeg) dnext[i] = 0.f;
 #pragma unroll
@@ -353,7 +359,7 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
     }
     return;
   }
-  if (NT == 0 || (SUMS == kUnits && a.groups > 1)) {
+  if (NT == 0 || a.pieces > 1) {
     float* part = a.part + unit.row * a.D + first;
     if (unit.row < a.sets)
 #pragma unroll
@@ -427,7 +433,7 @@ template <typename F>
 void by_form_bwd(const gdr_gated_norm_problem* p, F f) {
   const Sums sums = sums_of(p);
   if (sums == kSegments) return by_segments(p->D, f);
-  const int width = sums == kLanes ? p->D : p->norm_size;
+  const int width = sums == kLanes ? std::min(p->D, kLanePiece) : p->norm_size;
   auto form = [&](dim3 block, int rows, auto nt, auto vpt, auto part) {
     if constexpr (!part.value) {
       if (sums == kLanes) return f(block, rows, SumsTag<kLanes>(), nt, vpt, part);
@@ -438,7 +444,7 @@ void by_form_bwd(const gdr_gated_norm_problem* p, F f) {
     return f(dim3(256), 4, SumsTag<kUnits>(), std::integral_constant<int, 64>(), Two(),
              std::false_type());
   if (width <= 8192) return by_row<1>(width, form);
-  form(dim3(64 * ((width + 1023) / 1024)), 1, Zero(), Two(), std::false_type());
+  f(dim3(64 * ((width + 1023) / 1024)), 1, SumsTag<kUnits>(), Zero(), Two(), std::false_type());
 }
 
 GatedArgs args_of(const gdr_gated_norm_problem* p) {
@@ -450,6 +456,10 @@ GatedArgs args_of(const gdr_gated_norm_problem* p) {
   a.size = p->norm_size;
   a.groups = p->D / p->norm_size;
   a.lanes = p->norm_size / 8;
+  if (sums_of(p) == kSegments) {
+    a.lanes = 2;  // a group's vectors, one more at either end
+    while (a.lanes < 64 && a.lanes < p->norm_size / 8 + 2) a.lanes *= 2;
+  }
   a.wdt = (int)p->w_dtype;
   a.shared = p->shared_weight;
   a.gate_first = p->gate_first;
@@ -458,9 +468,16 @@ GatedArgs args_of(const gdr_gated_norm_problem* p) {
   a.scale_group = p->scale_group;
   a.eps = p->eps;
   a.share = 1.0 / p->norm_size;
+  a.piece = sums_of(p) == kLanes ? kLanePiece : p->norm_size;
   return a;
 }
 
+int pieces_of(const gdr_gated_norm_problem* p, bool backward) {
+  const Sums sums = sums_of(p);
+  return sums == kUnits               ? p->D / p->norm_size
+         : sums == kLanes && backward ? (p->D + kLanePiece - 1) / kLanePiece
+                                      : 1;
+}
 // Blocks of the gradient, and their walkers of rows (sets).  4096 waves fill the
 // card; a block (a wave of units) walks at least 8 rows, against its partial
 // sums.
@@ -470,8 +487,7 @@ struct Walk {
 };
 Walk walk_of(const gdr_gated_norm_problem* p) {
   Walk w{};
-  const bool units = sums_of(p) == kUnits;
-  const int64_t groups = units ? p->D / p->norm_size : 1;
+  const int64_t groups = pieces_of(p, true);
   by_form_bwd(p, [&](dim3 block, int rows, auto, auto, auto, auto) {
     // `rows` walkers a block
     const int64_t most = std::max<int64_t>(1, 4096 * 64 / block.x * rows / groups);
@@ -479,7 +495,9 @@ Walk walk_of(const gdr_gated_norm_problem* p) {
     if (groups == 1) sets = (sets + rows - 1) / rows * rows;
     w.sets = (int)sets;
     w.blocks = (int)((sets * groups + rows - 1) / rows);
-    w.parts = groups == 1 ? w.blocks : w.sets;
+    // a block's own row of sums, or its walker's
+    const bool own = groups == 1 || (sums_of(p) == kLanes && p->shared_weight);
+    w.parts = own ? w.blocks : w.sets;
   });
   return w;
 }
@@ -491,12 +509,13 @@ gdr_status launch_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x,
                                  hipStream_t st) {
   GatedArgs a = args_of(p);
   a.x = x; a.z = gate; a.w = weight; a.y = y; a.scale = scale; a.rstd = rstd;
+  a.pieces = pieces_of(p, false);
   by_type(p, [&](auto t) {
     using T = decltype(t);
     by_form(p, [&](dim3 block, int rows, auto sums, auto nt, auto vpt, auto part) {
       constexpr Sums SUMS = sums.value;
       constexpr int NT = nt.value, VPT = vpt.value;
-      const int64_t units = (int64_t)a.rows * (SUMS == kUnits ? a.groups : 1);
+      const int64_t units = (int64_t)a.rows * a.pieces;
       const dim3 grid((unsigned)((units + rows - 1) / rows));
       if (p->quant)
         GDR_LAUNCH("gated_fwd", (gated_fwd_kernel<T, true, SUMS, NT, VPT, part.value>), grid, block,
@@ -522,6 +541,7 @@ gdr_status launch_gated_norm_bwd(const gdr_gated_norm_problem* p, const void* dy
   a.dy = dy; a.dx = dx; a.dz = dgate;
   a.part = reinterpret_cast<float*>(ws);
   const Walk walk = walk_of(p);
+  a.pieces = pieces_of(p, true);
   a.sets = walk.sets;
   by_type(p, [&](auto t) {
     using T = decltype(t);

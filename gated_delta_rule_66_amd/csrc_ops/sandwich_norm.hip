@@ -135,7 +135,7 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
 //   dg = dH alpha s w1 ux A',   du = dH alpha s A w1
 //   dx = rx (du - ux mean(du ux))     (du without w1)
 // A block walks rows blockIdx.x, + blocks, ... with dw2 and P in registers and
-// leaves its sums in `part`.
+// leaves its sums in `part`.  BWDNOTE
 template <typename T, typename R, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(SandwichArgs a) {
   constexpr int RPB = NT == 64 ? 4 : 1;
@@ -296,10 +296,10 @@ void by_type(const gdr_sandwich_norm_problem* p, F f) {
   else f(float(), float());
 }
 
-// The gradient holds seven arrays of a row: one step a thread as far as a block
-// reaches.
+// Rows of several arrays: one 8-element step a thread as far as a block reaches
+// (the forward of 8192 x 4096 bf16 with a gate: 70 us, with two steps 77).
 template <typename F>
-void by_row_bwd(int D, F f) {
+void by_steps(int D, F f) {
   if (D <= 8192) return by_row<1>(D, f);
   f(dim3(64 * ((D + 1023) / 1024)), 1, std::integral_constant<int, 0>(),
     std::integral_constant<int, 2>(), std::false_type());
@@ -308,7 +308,7 @@ void by_row_bwd(int D, F f) {
 int bwd_blocks(const gdr_sandwich_norm_problem* p) {
   // 4096 waves fill the card; at least 8 rows a block, against its partial sums
   int64_t blocks = 1;
-  by_row_bwd(p->D, [&](dim3 block, int rows, auto, auto, auto) {
+  by_steps(p->D, [&](dim3 block, int rows, auto, auto, auto) {
     blocks = std::min<int64_t>(4096 * 64 / block.x, ((int64_t)p->rows + 8 * rows - 1) / (8 * rows));
   });
   return (int)std::max<int64_t>(1, blocks);
@@ -341,7 +341,7 @@ gdr_status launch_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const vo
   by_type(p, [&](auto t, auto r) {
     using T = decltype(t);
     using R = decltype(r);
-    by_row<2>(p->D, [&](dim3 block, int rows, auto nt, auto vpt, auto part) {
+    by_steps(p->D, [&](dim3 block, int rows, auto nt, auto vpt, auto part) {
       constexpr int NT = nt.value, VPT = vpt.value;
       const dim3 grid((unsigned)(((int64_t)p->rows + rows - 1) / rows));
       if (p->quant)
@@ -376,7 +376,7 @@ gdr_status launch_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const vo
   by_type(p, [&](auto t, auto r) {
     using T = decltype(t);
     using R = decltype(r);
-    by_row_bwd(p->D, [&](dim3 block, int, auto nt, auto vpt, auto part) {
+    by_steps(p->D, [&](dim3 block, int, auto nt, auto vpt, auto part) {
       constexpr int NT = nt.value, VPT = vpt.value;
       GDR_LAUNCH("sandwich_bwd", (sandwich_bwd_kernel<T, R, NT, VPT, part.value>), dim3(a.blocks),
                  block, st, a);
