@@ -363,7 +363,7 @@ def int8_matmul(x, x_scale, weight, w_scale, bias=None, out_dtype=torch.bfloat16
         weight = _moved(weight)
     p = Int8MatmulProblem(M, N, K, out, out if bias is None else _DT[bias.dtype], stride)
     ref = ctypes.byref(p)
-    n = lib.gdr_int8_matmul_workspace_size(ref) if M > 64 else 0
+    n = lib.gdr_int8_matmul_workspace_size(ref) if (K | stride) % 16 else 0
     ws = _bytes(n, dev) if n else None
     y = x.new_empty(lead + (N,), dtype=out_dtype)
     _launch(x, lib.gdr_int8_matmul, ref, _ptr(src), _ptr(x_scale), _ptr(weight), _ptr(w_scale),

@@ -150,9 +150,22 @@ __device__ __forceinline__ float inverse_root(double a) {
 // exponential is taken at -80 at the least, where the sigmoid is 2^-115: with
 // an infinity it would make silu's limit 0 and the slopes' products NaN.
 __device__ __forceinline__ float gate_input(float z) { return z < -80.f ? -80.f : z; }  // a NaN passes
+// The sigmoid of such a z to fp32's precision: the exponent's rounding is added
+// to the power, and the reciprocal's estimate gets a step of Newton's (with the
+// instructions alone a 16-bit stream's roundings fell the other way twice as
+// often as an exact gate's).
+__device__ __forceinline__ float gate_sigmoid(float z) {
+  constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911e-8f, kLn2 = 0.6931471805599453f;
+  const float p = -z * kLog2e;
+  const float rest = __builtin_fmaf(-z, kRest, __builtin_fmaf(-z, kLog2e, -p));
+  float e = __builtin_amdgcn_exp2f(p);
+  e = p < -150.f ? 0.f : __builtin_fmaf(e, rest * kLn2, e);  // (z = inf: the rest is NaN)
+  const float d = 1.f + e, r = fast_rcp(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+}
 __device__ __forceinline__ float gate_of(float z, int act) {
   if (act == 0) return z;
-  const float zc = gate_input(z), s = sigmoid(zc);
+  const float zc = gate_input(z), s = gate_sigmoid(zc);
   return act == 1 ? zc * s : s;
 }
 struct Gate {

@@ -717,9 +717,9 @@ typedef struct {
 gdr_status gdr_int8_matmul_check(const gdr_int8_matmul_problem* p, char* reason, size_t reason_len);
 
 /* Weights of rows of a multiple of 16 bytes (K) begin at a multiple of 16
- * bytes, and so does x if its stride is one, too.  The workspace (possibly of
- * size 0, and of none for up to 64 tokens) is 16-byte aligned: rows of other
- * lengths are copied there. */
+ * bytes, and so does x if its stride is one, too.  The workspace (of size 0
+ * where K and x_stride are multiples of 16, and possibly elsewhere) is 16-byte
+ * aligned: rows of other lengths are copied there. */
 size_t gdr_int8_matmul_workspace_size(const gdr_int8_matmul_problem* p);
 gdr_status gdr_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, const float* x_scale,
                            const void* weight, const float* w_scale, const void* bias, void* y,

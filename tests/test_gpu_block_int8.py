@@ -52,7 +52,9 @@ def test_lengths_of_the_sum(K):
     (64, 31, 4096), (65, 4099, 48), (100, 257, 2505), (256, 4096, 512), (129, 16384, 128),
     (1000, 2500, 192), (1000, 2500, 177), (2049, 1025, 176), (2049, 1025, 175), (4097, 4098, 80), (4097, 4098, 16),
     (4097, 4098, 79), (5000, 4000, 272), (300, 60000, 64), (60000, 300, 64), (16641, 1024, 128),
-    (200001, 90, 32), (3, 300001, 32)])
+    (200001, 90, 32), (3, 300001, 32),
+    # rows that are padded for few tokens, or read where they lie
+    (64, 12288, 1025), (33, 4100, 2049), (16, 12288, 513), (1, 12288, 514), (20, 9000, 4100)])
 def test_sizes(M, N, K):
     t = make(M, N, K, seed=M)
     for out, bdt in ((BF, BF), (HF, F32)) if M * N > 1 << 22 else ((BF, BF), (HF, F32), (F32, F32)):
@@ -60,6 +62,18 @@ def test_sizes(M, N, K):
         held(t, run(t, out), out)
     t["bias"] = None
     held(t, run(t, BF), BF)
+
+
+def test_workspaces():
+    """None where rows are multiples of 16 bytes; for few tokens, too, elsewhere."""
+    size = lambda M, N, K, stride: _lib.lib.gdr_int8_matmul_workspace_size(  # noqa: E731
+        ctypes.byref(_lib.Int8MatmulProblem(M, N, K, 0, 0, stride)))
+    for M in (1, 20, 64, 65, 300, 3000, 20000):
+        for N in (1, 70, 4096, 12288):
+            assert size(M, N, 4096, 4096) == size(M, N, 16, 4096) == 0
+    assert size(64, 12288, 4097, 4097) >= (64 + 12288) * 4112
+    assert size(3000, 4096, 4096, 4097) >= 3000 * 4096
+    assert size(3000, 4096, 4096, 4097) < 4096 * 4096
 
 
 def test_largest_sums_are_exact():
