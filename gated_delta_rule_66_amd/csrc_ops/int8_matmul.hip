@@ -5,6 +5,11 @@
 // what is rounded is the sum's conversion to fp32, the products with the
 // scales and the output.
 //
+// 18,062 tokens by 12,288 channels of K = 4096 take 845 to 890 us (2.1 to 2.15
+// POPS with random values; a library's product with 32-bit sums as its output
+// 810 to 870), 2903 x 5003 of K = 2505 59, 48 of them the product, 64 x 12,288 11,
+// 1 x 12,288 10 (5 TB/s).
+//
 // The weights are the matrix instruction's first operand and the tokens its
 // second, so that a lane ends with four consecutive channels of one token.
 #include <algorithm>
@@ -181,6 +186,15 @@ __device__ __forceinline__ void load_to_lds(u32x4 rs, int at, int off) {
 // run.  One barrier a step, before its last products: by then every wave has
 // read this step's tiles, whose place the request for STEPS steps on takes, and
 // waited for its own loads of the next one's.
+//
+// What bounds 256 x 256 tiles is power: 18,062 x 12,288 x 4096 take 850 us with
+// random values and 678 with zeros, at matrix units busy for half of the cycles
+// of a clock that falls to 1.6 GHz.  Left out in copies, the loads to LDS cost 130
+// us of the 850, the reads of operands 50; products alone take 670.  The loads
+// alone take 621 (22 bytes a cycle and CU, whatever the order of a row's pieces).
+// Steps of 64 bytes, four in flight: 913 us.  Small problems wait for loads:
+// there tiles of 64 x 64 keep four steps in flight (512 x 4096 x 4096 15 us; two
+// steps 17, 128 x 128 tiles 23).
 template <int KB>
 __device__ __forceinline__ int swizzle(int r) {
   static_assert(KB == 64 || KB == 128, "bytes of a row");
@@ -284,10 +298,12 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(MatArgs a) {
     for (int q = 0; q + 1 < Q; ++q) {
       operands(at, q + 1);
       __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);  // over the wave that reads operands
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int j = 0; j < MB; ++j) product(q & 1, i, j);
+      __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };

@@ -7,6 +7,14 @@
 
 namespace gdr {
 
+// GDR_LAUNCH with `lds` bytes (up to 64 KiB) that the kernel declares extern.
+#define GDR_LAUNCH_LDS(name, kernel, grid, block, lds, st, ...)        \
+  do {                                                                 \
+    if (::gdr::g_profiling) ::gdr::profile_begin(st, name);            \
+    hipLaunchKernelGGL(kernel, grid, block, lds, st, __VA_ARGS__);     \
+    if (::gdr::g_profiling) ::gdr::profile_end(st);                    \
+  } while (0)
+
 // Launch failures become a status; `what` names the operator.
 gdr_status launch_status(const char* what);
 

@@ -61,7 +61,9 @@ __device__ __forceinline__ float row_rstd(const float (&f)[VPT][8], int tid, int
   return inverse_root(sum / D + (double)eps);
 }
 
-// The forward.
+// The forward.  8192 rows of 4096 bf16 columns with a gate take 70 us for 336 MB
+// (4.8 TB/s), 4099 of 5003 fp16 columns with a residual in fp32 56 us for 246 MB
+// (4.4): two sums over the row one after the other.  Eight rows to int8 take 6 us.
 template <typename T, typename R, bool QUANT, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichArgs a) {
   __shared__ __align__(8) float lds[32];
@@ -135,20 +137,46 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
 //   dg = dH alpha s w1 ux A',   du = dH alpha s A w1
 //   dx = rx (du - ux mean(du ux))     (du without w1)
 // A block walks rows blockIdx.x, + blocks, ... with dw2 and P in registers and
-// leaves its sums in `part`.  BWDNOTE
+// leaves its sums in `part`.  8192 x 4096 with a gate take 117 us for 537 MB (4.6
+// TB/s): eight streams, two sums, 102 registers and so two rows of 512 threads a
+// CU.  Beyond 8192 columns dw2 and P lie in LDS and 48 registers are spilled (34
+// MB of columns: 220 us of 16,384, 135 of 8192).
 template <typename T, typename R, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(SandwichArgs a) {
   constexpr int RPB = NT == 64 ? 4 : 1;
   constexpr int COLS = 64 * VPT * 8;  // of a wave's row
+  constexpr bool kWeights = VPT == 1;  // LDS holds them beside the rows
   __shared__ float lds[16];
   __shared__ float wsum[NT == 64 ? 4 * COLS : 1];
   const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x, nt = row_threads<NT>();
   const int q = NT == 64 ? (threadIdx.x >> 6) : 0;
-  float dw[VPT][8], P[VPT][8];
+  // w2 and alpha s w1 by columns, in fp32
+  extern __shared__ __align__(16) float weights[];
+  float* w2 = weights;
+  float* sw1 = weights + a.D;
+  if (kWeights) {
+    for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+      w2[c] = load_scalar(a.pre, c, a.wdt);
+      float v = a.alpha;
+      if (a.scale) v *= load_scalar(a.scale, c, a.wdt);
+      if (a.post) v *= load_scalar(a.post, c, a.wdt);
+      sw1[c] = v;
+    }
+    __syncthreads();
+  }
+  // dw2 and P: in registers, or (two steps a thread) at the thread's place in LDS
+  __shared__ __align__(16) float sums[VPT == 2 ? 2 * 1024 * 2 * 8 : 1];
+  float dw[kWeights ? VPT : 1][8], P[kWeights ? VPT : 1][8];
+  auto kept = [&](int k, int i) { return sums + ((k * VPT + i) * 1024 + tid) * 8; };
+  if (kWeights) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = P[i][e] = 0.f;
+      for (int e = 0; e < 8; ++e) dw[kWeights ? i : 0][e] = P[kWeights ? i : 0][e] = 0.f;
+  } else {
+    for (int j = 0; j < 2 * VPT; ++j)
+      for (int e = 0; e < 8; ++e) kept(0, j)[e] = 0.f;
+  }
   for (int64_t row = (int64_t)blockIdx.x * RPB + q; row < a.rows; row += (int64_t)a.blocks * RPB) {
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
     const T* gate = reinterpret_cast<const T*>(a.gate) + row * a.gate_stride;
@@ -176,11 +204,13 @@ __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(Sandwic
     for (int i = 0; i < VPT; ++i) {
       const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, a.D);
       float w[8];
-      load_weight<PART>(a.pre, c, a.D, a.wdt, w);
+      if (kWeights) load8<float, PART>(w2 + c, a.D, w);
+      else load_weight<PART>(a.pre, c, a.D, a.wdt, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         u[i][e] *= rh;
-        dw[i][e] += d[i][e] * u[i][e];
+        if (kWeights) dw[kWeights ? i : 0][e] += d[i][e] * u[i][e];
+        else kept(0, i)[e] += d[i][e] * u[i][e];
         d[i][e] *= w[e];
         dot += c + e >= v0 ? d[i][e] * u[i][e] : 0.f;
       }
@@ -190,14 +220,20 @@ __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(Sandwic
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, a.D);
-      float w[8], sc[8];
+      float w[8];
+      if (kWeights) {
+        load8<float, PART>(sw1 + c, a.D, w);
+      } else {
+        float t[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.f, sc[e] = a.alpha;
-      if (a.post) load_weight<PART>(a.post, c, a.D, a.wdt, w);
-      if (a.scale) {
-        load_weight<PART>(a.scale, c, a.D, a.wdt, sc);
+        for (int e = 0; e < 8; ++e) w[e] = a.alpha;
+        for (int k = 0; k < 2; ++k) {
+          const void* p = k ? a.post : a.scale;
+          if (!p) continue;
+          load_weight<PART>(p, c, a.D, a.wdt, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc[e] *= a.alpha;
+          for (int e = 0; e < 8; ++e) w[e] *= t[e];
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[i][e] += rh * (d[i][e] - u[i][e] * dot);
@@ -209,9 +245,10 @@ __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(Sandwic
         const Gate t = a.gate ? gate_and_slope(a.act ? z : s[i][e], gate_sigmoid(z), a.act) : Gate{1.f, 0.f};
         ux[i][e] *= rx;
         const float b = g[i][e] * ux[i][e];
-        P[i][e] += b * t.value;
-        s[i][e] = b * sc[e] * w[e] * t.slope;
-        d[i][e] = g[i][e] * sc[e] * t.value * w[e];
+        if (kWeights) P[kWeights ? i : 0][e] += b * t.value;
+        else kept(1, i)[e] += b * t.value;
+        s[i][e] = b * w[e] * t.slope;
+        d[i][e] = g[i][e] * t.value * w[e];
         dot2 += c + e >= v0 ? d[i][e] * ux[i][e] : 0.f;
       }
       if (a.gate && v0 < a.D)
@@ -237,7 +274,8 @@ __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(Sandwic
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
         if ((i * nt + tid) * 8 < a.D)
-          store8<float, PART>(part + column_of<PART>(i * nt + tid, a.D), a.D, k ? P[i] : dw[i]);
+          store8<float, PART>(part + column_of<PART>(i * nt + tid, a.D), a.D,
+                              !kWeights ? kept(k, i) : k ? P[kWeights ? i : 0] : dw[kWeights ? i : 0]);
     } else {
       // columns of the block's four rows, each at its vector's place
       __syncthreads();
@@ -245,7 +283,8 @@ __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(Sandwic
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          wsum[q * COLS + (i * 64 + tid) * 8 + e] = k ? P[i][e] : dw[i][e];
+          wsum[q * COLS + (i * 64 + tid) * 8 + e] =
+              k ? P[kWeights ? i : 0][e] : dw[kWeights ? i : 0][e];
       __syncthreads();
       for (int j = threadIdx.x; j < ((a.D + 7) / 8) * 8; j += 256) {
         const int c = column_of<PART>(j / 8, a.D) + j % 8;
@@ -297,7 +336,8 @@ void by_type(const gdr_sandwich_norm_problem* p, F f) {
 }
 
 // Rows of several arrays: one 8-element step a thread as far as a block reaches
-// (the forward of 8192 x 4096 bf16 with a gate: 70 us, with two steps 77).
+// (the forward of 8192 x 4096 bf16 with a gate: 70 us, with two steps 77; the
+// gradient 117 and, with 193 registers, 139).
 template <typename F>
 void by_steps(int D, F f) {
   if (D <= 8192) return by_row<1>(D, f);
@@ -378,8 +418,8 @@ gdr_status launch_sandwich_norm_bwd(const gdr_sandwich_norm_problem* p, const vo
     using R = decltype(r);
     by_steps(p->D, [&](dim3 block, int, auto nt, auto vpt, auto part) {
       constexpr int NT = nt.value, VPT = vpt.value;
-      GDR_LAUNCH("sandwich_bwd", (sandwich_bwd_kernel<T, R, NT, VPT, part.value>), dim3(a.blocks),
-                 block, st, a);
+      GDR_LAUNCH_LDS("sandwich_bwd", (sandwich_bwd_kernel<T, R, NT, VPT, part.value>),
+                     dim3(a.blocks), block, VPT == 1 ? 2 * p->D * sizeof(float) : 0, st, a);
     });
   });
   GDR_LAUNCH("sandwich_reduce", sandwich_reduce_kernel,
