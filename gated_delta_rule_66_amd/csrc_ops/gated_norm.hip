@@ -133,9 +133,10 @@ constexpr int most_vectors() {
 
 // The forward.  Memory bounds it: 8192 rows of 4096 bf16 columns in heads of 128
 // take 43 us for 201 MB (4.7 TB/s), 4099 of 5005 fp16 columns in groups of 715
-// 33 us for 123 MB (3.7: a wave's second step is two fifths full).  To int8 the
-// gates' and quotients' some 40 vector operations an element nearly take the
-// memory's time: 18,062 x 4096 93 us for 370 MB (4.0).  Eight rows take 6 us.
+// 33 us for 123 MB (3.7: a wave's second step is two fifths full).  To 8 bits
+// 18,062 x 4096 take 93 us for 370 MB (4.0): exact gates (8 us) and quotients, the
+// kernel's text holds 1147 vector instructions for a thread's 16 elements with
+// both 8-bit types' branches, 696 without them.  Eight rows take 6 us.
 template <typename T, bool QUANT, Sums SUMS, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) {
   __shared__ __align__(8) float lds[32];
