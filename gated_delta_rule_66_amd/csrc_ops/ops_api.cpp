@@ -264,6 +264,9 @@ static gdr_status validate(const gdr_int8_matmul_problem* p, char* reason, size_
   if ((((int64_t)p->M + 127) / 128) * (((int64_t)p->N + 127) / 128) > (1 << 23) ||
       p->N > (1 << 26))
     return fail(GDR_ERR_SHAPE, reason, len, "problem too large (M=%d N=%d)", p->M, p->N);
+  // rows that are no multiple of 16 bytes may be copied, by 64 threads each
+  if ((p->K % 16 != 0 || p->x_stride % 16 != 0) && 64 * ((int64_t)p->M + p->N) > 0xffff0000ll)
+    return fail(GDR_ERR_SHAPE, reason, len, "problem too large (M=%d N=%d)", p->M, p->N);
   // the rows of a tile lie within 2^31 bytes
   if (p->x_stride < p->K || p->x_stride > (1 << 22))
     return fail(GDR_ERR_SHAPE, reason, len, "x_stride=%lld must be K=%d to 2^22",

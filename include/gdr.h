@@ -706,7 +706,7 @@ gdr_status gdr_quantize_rows(const gdr_quantize_problem* p, const void* x, void*
  * number reaches its token or channel only.
  *   x [M, K] int8 with a token stride; weight [N, K] int8; x_scale [M],
  *   w_scale [N] fp32; bias [N] bias_dtype (nullable); y [M, N] out_dtype
- * K <= 65536. */
+ * K <= 65536; M + N below 2^26 where rows are copied (below). */
 typedef struct {
   int32_t M, N, K;
   gdr_dtype out_dtype;            /* bf16, fp16 or fp32 */

@@ -98,6 +98,9 @@ BAD = [
     (matmul(M=(1 << 31) - 1, N=128), "GDR_ERR_SHAPE", "too large"),
     (matmul(M=1 << 20, N=1 << 18), "GDR_ERR_SHAPE", "too large"),
     (matmul(N=(1 << 26) + 1), "GDR_ERR_SHAPE", "too large"),
+    # rows that are copied first have 64 threads each
+    (matmul(M=1 << 26, N=8, K=65, x_stride=65), "GDR_ERR_SHAPE", "too large"),
+    (matmul(M=(1 << 26) - 128, N=128, x_stride=72), "GDR_ERR_SHAPE", "too large"),
     (matmul(x_stride=63), "GDR_ERR_SHAPE", "x_stride"),
     (matmul(x_stride=(1 << 22) + 1), "GDR_ERR_SHAPE", "x_stride"),
     (matmul(out_dtype=3), "GDR_ERR_DTYPE", "output"),
@@ -109,7 +112,8 @@ BAD = [
                                norm_size=16384, x_stride=16384, gate_stride=16384),
                                sandwich(), sandwich(quant=1, D=16384, x_stride=16384, gate_stride=1 << 40),
                                quantize(), quantize(D=65536, x_stride=65536, quant=1), matmul(),
-                               matmul(M=1 << 20, N=1 << 17), matmul(K=65536, x_stride=1 << 22)])
+                               matmul(M=1 << 20, N=1 << 17), matmul(K=65536, x_stride=1 << 22),
+                               matmul(M=1 << 26, N=8), matmul(M=1 << 25, N=8, K=65, x_stride=65)])
 def test_accepted(p):
     assert verdict(p) == ("GDR_OK", "")
 
