@@ -297,8 +297,8 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
       for (int e = 0; e < 8; ++e) {
         const bool second = kSeg && c + e >= sp[i].bound;
         z8[i][e] = gate_input(z8[i][e]);
-        s[i][e] = gate_sigmoid(z8[i][e]);
-        const float act = a.act == 1 ? z8[i][e] * s[i][e] : s[i][e];
+        s[i][e] = gate_tail(z8[i][e]);
+        const float sig = gate_sigmoid(z8[i][e], s[i][e]), act = a.act == 1 ? z8[i][e] * sig : sig;
         const float unit = u[i][e] * (second ? rnext[i] : r[i]) * (a.gate_first ? act : 1.f);
         const float k = a.gate_first ? 1.f : act;
         if (live) dw[i][e] += du[i][e] * unit * k;

@@ -150,31 +150,35 @@ __device__ __forceinline__ float inverse_root(double a) {
 // exponential is taken at -80 at the least, where the sigmoid is 2^-115: with
 // an infinity it would make silu's limit 0 and the slopes' products NaN.
 __device__ __forceinline__ float gate_input(float z) { return z < -80.f ? -80.f : z; }  // a NaN passes
-// The sigmoid of such a z to fp32's precision: the exponent's rounding is added
-// to the power, and the reciprocal's estimate gets a step of Newton's (with the
-// instructions alone a 16-bit stream's roundings fell the other way twice as
-// often as an exact gate's).
-__device__ __forceinline__ float gate_sigmoid(float z) {
+// sigmoid(-|z|), the smaller of a gate's sigmoid and its complement, to fp32's
+// precision: the exponent's rounding is added to the power, and the reciprocal's
+// estimate gets a step of Newton's (with the instructions alone a 16-bit
+// stream's roundings fell the other way twice as often as an exact gate's).  The
+// larger of the two is one less this value; the other way round nothing would
+// be left of an open gate's complement, and so of its slope.
+__device__ __forceinline__ float gate_tail(float z) {
   constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911e-8f, kLn2 = 0.6931471805599453f;
-  const float p = -z * kLog2e;
-  const float rest = __builtin_fmaf(-z, kRest, __builtin_fmaf(-z, kLog2e, -p));
+  const float m = fabsf(z), p = -m * kLog2e;
+  const float rest = __builtin_fmaf(-m, kRest, __builtin_fmaf(-m, kLog2e, -p));
   float e = __builtin_amdgcn_exp2f(p);
   e = p < -150.f ? 0.f : __builtin_fmaf(e, rest * kLn2, e);  // (z = inf: the rest is NaN)
   const float d = 1.f + e, r = fast_rcp(d);
-  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+  return e * __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
 }
+// The sigmoid from its tail (a NaN passes).
+__device__ __forceinline__ float gate_sigmoid(float z, float tail) { return z < 0.f ? tail : 1.f - tail; }
 __device__ __forceinline__ float gate_of(float z, int act) {
   if (act == 0) return z;
-  const float zc = gate_input(z), s = gate_sigmoid(zc);
+  const float zc = gate_input(z), s = gate_sigmoid(zc, gate_tail(zc));
   return act == 1 ? zc * s : s;
 }
 struct Gate {
   float value, slope;
 };
-// From z as gate_input gives it and s, its sigmoid.
-__device__ __forceinline__ Gate gate_and_slope(float z, float s, int act) {
+// From z as gate_input gives it and its tail.
+__device__ __forceinline__ Gate gate_and_slope(float z, float tail, int act) {
   if (act == 0) return {z, 1.f};
-  const float rest = 1.f - s;
+  const float s = gate_sigmoid(z, tail), rest = gate_sigmoid(-z, tail);
   if (act == 1) return {z * s, s * __builtin_fmaf(z, rest, 1.f)};
   return {s, s * rest};
 }

@@ -242,7 +242,7 @@ __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(Sandwic
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float z = gate_input(s[i][e]);
-        const Gate t = a.gate ? gate_and_slope(a.act ? z : s[i][e], gate_sigmoid(z), a.act) : Gate{1.f, 0.f};
+        const Gate t = a.gate ? gate_and_slope(a.act ? z : s[i][e], gate_tail(z), a.act) : Gate{1.f, 0.f};
         ux[i][e] *= rx;
         const float b = g[i][e] * ux[i][e];
         if (kWeights) P[kWeights ? i : 0][e] += b * t.value;

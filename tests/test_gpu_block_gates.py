@@ -1,0 +1,82 @@
+"""Gates far from zero in the gated norm and the sandwich norm, on the GPU
+against plain 64-bit forms (needs an MI355X).
+
+Tolerances, relative to a value's own terms: the smaller of a gate's sigmoid and
+its complement passes through an exponential and a reciprocal (an instruction's
+2^-23 each), a correction, a sum and a product (2^-24 each): within 2^-21; the
+larger is one less it.  A slope is a product of two such factors (silu's second
+factor 1 + z (1 - s) is at least 1/8 of its terms' sum for |z| >= 8): within 2^-20.
+The products with the unit row and the weights add six roundings: 2^-19 in all
+where no sum over the row takes part, and 2^-17 of the magnitudes where one does
+(at most 90 additions in a row)."""
+import pytest
+import torch
+
+import _block_ref as bref
+import _layer_ref as ref
+import gated_delta_rule_66_amd as gdr
+
+pytestmark = pytest.mark.gpu
+OUT, SLACK = 2.0 ** -19, 2.0 ** -17
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+EPS = 1e-6
+
+
+def gates(rows, D, low, high, dtype, seed=0):
+    """Magnitudes from low to high, of both signs in turn."""
+    g = torch.Generator().manual_seed(seed)
+    z = low + (high - low) * torch.rand(rows, D, generator=g)
+    return (z * (1 - 2 * (torch.arange(rows * D).view(rows, D) % 2))).to(dtype)
+
+
+def values(rows, D, dtype, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    return dict(x=r(rows, D).to(dtype), dy=r(rows, D).to(dtype), dh=r(rows, D).to(dtype),
+                res=r(rows, D).to(dtype), w=(1 + r(D) / 4).to(dtype), v=(1 + r(D) / 4).to(dtype))
+
+
+def act(z, name):
+    """As the references' own, with the complement s(-z), of which 1 - s(z) keeps
+    nothing beyond z = 37 in 64 bits either; a slope's magnitude is its own."""
+    s, rest = torch.sigmoid(z), torch.sigmoid(-z)
+    if name == "silu":
+        return z * s, s * (1 + z * rest), (s * (1 + z * rest)).abs()
+    return s, s * rest, s * rest
+
+
+@pytest.fixture(autouse=True)
+def exact_slopes(monkeypatch):
+    monkeypatch.setattr(bref, "act", act)
+
+
+# ---- slopes --------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["silu", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("D,size", [(320, 320), (384, 128), (300, 75), (1000, 1000), (8200, 8200)])
+def test_slopes_of_open_and_closed_gates(D, size, dtype, name):
+    """An open sigmoid's slope is its complement, which one less the sigmoid
+    would lose."""
+    rows = 5
+    t, z = values(rows, D, dtype), gates(rows, D, 8, 40, dtype)
+    w = t["w"][:size].contiguous()
+    for first in (True, False):
+        y, rstd = gdr.gated_rms_norm_fwd(t["x"].cuda(), z.cuda(), w.cuda(), EPS, size, first, name)
+        _, dz, _ = gdr.gated_rms_norm_bwd(t["dy"].cuda(), t["x"].cuda(), z.cuda(), w.cuda(), rstd, size,
+                                          first, name)
+        r = bref.gated(t["x"], z, w, EPS, size, first, name, t["dy"])
+        ref.held("y", y, r["y"], r["y"].abs(), dtype, SLACK)
+        ref.held("dz", dz, r["dz"], r["dzm"], dtype, OUT if first else SLACK)
+
+
+@pytest.mark.parametrize("name", ["silu", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("D", [320, 1001, 8200])
+def test_sandwich_slopes_of_open_and_closed_gates(D, dtype, name):
+    t, z = values(5, D, dtype), gates(5, D, 8, 40, dtype)
+    g = {k: v.cuda() for k, v in t.items()}
+    y, h, rx, rh = gdr.sandwich_rms_norm_fwd(g["x"], g["res"], g["w"], g["v"], z.cuda(), 0.5, name, EPS)
+    got = gdr.sandwich_rms_norm_bwd(g["dy"], g["dh"], g["x"], h, g["w"], g["v"], rx, rh, z.cuda(), 0.5, name)
+    r = bref.sandwich(t["x"], t["res"], t["w"], t["v"], EPS, z, 0.5, name, h, t["dy"], t["dh"])
+    ref.held("dgate", got[4], r["dgate"], r["dgatem"], dtype, SLACK)
