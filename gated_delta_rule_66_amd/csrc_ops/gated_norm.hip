@@ -299,7 +299,7 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
         z8[i][e] = gate_input(z8[i][e]);
         s[i][e] = gate_tail(z8[i][e]);
         const float sig = gate_sigmoid(z8[i][e], s[i][e]), act = a.act == 1 ? z8[i][e] * sig : sig;
-        const float unit = u[i][e] * (second ? rnext[i] : r[i]) * (a.gate_first ? act : 1.f);
+        const float unit = (a.gate_first ? u[i][e] * act : u[i][e]) * (second ? rnext[i] : r[i]);
         const float k = a.gate_first ? 1.f : act;
         if (live) dw[i][e] += du[i][e] * unit * k;
         du[i][e] *= w[i][e];
@@ -334,12 +334,15 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
         const bool second = kSeg && c + e >= sp[i].bound;
         const float re = second ? rnext[i] : r[i], mean = second ? dnext[i] : dot[i];
         const Gate t = gate_and_slope(z8[i][e], s[i][e], a.act);
-        const float xr = u[i][e] * re, d = du[i][e];
+        const float d = du[i][e];
         if (a.gate_first) {
-          const float dv = re * (d - xr * t.value * mean);
-          s[i][e] = dv * u[i][e] * t.slope;
-          u[i][e] = dv * t.value;
+          // (with eps = 0 re may be as large as the activation is small: their
+          // product comes first)
+          const float c = d - u[i][e] * t.value * re * mean;
+          s[i][e] = re * t.slope * c * u[i][e];
+          u[i][e] = re * t.value * c;
         } else {
+          const float xr = u[i][e] * re;
           s[i][e] = d * xr * t.slope;
           u[i][e] = re * (d * t.value - xr * mean);
         }

@@ -146,10 +146,10 @@ __device__ __forceinline__ float inverse_root(double a) {
   return (float)(a < __builtin_inf() && a > 0.0 ? z : y);
 }
 
-// A gate's activation (0: none, 1: silu, 2: sigmoid) and its derivative.  The
-// exponential is taken at -80 at the least, where the sigmoid is 2^-115: with
-// an infinity it would make silu's limit 0 and the slopes' products NaN.
-__device__ __forceinline__ float gate_input(float z) { return z < -80.f ? -80.f : z; }  // a NaN passes
+// A gate's activation (0: none, 1: silu, 2: sigmoid) and its derivative.  Below
+// -104 the sigmoid is less than half of fp32's smallest number; an infinity would
+// make silu's limit 0 a NaN.
+__device__ __forceinline__ float gate_input(float z) { return z < -128.f ? -128.f : z; }  // a NaN passes
 // sigmoid(-|z|), the smaller of a gate's sigmoid and its complement, to fp32's
 // precision: the exponent's rounding is added to the power, and the reciprocal's
 // estimate gets a step of Newton's (with the instructions alone a 16-bit
@@ -157,11 +157,17 @@ __device__ __forceinline__ float gate_input(float z) { return z < -80.f ? -80.f 
 // larger of the two is one less this value; the other way round nothing would
 // be left of an open gate's complement, and so of its slope.
 __device__ __forceinline__ float gate_tail(float z) {
+#pragma clang fp contract(off)  // the rounding of p itself is what is added back
   constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911e-8f, kLn2 = 0.6931471805599453f;
-  const float m = fabsf(z), p = -m * kLog2e;
+  float m = fabsf(z);
+  m = m > 128.f ? 128.f : m;
+  const float p = -m * kLog2e;
   const float rest = __builtin_fmaf(-m, kRest, __builtin_fmaf(-m, kLog2e, -p));
-  float e = __builtin_amdgcn_exp2f(p);
-  e = p < -150.f ? 0.f : __builtin_fmaf(e, rest * kLn2, e);  // (z = inf: the rest is NaN)
+  // the power instruction has no results below fp32's normal range: 2^64 of it
+  const bool deep = p < -64.f;
+  float e = __builtin_amdgcn_exp2f(deep ? p + 64.f : p);
+  e = __builtin_fmaf(e, rest * kLn2, e);
+  e = deep ? e * 0x1p-64f : e;
   const float d = 1.f + e, r = fast_rcp(d);
   return e * __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
 }

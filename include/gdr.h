@@ -593,9 +593,12 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_problem* p, const void* dy, const voi
  *   weight, dweight [D] w_dtype, or [norm_size] with shared_weight; q [rows, D]
  *   8 bits; scale [rows] or [rows, ceil(D / 128)] fp32; rstd [rows, D /
  *   norm_size] fp32
- * D <= 16384, a multiple of norm_size, which is D or at least 8.  An infinite gate has silu's and the
- * sigmoid's limit; a NaN or an infinity in x reaches its group only, and in 8
- * bits what its scale covers. */
+ * D <= 16384, a multiple of norm_size, which is D or at least 8.  An infinite
+ * gate has silu's and the sigmoid's limit; sigmoids below fp32's normal range (of
+ * gates below -87) have the precision of its subnormal numbers.  With eps = 0 a
+ * group's root mean square has to have an inverse in fp32 (2^-126 or more).  A
+ * NaN or an infinity in x reaches its group only, and in 8 bits what its scale
+ * covers. */
 typedef struct {
   int32_t rows, D, norm_size;
   gdr_dtype dtype;                /* bf16, fp16 or fp32 */

@@ -80,3 +80,60 @@ def test_sandwich_slopes_of_open_and_closed_gates(D, dtype, name):
     got = gdr.sandwich_rms_norm_bwd(g["dy"], g["dh"], g["x"], h, g["w"], g["v"], rx, rh, z.cuda(), 0.5, name)
     r = bref.sandwich(t["x"], t["res"], t["w"], t["v"], EPS, z, 0.5, name, h, t["dy"], t["dh"])
     ref.held("dgate", got[4], r["dgate"], r["dgatem"], dtype, SLACK)
+
+
+# ---- the range -------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["silu", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_closed_gates_to_the_end_of_fp32(dtype, name):
+    """Down to -104, where the sigmoid leaves fp32, and to 0 at minus infinity.
+    Beyond OUT a sigmoid is off by fp32's smallest step 2^-149, silu and its slope
+    by |z| of it, and every product by half a step."""
+    t = values(4, 320, dtype)
+    z = torch.linspace(-79, -110, 320).repeat(4, 1).to(dtype)
+    z[2, ::7], z[3, ::5] = -float("inf"), -3e38
+    closed = z < -200
+    zr = z.clone()
+    zr[closed] = -200.0                       # 0 in fp32, and no 0 times an infinity in the reference
+    r = bref.gated(t["x"], zr, t["w"], EPS, 0, True, name, t["dy"])
+    u = ref.d(t["x"]) * r["rstd"]
+    step = 2.0 ** -149 * (2 + 2 * ref.d(zr).abs())
+    y, rstd = gdr.gated_rms_norm_fwd(t["x"].cuda(), z.cuda(), t["w"].cuda(), EPS, 0, True, name)
+    _, dz, _ = gdr.gated_rms_norm_bwd(t["dy"].cuda(), t["x"].cuda(), z.cuda(), t["w"].cuda(), rstd, 0, True,
+                                      name)
+    uw = (u * ref.d(t["w"])).abs()
+    for got, want, size in ((y, r["y"], 1 + uw), (dz, r["dz"], 1 + uw * ref.d(t["dy"]).abs())):
+        bar = (OUT + ref.half_step(dtype) * 1.01) * want.abs() + step * size + \
+            torch.finfo(dtype).tiny * torch.finfo(dtype).eps
+        assert ((ref.d(got) - want).abs() <= bar).all()
+        assert (got.cpu()[closed] == 0).all()
+    # the sandwich norm's gate: h = 0 + act(g) x
+    nil = torch.zeros(4, 320, device="cuda")
+    h = gdr.sandwich_rms_norm_fwd(t["x"].cuda(), nil, None, t["v"].cuda(), z.cuda(), None, name, EPS)[1]
+    want = act(ref.d(zr), name)[0] * ref.d(t["x"])
+    bar = OUT * want.abs() + step * (1 + ref.d(t["x"]).abs())
+    assert ((ref.d(h) - want).abs() <= bar).all() and (h.cpu()[closed] == 0).all()
+
+
+@pytest.mark.parametrize("name", ["silu", "sigmoid"])
+@pytest.mark.parametrize("low,high", [(81, 87), (86.8, 87.2), (60, 70)])
+@pytest.mark.parametrize("D,size", [(320, 320), (384, 128), (300, 75), (8200, 8200)])
+def test_groups_of_closed_gates_without_eps(D, size, low, high, name):
+    """eps = 0 and the gate first: groups of closed gates are scaled up to unit
+    rows, whose gradients pass through inverse roots of up to 1e38.  A product
+    x act(z) below 2^-126 is rounded to a multiple of 2^-149, so a unit row is off
+    by 2^-150 of the inverse root beside its 2^-17: the output by its weight of it,
+    the weight's gradient by dy of it.  (In dx and dz this is beside the group's mean
+    and its own dy: 2^-150 1e38 is less than 2^-23.)"""
+    t = values(5, D, F32)
+    z = -gates(5, D, low, high, F32).abs()
+    w = t["w"][:size].contiguous()
+    y, rstd = gdr.gated_rms_norm_fwd(t["x"].cuda(), z.cuda(), w.cuda(), 0.0, size, False, name)
+    got = gdr.gated_rms_norm_bwd(t["dy"].cuda(), t["x"].cuda(), z.cuda(), w.cuda(), rstd, size, False, name)
+    r = bref.gated(t["x"], z, w, 0.0, size, False, name, t["dy"])
+    low = 2.0 ** -150 / SLACK * r["rstd"].repeat_interleave(size, -1)
+    ref.held("y", y, r["y"], r["y"].abs() + low * ref.d(w).abs().repeat(D // size), F32, SLACK)
+    r["dwm"] = r["dwm"] + (low * ref.d(t["dy"]).abs()).view(-1, size).sum(0)
+    for g, k in zip(got, ("dx", "dz", "dw")):
+        ref.held(k, g, r[k], r[k + "m"], F32, SLACK)
