@@ -185,7 +185,9 @@ struct Gate {
 __device__ __forceinline__ Gate gate_and_slope(float z, float tail, int act) {
   if (act == 0) return {z, 1.f};
   const float s = gate_sigmoid(z, tail), rest = gate_sigmoid(-z, tail);
-  if (act == 1) return {z * s, s * __builtin_fmaf(z, rest, 1.f)};
+  // (of an open gate nothing is left beyond 104, and an infinity's 0 times that
+  // would be a NaN)
+  if (act == 1) return {z * s, s * __builtin_fmaf(z > 128.f ? 128.f : z, rest, 1.f)};
   return {s, s * rest};
 }
 

@@ -137,3 +137,30 @@ def test_groups_of_closed_gates_without_eps(D, size, low, high, name):
     r["dwm"] = r["dwm"] + (low * ref.d(t["dy"]).abs()).view(-1, size).sum(0)
     for g, k in zip(got, ("dx", "dz", "dw")):
         ref.held(k, g, r[k], r[k + "m"], F32, SLACK)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+def test_slopes_at_plus_infinity(dtype):
+    """sigmoid: value 1, slope 0; silu: slope 1 (its value is infinite, and what
+    is made of it)."""
+    t = values(4, 96, dtype)
+    z = gates(4, 96, 1, 3, dtype)
+    open_ = torch.zeros(4, 96, dtype=torch.bool)
+    open_[:, ::9] = True
+    z[open_] = float("inf")
+    x, w, dy = t["x"].cuda(), t["w"].cuda(), t["dy"].cuda()
+    for size in (96, 32, 12):
+        v = w[:size].contiguous()
+        u = ref.d(x).view(-1, size)
+        u = (u / (u.square().mean(-1, keepdim=True) + EPS).sqrt() * ref.d(v)).view(4, 96)
+        for name in ("sigmoid", "silu"):
+            y, rstd = gdr.gated_rms_norm_fwd(x, z.cuda(), v, EPS, size, True, name)
+            _, dz, _ = gdr.gated_rms_norm_bwd(dy, x, z.cuda(), v, rstd, size, True, name)
+            want = u * ref.d(dy) * (1.0 if name == "silu" else 0.0)
+            ref.held("dz", dz.cpu()[open_], want[open_], want[open_].abs(), dtype, OUT)
+            if name == "sigmoid":
+                ref.held("y", y.cpu()[open_], u[open_], u[open_].abs(), dtype, OUT)
+    one = x.new_ones(96)
+    y, h, rx, rh = gdr.sandwich_rms_norm_fwd(x, x, w, one, z.cuda(), None, "sigmoid", EPS)
+    dgate = gdr.sandwich_rms_norm_bwd(dy, None, x, h, w, one, rx, rh, z.cuda(), None, "sigmoid")[4]
+    assert y.isfinite().all() and dgate.isfinite().all() and (dgate.cpu()[open_] == 0).all()
