@@ -516,7 +516,20 @@ Walk walk_of(const gdr_gated_norm_problem* p) {
   return w;
 }
 
+// Blocks of the forward: `rows` rows or, as units, groups each.
+int64_t blocks_of(const gdr_gated_norm_problem* p, int rows) {
+  return ((int64_t)p->rows * pieces_of(p, false) + rows - 1) / rows;
+}
+
 }  // namespace
+
+int64_t gated_norm_threads(const gdr_gated_norm_problem* p) {
+  int64_t threads = 0;
+  by_form(p, [&](dim3 block, int rows, auto, auto, auto, auto) {
+    threads = blocks_of(p, rows) * block.x;
+  });
+  return threads;
+}
 
 gdr_status launch_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x, const void* gate,
                                  const void* weight, void* y, float* scale, float* rstd,
@@ -529,8 +542,7 @@ gdr_status launch_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x,
     by_form(p, [&](dim3 block, int rows, auto sums, auto nt, auto vpt, auto part) {
       constexpr Sums SUMS = sums.value;
       constexpr int NT = nt.value, VPT = vpt.value;
-      const int64_t units = (int64_t)a.rows * a.pieces;
-      const dim3 grid((unsigned)((units + rows - 1) / rows));
+      const dim3 grid((unsigned)blocks_of(p, rows));
       if (p->quant)
         GDR_LAUNCH("gated_fwd", (gated_fwd_kernel<T, true, SUMS, NT, VPT, part.value>), grid, block,
                    st, a);

@@ -164,9 +164,6 @@ static gdr_status check_rows(int rows, int D, int most, gdr_dtype dtype, int qua
   if (rows < 1 || D < 1)
     return fail(GDR_ERR_SHAPE, reason, len, "sizes must be positive (rows=%d D=%d)", rows, D);
   if (D > most) return fail(GDR_ERR_SHAPE, reason, len, "at most %d columns, got %d", most, D);
-  // a launch holds fewer than 2^32 threads: 64, 256 or 1024 a row
-  if ((int64_t)rows * (D <= 1024 ? 64 : D <= 16384 ? 256 : 1024) > 0xffff0000ll)
-    return fail(GDR_ERR_SHAPE, reason, len, "too many rows (%d of %d columns)", rows, D);
   if (quant < 0 || quant > 2)
     return fail(GDR_ERR_ARG, reason, len, "quant must be 0 (none), 1 (e4m3) or 2 (int8)");
   if (group != 0 && group != 128)
@@ -176,9 +173,9 @@ static gdr_status check_rows(int rows, int D, int most, gdr_dtype dtype, int qua
     return fail(GDR_ERR_ARG, reason, len, "columns per scale are for quantised outputs");
   return GDR_OK;
 }
-// The same for rows held by 64 threads for each 512 columns.
-static gdr_status check_blocks(int rows, int D, char* reason, size_t len) {
-  if ((int64_t)rows * (64 * ((D + 511) / 512)) > 0xffff0000ll)
+// A launch holds fewer than 2^32 threads.
+static gdr_status check_threads(int64_t threads, int rows, int D, char* reason, size_t len) {
+  if (threads > 0xffff0000ll)
     return fail(GDR_ERR_SHAPE, reason, len, "too many rows (%d of %d columns)", rows, D);
   return GDR_OK;
 }
@@ -202,11 +199,7 @@ static gdr_status validate(const gdr_gated_norm_problem* p, char* reason, size_t
   if (p->norm_size < 8 && p->norm_size != p->D)
     return fail(GDR_ERR_SHAPE, reason, len, "norm_size must be D or at least 8, got %d",
                 p->norm_size);
-  // a group may have 64 threads for each 512 of its columns
-  if ((int64_t)p->rows * (p->D / p->norm_size) * (64 * ((p->norm_size + 511) / 512)) > 0xffff0000ll)
-    return fail(GDR_ERR_SHAPE, reason, len, "too many rows (%d of %d columns in groups of %d)",
-                p->rows, p->D, p->norm_size);
-  if ((s = check_blocks(p->rows, p->D, reason, len)) != GDR_OK) return s;
+  if ((s = check_threads(gated_norm_threads(p), p->rows, p->D, reason, len)) != GDR_OK) return s;
   if (!is_flag(p->shared_weight) || !is_flag(p->gate_first))
     return fail(GDR_ERR_ARG, reason, len, "shared_weight and gate_first must be 0 or 1");
   if (p->activation != 1 && p->activation != 2)
@@ -221,7 +214,7 @@ static gdr_status validate(const gdr_sandwich_norm_problem* p, char* reason, siz
   if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
   gdr_status s = check_rows(p->rows, p->D, 16384, p->dtype, p->quant, p->group_size, reason, len);
   if (s != GDR_OK) return s;
-  if ((s = check_blocks(p->rows, p->D, reason, len)) != GDR_OK) return s;
+  if ((s = check_threads(sandwich_norm_threads(p), p->rows, p->D, reason, len)) != GDR_OK) return s;
   if (p->res_dtype != p->dtype && p->res_dtype != GDR_FP32)
     return fail(GDR_ERR_DTYPE, reason, len, "the residual must have x's dtype or fp32 (got code %d)",
                 (int)p->res_dtype);
@@ -241,6 +234,9 @@ static gdr_status validate(const gdr_quantize_problem* p, char* reason, size_t l
   if (!p) return fail(GDR_ERR_NULL, reason, len, "problem descriptor is NULL");
   gdr_status s = check_rows(p->rows, p->D, 65536, p->dtype, p->quant, p->group_size, reason, len);
   if (s != GDR_OK) return s;
+  // 64, 256 or 1024 a row
+  const int a_row = p->D <= 1024 ? 64 : p->D <= 16384 ? 256 : 1024;
+  if ((s = check_threads((int64_t)p->rows * a_row, p->rows, p->D, reason, len)) != GDR_OK) return s;
   if (p->quant == 0)
     return fail(GDR_ERR_ARG, reason, len, "quant must be 1 (e4m3) or 2 (int8)");
   return check_stride("x", p->x_stride, p->D, reason, len);

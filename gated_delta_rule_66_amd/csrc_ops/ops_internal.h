@@ -42,6 +42,8 @@ void launch_reduce_rows(const float* part, int rows, int cols, void* out, int dt
                         hipStream_t st);
 
 // --- gated RMS norm (gated_norm.hip) ---
+// threads of the forward's launch (the gradient's is bounded)
+int64_t gated_norm_threads(const gdr_gated_norm_problem* p);
 gdr_status launch_gated_norm_fwd(const gdr_gated_norm_problem* p, const void* x, const void* gate,
                                  const void* weight, void* y, float* scale, float* rstd,
                                  hipStream_t st);
@@ -51,6 +53,7 @@ gdr_status launch_gated_norm_bwd(const gdr_gated_norm_problem* p, const void* dy
                                  void* dgate, void* dweight, void* ws, hipStream_t st);
 
 // --- sandwich RMS norm (sandwich_norm.hip) ---
+int64_t sandwich_norm_threads(const gdr_sandwich_norm_problem* p);  // the forward's
 gdr_status launch_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const void* x,
                                     const void* residual, const void* gate, const void* post,
                                     const void* res_scale, const void* pre, void* y, float* scale,

@@ -369,7 +369,19 @@ SandwichArgs args_of(const gdr_sandwich_norm_problem* p) {
   return a;
 }
 
+int64_t blocks_of(const gdr_sandwich_norm_problem* p, int rows) {
+  return ((int64_t)p->rows + rows - 1) / rows;
+}
+
 }  // namespace
+
+int64_t sandwich_norm_threads(const gdr_sandwich_norm_problem* p) {
+  int64_t threads = 0;
+  by_steps(p->D, [&](dim3 block, int rows, auto, auto, auto) {
+    threads = blocks_of(p, rows) * block.x;
+  });
+  return threads;
+}
 
 gdr_status launch_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const void* x,
                                     const void* residual, const void* gate, const void* post,
@@ -383,7 +395,7 @@ gdr_status launch_sandwich_norm_fwd(const gdr_sandwich_norm_problem* p, const vo
     using R = decltype(r);
     by_steps(p->D, [&](dim3 block, int rows, auto nt, auto vpt, auto part) {
       constexpr int NT = nt.value, VPT = vpt.value;
-      const dim3 grid((unsigned)(((int64_t)p->rows + rows - 1) / rows));
+      const dim3 grid((unsigned)blocks_of(p, rows));
       if (p->quant)
         GDR_LAUNCH("sandwich_fwd", (sandwich_fwd_kernel<T, R, true, NT, VPT, part.value>), grid,
                    block, st, a);
