@@ -131,6 +131,13 @@ constexpr int most_vectors() {
   return 1024 * VPT;
 }
 
+// f(the order as a constant): one branch for all elements of a row.
+template <typename F>
+__device__ __forceinline__ void by_order(int gate_first, F f) {
+  if (gate_first) f(std::true_type());
+  else f(std::false_type());
+}
+
 // The forward.  Memory bounds it: 8192 rows of 4096 bf16 columns in heads of 128
 // take 43 us for 201 MB (4.7 TB/s), 4099 of 5005 fp16 columns in groups of 715
 // 33 us for 123 MB (3.7: a wave's second step is two fifths full).  To 8 bits
@@ -156,6 +163,18 @@ __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) 
     load8<T, PART>(x + c, width, f[i]);
     load8<T, PART>(z + c, width, t[i]);
   }
+  by_activation<false>(a.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[i][e] = gate_value<act.value>(t[i][e]);
+  });
+  if (a.gate_first) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] *= t[i][e], t[i][e] = 1.f;
+  }
   // squares, mean and root in 64 bits, as the norm without a gate has them
   double sum[VPT], next[kSeg ? VPT : 1];
   Span sp[kSeg ? VPT : 1];
@@ -166,8 +185,6 @@ __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) 
     if (kSeg) next[i] = 0.0, sp[i] = span_of(a, c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      t[i][e] = gate_of(t[i][e], a.act);
-      if (a.gate_first) f[i][e] *= t[i][e];
       const double v = c + e >= v0 ? f[i][e] : 0.f;
       if (kSeg && c + e >= sp[i].bound) next[i] = __builtin_fma(v, v, next[i]);
       else sum[i] = __builtin_fma(v, v, sum[i]);
@@ -216,8 +233,7 @@ __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) 
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      f[i][e] = f[i][e] * (kSeg && c + e >= sp[i].bound ? rnext[i] : rstd[i]) * w[e];
-      if (!a.gate_first) f[i][e] *= t[i][e];
+      f[i][e] = f[i][e] * (kSeg && c + e >= sp[i].bound ? rnext[i] : rstd[i]) * w[e] * t[i][e];
       // (past the row's end the lanes hold groups that are none)
       if (QUANT && SUMS == kLanes && v0 >= a.D) f[i][e] = 0.f;
     }
@@ -276,38 +292,48 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
     const T* z = reinterpret_cast<const T*>(a.z) + row * a.z_stride + first;
     const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.D + first;
     const float* rs = a.rstd + row * a.groups;
-    float u[VPT][8], z8[VPT][8], s[VPT][8], du[VPT][8], r[VPT], rnext[kSeg ? VPT : 1];
+    float u[VPT][8], act[VPT][8], s[VPT][8], du[VPT][8], r[VPT], rnext[kSeg ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = column_of<PART>(i * nt + tid, width);
       load8<T, PART>(x + c, width, u[i]);
-      load8<T, PART>(z + c, width, z8[i]);
+      load8<T, PART>(z + c, width, act[i]);
       load8<T, PART>(dy + c, width, du[i]);
       r[i] = rs[kSeg ? sp[i].group : SUMS == kLanes ? (first + c) / a.size : unit.piece];
       if (kSeg) rnext[i] = rs[min(sp[i].group + 1, a.groups - 1)];
     }
+    by_activation<false>(a.act, [&](auto which) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const Gate g = gate_and_slope<which.value>(act[i][e]);
+          act[i][e] = g.value;
+          s[i][e] = g.slope;
+        }
+    });
     float dot[VPT], dnext[kSeg ? VPT : 1];
+    by_order(a.gate_first, [&](auto gate_first) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
-      const bool live = SUMS != kLanes || v0 < width;
-      dot[i] = 0.f;
-      if (kSeg) dnext[i] = 0.f;
+      for (int i = 0; i < VPT; ++i) {
+        const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
+        const bool live = SUMS != kLanes || v0 < width;
+        dot[i] = 0.f;
+        if (kSeg) dnext[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool second = kSeg && c + e >= sp[i].bound;
-        z8[i][e] = gate_input(z8[i][e]);
-        s[i][e] = gate_tail(z8[i][e]);
-        const float sig = gate_sigmoid(z8[i][e], s[i][e]), act = a.act == 1 ? z8[i][e] * sig : sig;
-        const float unit = (a.gate_first ? u[i][e] * act : u[i][e]) * (second ? rnext[i] : r[i]);
-        const float k = a.gate_first ? 1.f : act;
-        if (live) dw[i][e] += du[i][e] * unit * k;
-        du[i][e] *= w[i][e];
-        const float term = c + e >= v0 ? du[i][e] * k * unit : 0.f;
-        if (second) dnext[i] += term;
-        else dot[i] += term;
+        for (int e = 0; e < 8; ++e) {
+          const bool second = kSeg && c + e >= sp[i].bound;
+          const float re = second ? rnext[i] : r[i];
+          const float unit = gate_first.value ? u[i][e] * act[i][e] * re : u[i][e] * re;
+          const float k = gate_first.value ? 1.f : act[i][e];
+          if (live) dw[i][e] += du[i][e] * unit * k;
+          du[i][e] *= w[i][e];
+          const float term = c + e >= v0 ? du[i][e] * k * unit : 0.f;
+          if (second) dnext[i] += term;
+          else dot[i] += term;
+        }
       }
-    }
+    });
     if (SUMS == kLanes) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) dot[i] = lanes_sum(dot[i], a.lanes) / (float)a.size;
@@ -325,28 +351,33 @@ __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void 
         dnext[i] = total[min(sp[i].group + 1, a.groups - 1)] / (float)a.size;
       }
     }
+    by_order(a.gate_first, [&](auto gate_first) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = column_of<PART>(i * nt + tid, width);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool second = kSeg && c + e >= sp[i].bound;
+          const float re = second ? rnext[i] : r[i], mean = second ? dnext[i] : dot[i];
+          const float d = du[i][e];
+          if (gate_first.value) {
+            // (with eps = 0 re may be as large as the activation is small: their
+            // product comes first)
+            const float dv = d - u[i][e] * act[i][e] * re * mean;
+            s[i][e] = re * s[i][e] * dv * u[i][e];
+            u[i][e] = re * act[i][e] * dv;
+          } else {
+            const float xr = u[i][e] * re;
+            s[i][e] = d * xr * s[i][e];
+            u[i][e] = re * (d * act[i][e] - xr * mean);
+          }
+        }
+      }
+    });
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, width);
       if (v0 >= width) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool second = kSeg && c + e >= sp[i].bound;
-        const float re = second ? rnext[i] : r[i], mean = second ? dnext[i] : dot[i];
-        const Gate t = gate_and_slope(z8[i][e], s[i][e], a.act);
-        const float d = du[i][e];
-        if (a.gate_first) {
-          // (with eps = 0 re may be as large as the activation is small: their
-          // product comes first)
-          const float c = d - u[i][e] * t.value * re * mean;
-          s[i][e] = re * t.slope * c * u[i][e];
-          u[i][e] = re * t.value * c;
-        } else {
-          const float xr = u[i][e] * re;
-          s[i][e] = d * xr * t.slope;
-          u[i][e] = re * (d * t.value - xr * mean);
-        }
-      }
       store8<T, PART>(reinterpret_cast<T*>(a.dx) + row * a.D + first + c, width, u[i]);
       store8<T, PART>(reinterpret_cast<T*>(a.dz) + row * a.D + first + c, width, s[i]);
     }

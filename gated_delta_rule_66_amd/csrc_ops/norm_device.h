@@ -146,49 +146,58 @@ __device__ __forceinline__ float inverse_root(double a) {
   return (float)(a < __builtin_inf() && a > 0.0 ? z : y);
 }
 
-// A gate's activation (0: none, 1: silu, 2: sigmoid) and its derivative.  Below
-// -104 the sigmoid is less than half of fp32's smallest number; an infinity would
-// make silu's limit 0 a NaN.
-__device__ __forceinline__ float gate_input(float z) { return z < -128.f ? -128.f : z; }  // a NaN passes
-// sigmoid(-|z|), the smaller of a gate's sigmoid and its complement, to fp32's
-// precision: the exponent's rounding is added to the power, and the reciprocal's
-// estimate gets a step of Newton's (with the instructions alone a 16-bit
-// stream's roundings fell the other way twice as often as an exact gate's).  The
-// larger of the two is one less this value; the other way round nothing would
-// be left of an open gate's complement, and so of its slope.
-__device__ __forceinline__ float gate_tail(float z) {
-#pragma clang fp contract(off)  // the rounding of p itself is what is added back
-  constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911e-8f, kLn2 = 0.6931471805599453f;
-  float m = fabsf(z);
-  m = m > 128.f ? 128.f : m;
-  const float p = -m * kLog2e;
-  const float rest = __builtin_fmaf(-m, kRest, __builtin_fmaf(-m, kLog2e, -p));
-  // the power instruction has no results below fp32's normal range: 2^64 of it
-  const bool deep = p < -64.f;
-  float e = __builtin_amdgcn_exp2f(deep ? p + 64.f : p);
-  e = __builtin_fmaf(e, rest * kLn2, e);
-  e = deep ? e * 0x1p-64f : e;
+// A gate's activations (kNone: z itself) and their derivatives, from
+//   e = e^-|z|  and  r = 1 / (1 + e)
+// to fp32's precision: the power of the exponent's fraction, which has an error
+// of 2^-25 only, scaled by its whole part (subnormal numbers, too); the
+// reciprocal's estimate gets a step of Newton's (with the instructions alone a
+// 16-bit stream's roundings fell the other way twice as often as an exact
+// gate's).  |z| is taken at 128 at the most, where e^-|z| is less than half of
+// fp32's smallest number.  (minimum and maximum pass a NaN.)
+enum Activation { kNone, kSilu, kSigmoid };
+struct Tail {
+  float e, r;
+};
+__device__ __forceinline__ Tail gate_tail(float z) {  // |z| <= 128
+  constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911e-8f;
+  constexpr float kWhole = 12582912.f;  // 1.5 2^23: its last bits count whole numbers
+  const float m = fabsf(z);
+  const float k = __builtin_fmaf(-m, kLog2e, kWhole), n = k - kWhole;
+  const float f = __builtin_fmaf(-m, kRest, __builtin_fmaf(-m, kLog2e, -n));
+  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(f), __builtin_bit_cast(int, k) - 0x4b400000);
   const float d = 1.f + e, r = fast_rcp(d);
-  return e * __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+  return {e, __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r)};
 }
-// The sigmoid from its tail (a NaN passes).
-__device__ __forceinline__ float gate_sigmoid(float z, float tail) { return z < 0.f ? tail : 1.f - tail; }
-__device__ __forceinline__ float gate_of(float z, int act) {
-  if (act == 0) return z;
-  const float zc = gate_input(z), s = gate_sigmoid(zc, gate_tail(zc));
-  return act == 1 ? zc * s : s;
+template <Activation ACT>
+__device__ __forceinline__ float gate_value(float z) {
+  if (ACT == kNone) return z;
+  z = __builtin_elementwise_maximum(z, -128.f);  // an infinity times 0 would be a NaN
+  const Tail t = gate_tail(__builtin_elementwise_minimum(z, 128.f));
+  const float s = (z < 0.f ? t.e : 1.f) * t.r;
+  return ACT == kSilu ? z * s : s;
 }
 struct Gate {
   float value, slope;
 };
-// From z as gate_input gives it and its tail.
-__device__ __forceinline__ Gate gate_and_slope(float z, float tail, int act) {
-  if (act == 0) return {z, 1.f};
-  const float s = gate_sigmoid(z, tail), rest = gate_sigmoid(-z, tail);
-  // (of an open gate nothing is left beyond 104, and an infinity's 0 times that
-  // would be a NaN)
-  if (act == 1) return {z * s, s * __builtin_fmaf(z > 128.f ? 128.f : z, rest, 1.f)};
-  return {s, s * rest};
+// With t = e r, the smaller of the sigmoid and its complement: the larger is one
+// less it (the other way round nothing would be left of an open gate's
+// complement), their product the sigmoid's slope p, and silu's s + z p.
+template <Activation ACT>
+__device__ __forceinline__ Gate gate_and_slope(float z) {
+  if (ACT == kNone) return {z, 1.f};
+  z = __builtin_elementwise_maximum(z, -128.f);
+  const float zc = __builtin_elementwise_minimum(z, 128.f);
+  const Tail tail = gate_tail(zc);
+  const float t = tail.e * tail.r, big = 1.f - t, p = t * big, s = z < 0.f ? t : big;
+  if (ACT == kSilu) return {z * s, __builtin_fmaf(zc, p, s)};
+  return {s, p};
+}
+// f(the activation as a constant): one branch for all elements of a row.
+template <bool NONE, typename F>
+__device__ __forceinline__ void by_activation(int act, F f) {
+  if (act == 1) f(std::integral_constant<Activation, kSilu>());
+  else if (!NONE || act == 2) f(std::integral_constant<Activation, kSigmoid>());
+  else f(std::integral_constant<Activation, kNone>());
 }
 
 // Threads of a block (the most, where NT is 0): one row of NT threads, or (NT ==

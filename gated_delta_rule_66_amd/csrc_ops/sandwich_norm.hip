@@ -93,13 +93,17 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
       for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * rstd * w[e];
     }
   }
+  if (a.gate) {
+    by_activation<true>(a.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] *= gate_value<act.value>(g[i][e]);
+    });
+  }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v0 = (i * nt + tid) * 8, c = column_of<PART>(i * nt + tid, a.D);
-    if (a.gate) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] *= gate_of(g[i][e], a.act);
-    }
     if (a.scale) {
       float s[8];
       load_weight<PART>(a.scale, c, a.D, a.wdt, s);
@@ -239,16 +243,24 @@ __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(Sandwic
       for (int e = 0; e < 8; ++e) g[i][e] += rh * (d[i][e] - u[i][e] * dot);
       if (v0 < a.D)
         store8<R, PART>(reinterpret_cast<R*>(a.dres) + row * a.D + c, a.D, g[i]);
+      Gate t[8];
+      if (a.gate) {
+        by_activation<true>(a.act, [&](auto act) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = gate_and_slope<act.value>(s[i][e]);
+        });
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = {1.f, 0.f};
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float z = gate_input(s[i][e]);
-        const Gate t = a.gate ? gate_and_slope(a.act ? z : s[i][e], gate_tail(z), a.act) : Gate{1.f, 0.f};
         ux[i][e] *= rx;
         const float b = g[i][e] * ux[i][e];
-        if (kWeights) P[kWeights ? i : 0][e] += b * t.value;
-        else kept(1, i)[e] += b * t.value;
-        s[i][e] = b * w[e] * t.slope;
-        d[i][e] = g[i][e] * t.value * w[e];
+        if (kWeights) P[kWeights ? i : 0][e] += b * t[e].value;
+        else kept(1, i)[e] += b * t[e].value;
+        s[i][e] = b * w[e] * t[e].slope;
+        d[i][e] = g[i][e] * t[e].value * w[e];
         dot2 += c + e >= v0 ? d[i][e] * ux[i][e] : 0.f;
       }
       if (a.gate && v0 < a.D)
