@@ -168,7 +168,8 @@ __device__ __forceinline__ int lds_address(const void* p) {
 // cannot tell the buffers apart, waits for the builtin's loads before the next
 // read of LDS.  There is no register to wait for: the wave waits on its vector
 // memory counter before the barrier that hands the tile over.  (m0, which holds
-// the address in LDS, is used by nothing else here.)
+// the address in LDS, is a register that the compiler reserves, and warns of in a
+// list of clobbered ones; nothing else here reads or writes it.)
 __device__ __forceinline__ void load_to_lds(u32x4 rs, int at, int off) {
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at),
@@ -195,12 +196,9 @@ __device__ __forceinline__ void load_to_lds(u32x4 rs, int at, int off) {
 // Steps of 64 bytes, four in flight: 913 us.  Small problems wait for loads:
 // there tiles of 64 x 64 keep four steps in flight (512 x 4096 x 4096 15 us; two
 // steps 17, 128 x 128 tiles 23).
-template <int KB>
-__device__ __forceinline__ int swizzle(int r) {
-  static_assert(KB == 64 || KB == 128, "bytes of a row");
-  return KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
-}
-template <int WN, int WM, int NB, int MB, int KB, int STEPS, typename O>
+constexpr int KB = 128;
+__device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
+template <int WN, int WM, int NB, int MB, int STEPS, typename O>
 __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(MatArgs a) {
   constexpr int NW = WN * WM, NT = 64 * NW;
   constexpr int BN = 32 * NB * WN, BM = 32 * MB * WM;
@@ -237,7 +235,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(MatArgs a) {
   const int first = is_w ? n0 : m0, rows = min(is_w ? BN : BM, (is_w ? a.N : a.M) - first);
   const int8_t* src = (is_w ? a.w : a.x) + (int64_t)first * stride;
   const int lrow = lane / (KB / 16), lpos = lane % (KB / 16);
-  const int piece[2] = {16 * (lpos ^ swizzle<KB>(lrow)), 16 * (lpos ^ swizzle<KB>(RPL + lrow))};
+  const int piece[2] = {16 * (lpos ^ swizzle(lrow)), 16 * (lpos ^ swizzle(RPL + lrow))};
   u32x4 rs = tile_rsrc(src, (int64_t)(rows - 1) * stride + a.K);
   const int to = lds_address(buf) + row0 * KB;
   int from[PER];
@@ -263,9 +261,9 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(MatArgs a) {
   // Waits until the wave's loads are done but for those of `ahead` steps, then
   // for the other waves (whose barrier does not wait for loads to LDS).
   auto arrive = [&](int ahead) {
-    if (STEPS > 4 && ahead == 3) __builtin_amdgcn_s_waitcnt(vmcnt_imm(3 * PER));
-    else if (STEPS > 3 && ahead == 2) __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * PER));
-    else if (STEPS > 2 && ahead == 1) __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER));
+    static_assert(STEPS == 2 || STEPS == 4, "steps ahead");
+    if (STEPS == 4 && ahead == 2) __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * PER));
+    else if (STEPS == 4 && ahead == 1) __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER));
     else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     __syncthreads();
   };
@@ -278,7 +276,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(MatArgs a) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
   i32x4 fw[2][NB], fx[2][MB];
-  const int lr = lane & 31, lh = lane >> 5, sw = swizzle<KB>(lr);
+  const int lr = lane & 31, lh = lane >> 5, sw = swizzle(lr);
   const int w_at = (wn * NB * 32 + lr) * KB, x_at = (BN + wm * MB * 32 + lr) * KB;
   auto operands = [&](int at, int q) {
     const uint8_t* p = buf + at + 16 * ((2 * q + lh) ^ sw);
@@ -524,7 +522,7 @@ gdr_status launch_int8_matmul(const gdr_int8_matmul_problem* p, const void* x, c
       constexpr int WN = wn.value, WM = wm.value, NB = nb.value, MB = mb.value;
       a.tiles_n = (p->N + 32 * NB * WN - 1) / (32 * NB * WN);
       a.tiles_m = (p->M + 32 * MB * WM - 1) / (32 * MB * WM);
-      GDR_LAUNCH("int8_tile", (int8_tile_kernel<WN, WM, NB, MB, 128, steps.value, O>),
+      GDR_LAUNCH("int8_tile", (int8_tile_kernel<WN, WM, NB, MB, steps.value, O>),
                  dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(64 * WN * WM), st, a);
     };
     const std::integral_constant<int, 1> c1;
