@@ -164,3 +164,30 @@ def test_slopes_at_plus_infinity(dtype):
     y, h, rx, rh = gdr.sandwich_rms_norm_fwd(x, x, w, one, z.cuda(), None, "sigmoid", EPS)
     dgate = gdr.sandwich_rms_norm_bwd(dy, None, x, h, w, one, rx, rh, z.cuda(), None, "sigmoid")[4]
     assert y.isfinite().all() and dgate.isfinite().all() and (dgate.cpu()[open_] == 0).all()
+
+
+def test_gates_that_are_no_numbers():
+    """A NaN in the gate reaches its own output after the norm, its group's
+    before it, and the gradients of its group (of its row, in the sandwich norm)."""
+    t = values(4, 96, F32)
+    z = gates(4, 96, 1, 3, F32)
+    z[1, 40] = float("nan")
+    x, w, dy, zc = t["x"].cuda(), t["w"].cuda(), t["dy"].cuda(), z.cuda()
+    own, row = (torch.zeros(4, 96, dtype=torch.bool) for _ in range(2))
+    own[1, 40], row[1] = True, True
+    for size in (96, 32, 24):
+        group = torch.zeros(4, 96, dtype=torch.bool)
+        group[1, 40 // size * size:(40 // size + 1) * size] = True
+        v = w[:size].contiguous()
+        for name in ("silu", "sigmoid"):
+            for first in (True, False):
+                y, rstd = gdr.gated_rms_norm_fwd(x, zc, v, EPS, size, first, name)
+                assert torch.equal(y.isnan().cpu(), own if first else group)
+                dx, dz, _ = gdr.gated_rms_norm_bwd(dy, x, zc, v, rstd, size, first, name)
+                assert torch.equal(dx.isnan().cpu(), group)
+                assert torch.equal(dz.isnan().cpu(), own if first else group)
+    for name in ("silu", "sigmoid", None):
+        y, h, rx, rh = gdr.sandwich_rms_norm_fwd(x, x, w, w, zc, None, name, EPS)
+        assert torch.equal(h.isnan().cpu(), own) and torch.equal(y.isnan().cpu(), row)
+        got = gdr.sandwich_rms_norm_bwd(dy, None, x, h, w, w, rx, rh, zc, None, name)
+        assert all(torch.equal(g.isnan().cpu(), row) for g in (got[0], got[1], got[4]))
