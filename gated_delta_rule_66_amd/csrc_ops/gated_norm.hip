@@ -20,7 +20,7 @@ namespace gdr {
 namespace {
 
 // Narrower groups (of a width that lanes do not take) are summed as segments.
-constexpr int kUnitColumns = 192;
+constexpr int kUnitColumns = 224;
 // Columns of a row that a block's threads hold in the gradient of lanes, a
 // multiple of every group's.
 constexpr int kLanePiece = 8192;
@@ -140,10 +140,11 @@ __device__ __forceinline__ void by_order(int gate_first, F f) {
 
 // The forward.  Memory bounds it: 8192 rows of 4096 bf16 columns in heads of 128
 // take 43 us for 201 MB (4.7 TB/s), 4099 of 5005 fp16 columns in groups of 715
-// 33 us for 123 MB (3.7: a wave's second step is two fifths full).  To 8 bits
-// 18,062 x 4096 take 93 us for 370 MB (4.0): exact gates (8 us) and quotients, the
-// kernel's text holds 1147 vector instructions for a thread's 16 elements with
-// both 8-bit types' branches, 696 without them.  Eight rows take 6 us.
+// 36 us for 123 MB (3.4: a wave's second step is two fifths full).  To 8 bits
+// 18,062 x 4096 take 98 us for 370 MB (3.8): exact gates (8 us) and quotients, the
+// kernel's text holds 1371 vector instructions for a thread's 16 elements with
+// both 8-bit types' and both activations' branches, 931 without the 8-bit types.
+// Eight rows take 5 us.
 template <typename T, bool QUANT, Sums SUMS, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) {
   __shared__ __align__(8) float lds[32];
@@ -254,9 +255,11 @@ __global__ __launch_bounds__(block_of<NT>()) void gated_fwd_kernel(GatedArgs a) 
 // its sum in `part`, which launch_reduce_rows adds in order.  Where lanes hold
 // groups that share their weights the block adds up its groups first.
 // 8192 x 4096 in heads of 128 take 62 us for 336 MB (5.4 TB/s), 4099 x 5005 in
-// groups of 715 65 us for 205 MB (3.2: waves of two steps hold 221 registers, two
-// of them a SIMD).  One group of 16,384 columns spills some 150 registers (34 MB
-// of columns: 269 us, of 8192: 77).
+// groups of 715 58 us for 205 MB (3.5: waves of two steps hold 204 registers, two
+// of them a SIMD).  Beyond 8192 columns two steps of 1024 threads spill: one group
+// of 16,384 some 160 registers (33.5 million elements 218 us, of 8192 69), segments
+// some 480 (16,380 columns in groups of 12 302 us, 12,288 in 96 404; 4995 in 45,
+// which spill none, 125).
 template <typename T, Sums SUMS, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>(), NT == 64 && VPT == 2 ? 2 : 4) void gated_bwd_kernel(GatedArgs a) {
   constexpr int RPB = NT == 64 ? 4 : 1;
@@ -434,10 +437,10 @@ void by_type(const gdr_gated_norm_problem* p, F f) {
 
 // How the sums of a problem's groups are formed.  Units hold a wave or a block a
 // group, wherever no scale spans several groups and a wave's lanes are busy
-// enough: (33 MB of
-// columns, forward and gradient, as units and as segments: 4992 in groups of
-// 208 83 + 107 and 78 + 137 us, 5005 in 143 117 + 147 and 82 + 142, 4992 in 96
-// 159 + 204 and 73 + 125).
+// enough: (33.5 million bf16 elements, forward and gradient, as units and as
+// segments: groups of 336 66 + 83 and 86 + 120 us, of 240 87 + 110 and 86 + 115, of
+// 208 97 + 123 and 85 + 118, of 143 136 + 170 and 93 + 130, of 96 188 + 239 and 85 +
+// 116).
 Sums sums_of(const gdr_gated_norm_problem* p) {
   const int n = p->norm_size;
   if (n % 8 == 0 && n <= 512 && (n & (n - 1)) == 0) return kLanes;
@@ -472,8 +475,9 @@ void by_form(const gdr_gated_norm_problem* p, F f) {
   });
 }
 // The gradient holds six arrays of a row: one step a thread as far as a block
-// reaches (4096 columns by 256 threads of two steps took 193 registers and 75
-// us, by 512 threads of one 111 and 61), two for a wave's units.
+// reaches (as it was first built, 4096 columns by 256 threads of two steps took 193
+// registers and 75 us, by 512 threads of one 111 and 61; now 103 and 62), two for a
+// wave's units.
 template <typename F>
 void by_form_bwd(const gdr_gated_norm_problem* p, F f) {
   const Sums sums = sums_of(p);

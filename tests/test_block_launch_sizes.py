@@ -32,10 +32,10 @@ def quantize(rows, D):
     (lambda n: gated(n, 1024, 8), lib.gdr_gated_norm_check, 1),
     (lambda n: gated(n, 1040, 16), lib.gdr_gated_norm_check, 2),
     # units: a wave or more a group
-    (lambda n: gated(n, 2000, 200), lib.gdr_gated_norm_check, 10),
+    (lambda n: gated(n, 2000, 250), lib.gdr_gated_norm_check, 8),
     (lambda n: gated(n, 8160, 2040), lib.gdr_gated_norm_check, 8),
     # segments: a block of 512 columns a wave, beyond 8192 of 1024
-    (lambda n: gated(n, 2000, 200, 2), lib.gdr_gated_norm_check, 4),
+    (lambda n: gated(n, 2000, 250, 2), lib.gdr_gated_norm_check, 4),
     (lambda n: gated(n, 4096, 64 + 64, 2), lib.gdr_gated_norm_check, 4),
     (lambda n: gated(n, 16380, 12), lib.gdr_gated_norm_check, 16),
     (lambda n: sandwich(n, 512), lib.gdr_sandwich_norm_check, 1),
