@@ -7,8 +7,8 @@
 //
 // 18,062 tokens by 12,288 channels of K = 4096 take 845 to 890 us (2.1 to 2.15
 // POPS with random values; a library's product with 32-bit sums as its output
-// 810 to 870), 2903 x 5003 of K = 2505 59, 48 of them the product, 64 x 12,288 11,
-// 1 x 12,288 10 (5 TB/s).
+// 810 to 870), 2903 x 5003 of K = 2505 59, 48 of them the product; with the weights
+// in the caches 64 x 12,288 11, 1 x 12,288 10 (5 TB/s), from memory 8 x 12,288 14.
 //
 // The weights are the matrix instruction's first operand and the tokens its
 // second, so that a lane ends with four consecutive channels of one token.
@@ -427,7 +427,8 @@ struct MatPlan {
 // 4096 58, 42 and 52, 4096 x 4096 (80 in 128 x 128) 73.
 // Few tokens: the weights' bytes (4.5 us for 1 x 4096 of K = 4096, 10 for 1 x
 // 12288) and the tokens' from L2 for every 16 channels (5.9 and 14.1 for 16
-// tokens, against 10.2 and 11.1 in 64 x 64 tiles).
+// tokens, against 10.2 and 11.1 in 64 x 64 tiles).  All of these with operands that
+// stay in the caches from call to call.
 MatPlan plan_of(const gdr_int8_matmul_problem* p) {
   const double M = p->M, N = p->N, K = p->K, never = 1e30;
   auto tile_us = [&](double edge, double slots, double full, double half) {

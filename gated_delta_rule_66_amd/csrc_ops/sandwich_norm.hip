@@ -61,9 +61,10 @@ __device__ __forceinline__ float row_rstd(const float (&f)[VPT][8], int tid, int
   return inverse_root(sum / D + (double)eps);
 }
 
-// The forward.  8192 rows of 4096 bf16 columns with a gate take 70 us for 336 MB
-// (4.8 TB/s), 4099 of 5003 fp16 columns with a residual in fp32 56 us for 246 MB
-// (4.4): two sums over the row one after the other.  Eight rows to int8 take 6 us.
+// The forward.  8192 rows of 4096 bf16 columns with a gate take 72 to 75 us for 336
+// MB (4.5 to 4.7 TB/s), 4099 of 5003 fp16 columns with a residual in fp32 56 us for
+// 246 MB (4.4): two sums over the row one after the other.  18,062 rows of 4096 to
+// int8 take 174 us for 666 MB (3.8), eight 6 us.
 template <typename T, typename R, bool QUANT, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichArgs a) {
   __shared__ __align__(8) float lds[32];
@@ -141,10 +142,10 @@ __global__ __launch_bounds__(block_of<NT>()) void sandwich_fwd_kernel(SandwichAr
 //   dg = dH alpha s w1 ux A',   du = dH alpha s A w1
 //   dx = rx (du - ux mean(du ux))     (du without w1)
 // A block walks rows blockIdx.x, + blocks, ... with dw2 and P in registers and
-// leaves its sums in `part`.  8192 x 4096 with a gate take 117 us for 537 MB (4.6
-// TB/s): eight streams, two sums, 102 registers and so two rows of 512 threads a
-// CU.  Beyond 8192 columns dw2 and P lie in LDS and 48 registers are spilled (34
-// MB of columns: 220 us of 16,384, 135 of 8192).
+// leaves its sums in `part`.  8192 x 4096 with a gate take 115 us for 537 MB (4.7
+// TB/s): eight streams, two sums, 104 registers and so two rows of 512 threads a
+// CU.  Beyond 8192 columns dw2 and P lie in LDS and some 32 registers are spilled
+// (33.5 million elements: 170 us of 16,384 columns, 129 of 8192).
 template <typename T, typename R, int NT, int VPT, bool PART>
 __global__ __launch_bounds__(block_of<NT>(), 4) void sandwich_bwd_kernel(SandwichArgs a) {
   constexpr int RPB = NT == 64 ? 4 : 1;
@@ -348,8 +349,8 @@ void by_type(const gdr_sandwich_norm_problem* p, F f) {
 }
 
 // Rows of several arrays: one 8-element step a thread as far as a block reaches
-// (the forward of 8192 x 4096 bf16 with a gate: 70 us, with two steps 77; the
-// gradient 117 and, with 193 registers, 139).
+// (as they were first built, the forward of 8192 x 4096 bf16 with a gate: 70 us, with
+// two steps 77; the gradient 117 and, with 193 registers, 139).
 template <typename F>
 void by_steps(int D, F f) {
   if (D <= 8192) return by_row<1>(D, f);
